@@ -456,6 +456,133 @@ mx_status mx_gemm_grouped(const mx_tensor* A, const int32_t* row_index, int64_t 
 #define MX_NOALLOC_MAX_JOBS 256
 mx_status mx_quantize_batch_noalloc(const mx_quantize_job* jobs, int32_t count, mx_stream stream);
 
+/* ---- around the expert products ------------------------------------------
+ * The steps of a mixture-of-experts layer before, between and behind its
+ * grouped products ([INK] "A precision choice for each stage": NVFP4 forward
+ * in the expert layers, saved tensors kept quantized for the backward pass).
+ * All of them are deterministic: equal inputs give equal bits. */
+
+/* One routing of `tokens` tokens to `experts` experts, topk each (host struct;
+ * the pointers are device pointers, dense arrays).  R = tokens * topk slots. */
+typedef struct {
+  int64_t tokens;
+  int32_t experts;
+  int32_t topk;
+  int32_t* expert;        /* [tokens, topk] chosen experts, -1: no choice */
+  float* weight;          /* [tokens, topk] their weights, 0 where expert is -1 */
+  int32_t* slot_row;      /* [tokens, topk] routed row of the slot, -1: none */
+  int32_t* row_index;     /* [R] token of each routed row; -1 past the last one */
+  int64_t* group_offsets; /* [experts + 1] rows of expert e: [off[e], off[e + 1]) */
+  int64_t* counts;        /* [experts] tokens that chose e */
+  int64_t* valid;         /* [1] tokens that are not padding */
+  float* prob_sum;        /* [experts] sum over the tokens of p[t, e] */
+  float* loss;            /* [1] balance loss */
+} mx_routing;
+
+#define MX_ROUTE_NORMALIZE 1u /* weights divided by the sum of the token's weights */
+#define MX_ROUTE_MAX_EXPERTS 1024
+#define MX_ROUTE_MAX_TOPK 16
+#define MX_ROUTE_MAX_TOKENS (1 << 23)
+
+/* Router of a mixture-of-experts layer.  logits [tokens, experts] (BF16 or
+ * FP32, row pitch ld elements; element alignment is enough, 16-byte aligned
+ * rows load faster).  Per token p = softmax(logits) in FP32; the topk largest
+ * logits are chosen in descending order, equal ones by lower index, and their
+ * weights are p, divided by the token's sum of chosen p with
+ * MX_ROUTE_NORMALIZE.  A logit of -inf (or NaN) is never chosen and -inf has
+ * p = 0; with fewer than topk others the remaining slots are empty (expert
+ * -1, weight 0, slot_row -1).  A row that holds NaN or +inf gets NaN weights
+ * and makes prob_sum and loss NaN; its choices stay valid indices.
+ * token_mask (device uint8 [tokens], NULL: all ones): a token with 0 is
+ * padding; its logits are not looked at, its slots are empty and it counts in
+ * nothing.
+ * Routed rows are sorted by expert, within one by token: group_offsets and
+ * row_index are what mx_gemm_grouped and mx_wgrad_grouped take, slot_row what
+ * mx_combine takes.  Balance loss: with V = *valid,
+ *   loss = experts / (topk V^2) * sum_e counts[e] * prob_sum[e]   (V = 0: 0),
+ * 1 for perfectly even routing.  Sums over tokens are FP32 in a fixed order.
+ * workspace: mx_route_workspace_bytes(tokens, experts) bytes of device memory,
+ * 16-byte aligned, written before it is read (NULL when that is 0).
+ * Requirements: 1 <= experts <= MX_ROUTE_MAX_EXPERTS, 1 <= topk <=
+ * min(experts, MX_ROUTE_MAX_TOPK), 0 <= tokens <= MX_ROUTE_MAX_TOKENS. */
+size_t mx_route_workspace_bytes(int64_t tokens, int32_t experts);
+mx_status mx_route(const void* logits, int32_t ldt, int64_t ld, const uint8_t* token_mask, uint32_t flags,
+                   const mx_routing* out, void* workspace, size_t workspace_bytes, mx_stream stream);
+
+/* Gradient of the logits: of the weights (d_weight [tokens, topk] FP32, NULL:
+ * zero) and of the balance loss (d_loss, one FP32 on the device, NULL: zero;
+ * the counts are constants of the loss).  Reads logits, token_mask, flags as
+ * the forward call got them, and expert, counts and valid of `routing` (the
+ * other pointers may be NULL).  counts and valid may be sums over several
+ * devices: the gradient is then that of the loss over all their tokens.
+ * d_logits [tokens, experts] has the logits' dtype and row pitch ld_d (element
+ * alignment); padding tokens get zeros. */
+mx_status mx_route_backward(const void* logits, int32_t ldt, int64_t ld, const uint8_t* token_mask, uint32_t flags,
+                            const mx_routing* routing, const float* d_weight, const float* d_loss, void* d_logits,
+                            int64_t ld_d, mx_stream stream);
+
+/* Gated activation with an 8-bit checkpoint.  h [rows, 2 cols] (dtype dt, row
+ * pitch ld_h) holds the gate in columns 0 .. cols-1 and the up projection in
+ * cols .. 2 cols-1; y [rows, cols] (same dtype) = gate * sigmoid(gate) * up in
+ * FP32, rounded once.  `saved` (NULL: nothing is saved) receives h quantized
+ * to 8 bits, [rows, 2 cols] in the row layout (MX_MXFP8_E4M3, MX_MXFP8_E5M2 or
+ * MX_MXINT8), with the codes and scales that mx_quantize(h, saved, rnd, rng)
+ * gives.  `amax` (NULL: not wanted; device FP32) receives max |y| of the
+ * stored values, for mx_quantize with MX_FLAG_AMAX_GIVEN.
+ * Requirements: cols % 32 == 0. */
+mx_status mx_swiglu(const void* h, int32_t dt, int64_t rows, int64_t cols, int64_t ld_h, void* y, int64_t ld_y,
+                    const mx_tensor* saved, int32_t rnd, mx_rng rng, float* amax, mx_stream stream);
+
+/* Backward pass of mx_swiglu from its checkpoint: with gate, up the decoded
+ * values of `saved` [rows, 2 cols] and s = sigmoid(gate),
+ *   dh[:, :cols] = dy * up * s * (1 + gate * (1 - s)),
+ *   dh[:, cols:] = dy * gate * s
+ * (FP32, rounded once; dy [rows, cols] and dh [rows, 2 cols] of dtype dt).
+ * `y_saved` (NULL: not wanted): gate * s * up of the decoded values, quantized
+ * to an 8-bit MX format [rows, cols] in the row layout (round to nearest), the
+ * operand of the next mx_wgrad_grouped, which then need not be kept from the
+ * forward pass. */
+mx_status mx_swiglu_backward(const mx_tensor* saved, const void* dy, int32_t dt, int64_t rows, int64_t cols,
+                             int64_t ld_dy, void* dh, int64_t ld_dh, const mx_tensor* y_saved, mx_stream stream);
+
+/* Grouped weight gradient from an 8-bit checkpoint: for every group e and its
+ * rows r in [off[e], off[e + 1]),
+ *   dW[e * N + n, k] = sum_r dY[r, n] * X[src(r), k]
+ * (added to what dW holds with MX_WGRAD_ACCUMULATE; a group without rows gives
+ * 0, or adds nothing).  dY: BF16 [routed_rows, N], row pitch ld_dy, 16-byte
+ * aligned rows.  X: an 8-bit MX tensor (E4M3, E5M2, INT8; row layout) of K
+ * columns, its elements decoded to BF16 (exact for scale codes 10 .. 254) and
+ * the exact products summed in FP32.  src(r) = row_index[r], clamped into X's
+ * rows, or r where row_index is NULL (X then has routed_rows rows).
+ * group_offsets: as in mx_gemm_grouped (device int64 [num_groups + 1],
+ * clamped into [0, routed_rows]); NULL with num_groups == 1 takes all rows.
+ * dW [num_groups * N, K]: FP32 or BF16 (dwdt), row pitch ld_dw, element
+ * alignment. */
+#define MX_WGRAD_ACCUMULATE 1u
+mx_status mx_wgrad_grouped(const void* dY, int64_t ld_dy, int64_t routed_rows, int64_t N, const mx_tensor* X,
+                           const int32_t* row_index, int32_t num_groups, const int64_t* group_offsets, void* dW,
+                           int32_t dwdt, int64_t ld_dw, uint32_t flags, mx_stream stream);
+
+/* Combination of routed rows: out[t, :] = sum_j weight[t, j] * Y[slot_row[t,
+ * j], :] in FP32, slots in order, rounded once.  Y [rows, cols] (ydt, row pitch
+ * ld_y, 16-byte aligned rows); slot_row, weight: dense [tokens, topk]; weight
+ * NULL takes 1 for every slot.  A slot whose row lies outside [0, rows) adds
+ * nothing.  out [tokens, cols] (odt, pitch ld_out, element alignment; it may
+ * not overlap Y). */
+mx_status mx_combine(const void* Y, int32_t ydt, int64_t rows, int64_t cols, int64_t ld_y, const int32_t* slot_row,
+                     const float* weight, int64_t tokens, int32_t topk, void* out, int32_t odt, int64_t ld_out,
+                     mx_stream stream);
+
+/* Its gradients, for d_out [tokens, cols]: dY[slot_row[t, j], :] = weight[t,
+ * j] * d_out[t, :] (rows that no slot names are not written) and d_weight[t,
+ * j] = <d_out[t, :], Y[slot_row[t, j], :]> (0 for a slot without a row).
+ * Either of dY and d_weight may be NULL; Y may be NULL when d_weight is.  d_out,
+ * Y and dY have dtype dt and 16-byte aligned rows. */
+mx_status mx_combine_backward(const void* d_out, int32_t dt, int64_t ld_do, const void* Y, int64_t ld_y,
+                              int64_t rows, int64_t cols, const int32_t* slot_row, const float* weight,
+                              int64_t tokens, int32_t topk, void* dY, int64_t ld_dy, float* d_weight,
+                              mx_stream stream);
+
 /* Human-readable name of a status code (static string). */
 const char* mx_status_string(int32_t status);
 

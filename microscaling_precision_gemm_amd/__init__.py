@@ -24,6 +24,9 @@ MX_FLAG_SCALE_CEIL, MX_FLAG_FOUR_OVER_SIX, MX_FLAG_BLOCK_2D = 4, 8, 16
 MX_GEMM_FP8_NATIVE = 1
 MX_LAYOUT_ROWS, MX_LAYOUT_TILED = 0, 1
 MX_NOALLOC_MAX_JOBS = 256
+MX_ROUTE_NORMALIZE = 1
+MX_ROUTE_MAX_EXPERTS, MX_ROUTE_MAX_TOPK, MX_ROUTE_MAX_TOKENS = 1024, 16, 1 << 23
+MX_WGRAD_ACCUMULATE = 1
 
 FORMATS = {"mxfp8": MX_MXFP8_E4M3, "mxfp4": MX_MXFP4_E2M1, "nvfp4": MX_NVFP4, "mxint8": MX_MXINT8,
            "s2f6": MX_MXINT8, "mxfp8_e5m2": MX_MXFP8_E5M2, "mxfp6_e3m2": MX_MXFP6_E3M2,
@@ -34,7 +37,8 @@ EXPORTED = [
     "mx_codes_bytes", "mx_scales_bytes", "mx_rht_signs", "mx_quantize", "mx_amax",
     "mx_dequantize", "mx_requant_transpose", "mx_hadamard16", "mx_gemm", "mx_gemm_ex",
     "mx_gemm_grouped", "mx_gemm_quantize", "mx_gemm_quantize_a", "mx_quantize_batch", "mx_error_stats",
-    "mx_quantize_batch_noalloc", "mx_status_string",
+    "mx_quantize_batch_noalloc", "mx_route_workspace_bytes", "mx_route", "mx_route_backward", "mx_swiglu",
+    "mx_swiglu_backward", "mx_wgrad_grouped", "mx_combine", "mx_combine_backward", "mx_status_string",
 ]
 
 
@@ -59,6 +63,13 @@ class _Job(ctypes.Structure):
                 ("rht_sign_mask", ctypes.c_uint16), ("amax", ctypes.c_void_p)]
 
 
+class _Routing(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("experts", ctypes.c_int32), ("topk", ctypes.c_int32),
+                ("expert", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("slot_row", ctypes.c_void_p),
+                ("row_index", ctypes.c_void_p), ("group_offsets", ctypes.c_void_p), ("counts", ctypes.c_void_p),
+                ("valid", ctypes.c_void_p), ("prob_sum", ctypes.c_void_p), ("loss", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -80,7 +91,7 @@ def load():
     L = ctypes.CDLL(LIB_PATH)
     vp, i32, i64, u32, u64, u16 = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
                                    ctypes.c_uint32, ctypes.c_uint64, ctypes.c_uint16)
-    TP = ctypes.POINTER(_Tensor)
+    TP, RP = ctypes.POINTER(_Tensor), ctypes.POINTER(_Routing)
     sig = {
         "mx_codes_bytes": (ctypes.c_size_t, [i32, i64, i64]),
         "mx_scales_bytes": (ctypes.c_size_t, [i32, i64, i64]),
@@ -98,6 +109,14 @@ def load():
         "mx_gemm_quantize_a": (i32, [vp, i64, i64, i32, i32, _Rng, TP, vp, i32, i64, TP, vp]),
         "mx_quantize_batch": (i32, [ctypes.POINTER(_Job), i32, vp]),
         "mx_quantize_batch_noalloc": (i32, [ctypes.POINTER(_Job), i32, vp]),
+        "mx_route_workspace_bytes": (ctypes.c_size_t, [i64, i32]),
+        "mx_route": (i32, [vp, i32, i64, vp, u32, RP, vp, ctypes.c_size_t, vp]),
+        "mx_route_backward": (i32, [vp, i32, i64, vp, u32, RP, vp, vp, vp, i64, vp]),
+        "mx_swiglu": (i32, [vp, i32, i64, i64, i64, vp, i64, TP, i32, _Rng, vp, vp]),
+        "mx_swiglu_backward": (i32, [TP, vp, i32, i64, i64, i64, vp, i64, TP, vp]),
+        "mx_wgrad_grouped": (i32, [vp, i64, i64, i64, TP, vp, i32, vp, vp, i32, i64, u32, vp]),
+        "mx_combine": (i32, [vp, i32, i64, i64, i64, vp, vp, i64, i32, vp, i32, i64, vp]),
+        "mx_combine_backward": (i32, [vp, i32, i64, vp, i64, i64, i64, vp, vp, i64, i32, vp, i64, vp, vp]),
         "mx_status_string": (ctypes.c_char_p, [i32]),
     }
     for name, (res, args) in sig.items():
@@ -344,3 +363,175 @@ def mx_gemm_grouped(A: MXTensor, row_index, routed_rows: int, B: MXTensor, num_g
                              num_groups, _ptr(group_offsets), _ptr(C), _dt(C), C.stride(0),
                              _stream(stream)))
     return C
+
+
+# ---- around the expert products --------------------------------------------
+def _need(cond, what: str):
+    if not cond:
+        raise MXError(what)
+
+
+def _rows_of(t, rows, cols, what: str) -> int:
+    """Row pitch of a [rows, cols] matrix whose columns are adjacent."""
+    _need(t.dim() == 2 and t.shape[0] == rows and t.shape[1] == cols, f"{what}: expected [{rows}, {cols}], got "
+          f"{list(t.shape)}")
+    _need(cols <= 1 or t.stride(1) == 1, f"{what}: columns must be adjacent")
+    # the pitch of a single row is no matter: one that keeps rows aligned
+    return t.stride(0) if rows > 1 else (cols + 7) // 8 * 8
+
+
+def _dense(t, dtype, shape, what: str):
+    if t is not None:
+        _need(t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous(),
+              f"{what}: expected a dense {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    return t
+
+
+class Routing:
+    """The device buffers of one routing (the fields of mx_routing in mx.h)
+    and the workspace mx_route needs: experts, weights, slot_row [tokens,
+    topk]; row_index [tokens * topk]; group_offsets [experts + 1]; counts,
+    prob_sum [experts]; valid, loss [1]."""
+
+    def __init__(self, tokens: int, experts: int, topk: int, device="cuda"):
+        torch = _torch()
+        _need(tokens >= 0 and experts >= 1 and topk >= 1, "routing: sizes")
+        self.tokens, self.num_experts, self.topk = int(tokens), int(experts), int(topk)
+        new = lambda dtype, *shape: torch.empty(shape, dtype=dtype, device=device)
+        self.experts = new(torch.int32, tokens, topk)
+        self.weights = new(torch.float32, tokens, topk)
+        self.slot_row = new(torch.int32, tokens, topk)
+        self.row_index = new(torch.int32, tokens * topk)
+        self.group_offsets = new(torch.int64, experts + 1)
+        self.counts = new(torch.int64, experts)
+        self.valid = new(torch.int64, 1)
+        self.prob_sum = new(torch.float32, experts)
+        self.loss = new(torch.float32, 1)
+        self.workspace = new(torch.uint8, int(load().mx_route_workspace_bytes(tokens, experts)))
+
+    def desc(self) -> _Routing:
+        return _Routing(self.tokens, self.num_experts, self.topk, _ptr(self.experts), _ptr(self.weights),
+                        _ptr(self.slot_row), _ptr(self.row_index), _ptr(self.group_offsets), _ptr(self.counts),
+                        _ptr(self.valid), _ptr(self.prob_sum), _ptr(self.loss))
+
+
+def routing(tokens: int, experts: int, topk: int, device="cuda") -> Routing:
+    """Allocate the buffers of a routing of `tokens` tokens."""
+    return Routing(tokens, experts, topk, device)
+
+
+def mx_route_workspace_bytes(tokens: int, experts: int) -> int:
+    return int(load().mx_route_workspace_bytes(tokens, experts))
+
+
+def mx_route(logits, out: Routing, token_mask=None, flags: int = 0, stream=None) -> Routing:
+    """Route each row of logits [tokens, experts] (bf16 or fp32) to its topk
+    largest experts; token_mask: uint8 [tokens], 0 for padding."""
+    ld = _rows_of(logits, out.tokens, out.num_experts, "logits")
+    _dense(token_mask, _torch().uint8, (out.tokens,), "token_mask")
+    d = out.desc()
+    _check(load().mx_route(_ptr(logits), _dt(logits), ld, _ptr(token_mask), flags, ctypes.byref(d),
+                           _ptr(out.workspace), out.workspace.numel(), _stream(stream)))
+    return out
+
+
+def mx_route_backward(logits, r: Routing, d_weights, d_loss, d_logits, token_mask=None, flags: int = 0,
+                      stream=None):
+    """Gradient of the logits from d_weights (fp32 [tokens, topk] or None) and
+    d_loss (fp32 [1] on the device or None), for the routing r."""
+    torch = _torch()
+    ld = _rows_of(logits, r.tokens, r.num_experts, "logits")
+    ld_d = _rows_of(d_logits, r.tokens, r.num_experts, "d_logits")
+    _need(d_logits.dtype == logits.dtype, "d_logits: dtype of logits expected")
+    _dense(token_mask, torch.uint8, (r.tokens,), "token_mask")
+    _dense(d_weights, torch.float32, (r.tokens, r.topk), "d_weights")
+    _need(d_loss is None or (d_loss.dtype == torch.float32 and d_loss.numel() == 1), "d_loss: one fp32 expected")
+    d = r.desc()
+    _check(load().mx_route_backward(_ptr(logits), _dt(logits), ld, _ptr(token_mask), flags, ctypes.byref(d),
+                                    _ptr(d_weights), _ptr(d_loss), _ptr(d_logits), ld_d, _stream(stream)))
+    return d_logits
+
+
+def mx_swiglu(h, y, saved: "MXTensor | None" = None, rnd: int = MX_RNE, seed: int = 0, counter: int = 0,
+              amax=None, stream=None):
+    """y [rows, cols] = gate * sigmoid(gate) * up for h = [gate | up]; `saved`
+    receives h in 8 bits, `amax` (fp32 [1]) the largest |y|."""
+    _need(y.dim() == 2, "y: a matrix expected")
+    rows, cols = y.shape
+    ld_h, ld_y = _rows_of(h, rows, 2 * cols, "h"), _rows_of(y, rows, cols, "y")
+    _need(y.dtype == h.dtype, "y: dtype of h expected")
+    _need(amax is None or (amax.dtype == _torch().float32 and amax.numel() == 1), "amax: one fp32 expected")
+    d = saved.desc() if saved is not None else None
+    _check(load().mx_swiglu(_ptr(h), _dt(h), rows, cols, ld_h, _ptr(y), ld_y,
+                            ctypes.byref(d) if d is not None else None, rnd, _Rng(seed, counter), _ptr(amax),
+                            _stream(stream)))
+    return y
+
+
+def mx_swiglu_backward(saved: MXTensor, dy, dh, y_saved: "MXTensor | None" = None, stream=None):
+    """dh [rows, 2 cols] from the 8-bit checkpoint of mx_swiglu and dy [rows,
+    cols]; `y_saved` receives the decoded activation in 8 bits."""
+    _need(dy.dim() == 2, "dy: a matrix expected")
+    rows, cols = dy.shape
+    ld_dy, ld_dh = _rows_of(dy, rows, cols, "dy"), _rows_of(dh, rows, 2 * cols, "dh")
+    _need(dh.dtype == dy.dtype, "dh: dtype of dy expected")
+    d = saved.desc()
+    dys = y_saved.desc() if y_saved is not None else None
+    _check(load().mx_swiglu_backward(ctypes.byref(d), _ptr(dy), _dt(dy), rows, cols, ld_dy, _ptr(dh), ld_dh,
+                                     ctypes.byref(dys) if dys is not None else None, _stream(stream)))
+    return dh
+
+
+def mx_wgrad_grouped(dY, X: MXTensor, row_index, num_groups: int, group_offsets, dW, flags: int = 0, stream=None):
+    """dW [num_groups * N, K] (fp32 or bf16) = per group, dY^T [N, rows] times
+    the 8-bit rows of X (through row_index, if given)."""
+    torch = _torch()
+    _need(dY.dim() == 2 and dY.dtype == torch.bfloat16, "dY: a bf16 matrix expected")
+    rows, N = dY.shape
+    ld_dy = _rows_of(dY, rows, N, "dY")
+    ld_dw = _rows_of(dW, num_groups * N, X.cols, "dW")
+    _dense(row_index, torch.int32, (rows,), "row_index")
+    _dense(group_offsets, torch.int64, (num_groups + 1,), "group_offsets")
+    d = X.desc()
+    _check(load().mx_wgrad_grouped(_ptr(dY), ld_dy, rows, N, ctypes.byref(d), _ptr(row_index), num_groups,
+                                   _ptr(group_offsets), _ptr(dW), _dt(dW), ld_dw, flags, _stream(stream)))
+    return dW
+
+
+def mx_combine(Y, slot_row, weights, out, stream=None):
+    """out [tokens, cols] = sum over the slots of weights * Y[slot_row]
+    (weights None: 1)."""
+    torch = _torch()
+    _need(Y.dim() == 2 and slot_row.dim() == 2, "Y, slot_row: matrices expected")
+    tokens, topk = slot_row.shape
+    rows, cols = Y.shape
+    ld_y, ld_out = _rows_of(Y, rows, cols, "Y"), _rows_of(out, tokens, cols, "out")
+    _dense(slot_row, torch.int32, (tokens, topk), "slot_row")
+    _dense(weights, torch.float32, (tokens, topk), "weights")
+    _check(load().mx_combine(_ptr(Y), _dt(Y), rows, cols, ld_y, _ptr(slot_row), _ptr(weights), tokens, topk,
+                             _ptr(out), _dt(out), ld_out, _stream(stream)))
+    return out
+
+
+def mx_combine_backward(d_out, Y, slot_row, weights, dY, d_weights, stream=None):
+    """Gradients of mx_combine: dY [rows, cols] (None: not wanted) and
+    d_weights [tokens, topk] (None: not wanted; Y may then be None)."""
+    torch = _torch()
+    _need(d_out.dim() == 2 and slot_row.dim() == 2, "d_out, slot_row: matrices expected")
+    tokens, topk = slot_row.shape
+    cols = d_out.shape[1]
+    ld_do = _rows_of(d_out, tokens, cols, "d_out")
+    _dense(slot_row, torch.int32, (tokens, topk), "slot_row")
+    _dense(weights, torch.float32, (tokens, topk), "weights")
+    _dense(d_weights, torch.float32, (tokens, topk), "d_weights")
+    _need(d_weights is None or Y is not None, "d_weights needs Y")
+    some = Y if Y is not None else dY
+    rows = some.shape[0] if some is not None else 0
+    ld_y = _rows_of(Y, rows, cols, "Y") if Y is not None else 0
+    ld_dy = _rows_of(dY, rows, cols, "dY") if dY is not None else 0
+    for t in (Y, dY):
+        _need(t is None or t.dtype == d_out.dtype, "Y, dY: dtype of d_out expected")
+    _check(load().mx_combine_backward(_ptr(d_out), _dt(d_out), ld_do, _ptr(Y), ld_y, rows, cols, _ptr(slot_row),
+                                      _ptr(weights), tokens, topk, _ptr(dY), ld_dy, _ptr(d_weights),
+                                      _stream(stream)))
+    return dY, d_weights

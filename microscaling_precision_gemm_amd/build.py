@@ -27,6 +27,10 @@ SOURCES = [
     os.path.join(CSRC, "kernels", "gemm_f6.hip"),
     os.path.join(CSRC, "kernels", "stats.hip"),
     os.path.join(CSRC, "kernels", "gemm_qa.hip"),
+    os.path.join(CSRC, "kernels", "route.hip"),
+    os.path.join(CSRC, "kernels", "swiglu.hip"),
+    os.path.join(CSRC, "kernels", "wgrad.hip"),
+    os.path.join(CSRC, "kernels", "combine.hip"),
 ]
 
 # -ffp-contract=off: the quantizers' FP32 scale arithmetic must round once per

@@ -546,4 +546,182 @@ mx_status mx_gemm_grouped(const mx_tensor* A, const int32_t* row_index, int64_t 
       group_offsets, N, K, C, cdt, ldc, reinterpret_cast<hipStream_t>(stream)));
 }
 
+// ---- around the expert products --------------------------------------------
+namespace {
+bool elem_aligned(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+bool saved_fmt(int32_t f) { return f == MX_MXFP8_E4M3 || f == MX_MXFP8_E5M2 || f == MX_MXINT8; }
+
+// The sizes of a routing and the arguments both passes share.
+mx_status make_route_args(const void* logits, int32_t ldt, int64_t ld, const uint8_t* token_mask, uint32_t flags,
+                          const mx_routing* r, mxk::RouteArgs* a) {
+  if (!r) return MX_ERR_NULL;
+  if (!valid_dt(ldt)) return MX_ERR_FORMAT;
+  if (flags & ~MX_ROUTE_NORMALIZE) return MX_ERR_UNSUPPORTED;
+  if (r->tokens < 0 || r->tokens > MX_ROUTE_MAX_TOKENS || r->experts < 1 || r->experts > MX_ROUTE_MAX_EXPERTS ||
+      r->topk < 1 || r->topk > MX_ROUTE_MAX_TOPK || r->topk > r->experts || ld < r->experts)
+    return MX_ERR_SHAPE;
+  if (r->tokens > 0 && (!logits || !r->expert)) return MX_ERR_NULL;
+  if (!r->counts || !r->valid) return MX_ERR_NULL;
+  if (!elem_aligned(logits, dt_bytes(ldt)) || !elem_aligned(r->expert, 4) || !elem_aligned(r->counts, 8) ||
+      !elem_aligned(r->valid, 8))
+    return MX_ERR_ALIGN;
+  *a = {logits, (int)ldt, ld, r->tokens, r->experts, r->topk, token_mask, (flags & MX_ROUTE_NORMALIZE) != 0,
+        r->expert, r->weight, r->slot_row, r->row_index, r->group_offsets, r->counts, r->valid, r->prob_sum,
+        r->loss};
+  return MX_OK;
+}
+
+// An 8-bit MX tensor in the row layout.
+mx_status check_saved(const mx_tensor* t, int64_t rows, int64_t cols) {
+  const mx_status st = check_tensor(t, rows, cols);
+  if (st != MX_OK) return st;
+  return saved_fmt(t->fmt) && t->layout == MX_LAYOUT_ROWS ? MX_OK : MX_ERR_UNSUPPORTED;
+}
+
+mx_status check_slots(const int32_t* slot_row, const float* weight, int64_t tokens, int32_t topk) {
+  if (tokens < 0 || topk < 1) return MX_ERR_SHAPE;
+  if (tokens > 0 && !slot_row) return MX_ERR_NULL;
+  return elem_aligned(slot_row, 4) && elem_aligned(weight, 4) ? MX_OK : MX_ERR_ALIGN;
+}
+}  // namespace
+
+size_t mx_route_workspace_bytes(int64_t tokens, int32_t experts) {
+  if (tokens < 0 || tokens > MX_ROUTE_MAX_TOKENS || experts < 1 || experts > MX_ROUTE_MAX_EXPERTS) return 0;
+  return mxk::route_workspace(tokens, experts);
+}
+
+mx_status mx_route(const void* logits, int32_t ldt, int64_t ld, const uint8_t* token_mask, uint32_t flags,
+                   const mx_routing* out, void* workspace, size_t workspace_bytes, mx_stream stream) {
+  mxk::RouteArgs a;
+  const mx_status st = make_route_args(logits, ldt, ld, token_mask, flags, out, &a);
+  if (st != MX_OK) return st;
+  if (!a.offsets || !a.prob_sum || !a.loss) return MX_ERR_NULL;
+  if (a.tokens > 0 && (!a.weights || !a.slot_row || !a.row_index)) return MX_ERR_NULL;
+  if (!elem_aligned(a.weights, 4) || !elem_aligned(a.slot_row, 4) || !elem_aligned(a.row_index, 4) ||
+      !elem_aligned(a.offsets, 8) || !elem_aligned(a.prob_sum, 4) || !elem_aligned(a.loss, 4))
+    return MX_ERR_ALIGN;
+  const size_t need = mxk::route_workspace(a.tokens, a.experts);
+  if (need > 0) {
+    if (!workspace) return MX_ERR_NULL;
+    if (workspace_bytes < need) return MX_ERR_SHAPE;
+    if (!aligned16(workspace)) return MX_ERR_ALIGN;
+  }
+  return hip_status(mxk::launch_route(a, workspace, reinterpret_cast<hipStream_t>(stream)));
+}
+
+mx_status mx_route_backward(const void* logits, int32_t ldt, int64_t ld, const uint8_t* token_mask, uint32_t flags,
+                            const mx_routing* routing, const float* d_weight, const float* d_loss, void* d_logits,
+                            int64_t ld_d, mx_stream stream) {
+  mxk::RouteArgs a;
+  mx_status st = make_route_args(logits, ldt, ld, token_mask, flags, routing, &a);
+  if (st != MX_OK) return st;
+  st = check_output(d_logits, ldt, a.tokens, a.experts, ld_d);
+  if (st != MX_OK) return st;
+  if (!elem_aligned(d_weight, 4) || !elem_aligned(d_loss, 4)) return MX_ERR_ALIGN;
+  if (a.tokens == 0) return MX_OK;
+  return hip_status(
+      mxk::launch_route_bwd(a, d_weight, d_loss, d_logits, ld_d, reinterpret_cast<hipStream_t>(stream)));
+}
+
+mx_status mx_swiglu(const void* h, int32_t dt, int64_t rows, int64_t cols, int64_t ld_h, void* y, int64_t ld_y,
+                    const mx_tensor* saved, int32_t rnd, mx_rng rng, float* amax, mx_stream stream) {
+  if (rnd != MX_RNE && rnd != MX_SR) return MX_ERR_FORMAT;
+  if (rows < 0 || cols < 0 || cols % 32) return MX_ERR_SHAPE;
+  mx_status st = check_matrix(h, dt, rows, 2 * cols, ld_h);
+  if (st != MX_OK) return st;
+  st = check_matrix(y, dt, rows, cols, ld_y);
+  if (st != MX_OK) return st;
+  if (saved) {
+    st = check_saved(saved, rows, 2 * cols);
+    if (st != MX_OK) return st;
+  }
+  if (!elem_aligned(amax, 4)) return MX_ERR_ALIGN;
+  if (rows * cols == 0 && !amax) return MX_OK;
+  const mxk::SwigluArgs a = {h, (int)dt, rows, cols, ld_h, y, ld_y, saved ? saved->fmt : 0,
+                             saved ? static_cast<uint8_t*>(saved->codes) : nullptr, saved ? saved->scales : nullptr,
+                             rnd == MX_SR, rng.seed, rng.counter, amax};
+  return hip_status(mxk::launch_swiglu(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+mx_status mx_swiglu_backward(const mx_tensor* saved, const void* dy, int32_t dt, int64_t rows, int64_t cols,
+                             int64_t ld_dy, void* dh, int64_t ld_dh, const mx_tensor* y_saved, mx_stream stream) {
+  if (rows < 0 || cols < 0 || cols % 32) return MX_ERR_SHAPE;
+  mx_status st = check_saved(saved, rows, 2 * cols);
+  if (st != MX_OK) return st;
+  st = check_matrix(dy, dt, rows, cols, ld_dy);
+  if (st != MX_OK) return st;
+  st = check_matrix(dh, dt, rows, 2 * cols, ld_dh);
+  if (st != MX_OK) return st;
+  if (y_saved) {
+    st = check_saved(y_saved, rows, cols);
+    if (st != MX_OK) return st;
+  }
+  if (rows * cols == 0) return MX_OK;
+  const mxk::SwigluBwdArgs a = {saved->fmt, static_cast<const uint8_t*>(saved->codes), saved->scales, dy, (int)dt,
+                                rows, cols, ld_dy, dh, ld_dh, y_saved ? y_saved->fmt : 0,
+                                y_saved ? static_cast<uint8_t*>(y_saved->codes) : nullptr,
+                                y_saved ? y_saved->scales : nullptr};
+  return hip_status(mxk::launch_swiglu_bwd(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+mx_status mx_wgrad_grouped(const void* dY, int64_t ld_dy, int64_t routed_rows, int64_t N, const mx_tensor* X,
+                           const int32_t* row_index, int32_t num_groups, const int64_t* group_offsets, void* dW,
+                           int32_t dwdt, int64_t ld_dw, uint32_t flags, mx_stream stream) {
+  if (!X) return MX_ERR_NULL;
+  if (flags & ~MX_WGRAD_ACCUMULATE) return MX_ERR_UNSUPPORTED;
+  if (num_groups < 1 || routed_rows < 0 || N < 0) return MX_ERR_SHAPE;
+  mx_status st = check_saved(X, X->rows, X->cols);
+  if (st != MX_OK) return st;
+  if (row_index ? (routed_rows > 0 && X->rows == 0) : X->rows != routed_rows) return MX_ERR_SHAPE;
+  if (!elem_aligned(row_index, 4) || !elem_aligned(group_offsets, 8)) return MX_ERR_ALIGN;
+  if (!group_offsets && num_groups != 1) return MX_ERR_NULL;
+  st = check_matrix(dY, MX_BF16, routed_rows, N, ld_dy);
+  if (st != MX_OK) return st;
+  const int64_t K = X->cols;
+  st = check_output(dW, dwdt, num_groups * N, K, ld_dw);
+  if (st != MX_OK) return st;
+  if (N * K == 0) return MX_OK;
+  const mxk::WgradArgs a = {static_cast<const uint16_t*>(dY), ld_dy, routed_rows, N, X->fmt,
+                            static_cast<const uint8_t*>(X->codes), X->scales, X->rows, K, row_index, group_offsets,
+                            num_groups, dW, (int)dwdt, ld_dw, (flags & MX_WGRAD_ACCUMULATE) != 0};
+  return hip_status(mxk::launch_wgrad_grouped(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+mx_status mx_combine(const void* Y, int32_t ydt, int64_t rows, int64_t cols, int64_t ld_y, const int32_t* slot_row,
+                     const float* weight, int64_t tokens, int32_t topk, void* out, int32_t odt, int64_t ld_out,
+                     mx_stream stream) {
+  mx_status st = check_slots(slot_row, weight, tokens, topk);
+  if (st != MX_OK) return st;
+  st = check_matrix(Y, ydt, rows, cols, ld_y);
+  if (st != MX_OK) return st;
+  st = check_output(out, odt, tokens, cols, ld_out);
+  if (st != MX_OK) return st;
+  if (tokens * cols == 0) return MX_OK;
+  return hip_status(mxk::launch_combine(Y, ydt, ld_y, rows, slot_row, weight, tokens, topk, cols, out, odt, ld_out,
+                                        reinterpret_cast<hipStream_t>(stream)));
+}
+
+mx_status mx_combine_backward(const void* d_out, int32_t dt, int64_t ld_do, const void* Y, int64_t ld_y,
+                              int64_t rows, int64_t cols, const int32_t* slot_row, const float* weight,
+                              int64_t tokens, int32_t topk, void* dY, int64_t ld_dy, float* d_weight,
+                              mx_stream stream) {
+  mx_status st = check_slots(slot_row, weight, tokens, topk);
+  if (st != MX_OK) return st;
+  st = check_matrix(d_out, dt, tokens, cols, ld_do);
+  if (st != MX_OK) return st;
+  if (rows < 0) return MX_ERR_SHAPE;
+  if (d_weight) {
+    st = check_matrix(Y, dt, rows, cols, ld_y);
+    if (st != MX_OK) return st;
+    if (!elem_aligned(d_weight, 4)) return MX_ERR_ALIGN;
+  }
+  if (dY) {
+    st = check_matrix(dY, dt, rows, cols, ld_dy);
+    if (st != MX_OK) return st;
+  }
+  if (tokens == 0 || (!dY && !d_weight)) return MX_OK;
+  return hip_status(mxk::launch_combine_bwd(d_out, dt, ld_do, Y, ld_y, rows, slot_row, weight, tokens, topk, cols,
+                                            dY, ld_dy, d_weight, reinterpret_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -1,0 +1,63 @@
+// decode8.h -- the 8-bit MX element types (E4M3, E5M2, INT8) times their block
+// scale, as FP32 (exact) and as BF16.  gfx950's scaled conversions give the
+// BF16 value of code * 2^(sc - 127) for every code and every scale code
+// 0..254, rounded to nearest even where BF16 cannot hold it (checked on the
+// device over all pairs: E4M3 is exact for scale codes 3..254, E5M2 for
+// 10..254).  Scale code 255 makes the block NaN.
+#pragma once
+#include <stdint.h>
+
+#include "codec.h"
+#include "rows.h"
+
+namespace mxk {
+
+// 2^(sc - 127) as FP32: code 0 is the subnormal 2^-127, 255 is NaN
+__device__ inline float e8m0_value(uint32_t sc) {
+  return sc == 0xFFu ? __builtin_nanf("") : (sc == 0u ? u2f(0x00400000u) : u2f(sc << 23));
+}
+
+// 4 codes of w times 2^(sc - 127): FP32
+template <int FMT>
+__device__ inline void decode4_f32(uint32_t w, float X, float* v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t c = (w >> (8 * i)) & 0xFFu;
+    float e;
+    if constexpr (FMT == FMT_MXFP8) {
+      const uint32_t mag = c & 0x7Fu;
+      e = mag == 0x7Fu ? __builtin_nanf("") : e4m3_mag_value(mag);
+      if (c & 0x80u) e = -e;
+    } else if constexpr (FMT == FMT_MXFP8_E5M2) {
+      e = e5m2_value(c);
+    } else {
+      e = int8_value(c);
+    }
+    v[i] = e * X;
+  }
+}
+
+// the same as BF16 pairs (element 2j in the low half of o[j])
+template <int FMT>
+__device__ inline void decode4_bf16(uint32_t w, uint32_t sc, uint32_t* o) {
+  if constexpr (FMT == FMT_MXINT8) {
+    const float X = e8m0_value(sc) * 0.015625f;
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = (float)(int8_t)(uint8_t)(w >> (8 * i)) * X;
+    o[0] = pack_bf16(v[0], v[1]);
+    o[1] = pack_bf16(v[2], v[3]);
+  } else {
+    const float X = u2f(sc << 23);
+    if constexpr (FMT == FMT_MXFP8) {
+      o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, X, false));
+      o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, X, true));
+    } else {
+      o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, X, false));
+      o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, X, true));
+    }
+    if (sc == 0xFFu) o[0] = o[1] = 0x7FC07FC0u;
+  }
+}
+
+}  // namespace mxk

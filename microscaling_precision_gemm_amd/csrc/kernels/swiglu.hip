@@ -1,0 +1,200 @@
+// swiglu.hip -- the gated activation between the two products of an expert,
+// its 8-bit checkpoint and its backward pass from that checkpoint.
+//   h = [gate | up],  s = 1 / (1 + exp(-gate)),  y = gate * s * up
+//   saved = Q8(h): h block-scaled to 8 bits along its rows, exactly the codes
+//   and scales the quantizer gives ("Thinking Machines ... Inkling 2 Small",
+//   section "A precision choice for each stage": saved forward tensors are
+//   kept quantized and decoded again for the backward pass)
+//   from h' = dec(saved):  d_gate = dy * up' * s' * (1 + gate' * (1 - s'))
+//                          d_up   = dy * gate' * s'
+// All steps are FP32; y, dh are rounded once.
+//
+// Bound by HBM.  A lane takes 8 consecutive gate elements and the 8 up
+// elements beside them, a lane quad one 32-element block of each half, so the
+// block maxima need two DPP steps and h is read once for both results.
+#include "../device/codec.h"
+#include "../device/cvt.h"
+#include "../device/decode8.h"
+#include "../device/mxenc.h"
+#include "../device/rows.h"
+#include "../device/wave.h"
+#include "../launch.h"
+
+namespace mxk {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+__device__ inline float sigmoid(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * x));
+}
+
+__global__ void k_clear(float* p) { *p = 0.0f; }
+
+// bits of the largest |v| of the workgroup into *amax (FP32 bits of
+// non-negative values order as integers; the order of the maxima is no matter)
+__device__ inline void block_max(uint32_t m, float* amax) {
+  __shared__ uint32_t red[kThreads / 64];
+  m = wave_max_u32(m);
+  if ((threadIdx.x & 63u) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kThreads / 64; ++w) m = red[w] > m ? red[w] : m;
+    atomicMax(reinterpret_cast<uint32_t*>(amax), m);
+  }
+}
+
+// FMT 0: nothing is saved.  Q chunks of 8 columns, cpr of them in a row.
+template <int DT, int FMT, bool SR>
+__global__ __launch_bounds__(kThreads) void k_swiglu(const void* __restrict__ h, int64_t ld_h, int64_t cpr,
+                                                     int64_t Q, void* __restrict__ y, int64_t ld_y,
+                                                     uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
+                                                     MxEnc enc, float* __restrict__ amax) {
+  const int64_t cols = 8 * cpr;
+  uint32_t m = 0;
+  for (int64_t q = (int64_t)blockIdx.x * kThreads + threadIdx.x; q < Q; q += (int64_t)gridDim.x * kThreads) {
+    const int64_t r = q / cpr, c = q - r * cpr;
+    float g[8], u[8], v[8];
+    load8<DT>(h, r * ld_h + 8 * c, g);
+    load8<DT>(h, r * ld_h + cols + 8 * c, u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = g[i] * sigmoid(g[i]) * u[i];
+    store8<DT>(y, r * ld_y + 8 * c, v);
+    if (amax) {
+      if constexpr (DT == DT_BF16) {  // of the values as stored
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = u2f(pack_bf16(v[i], v[i]) << 16);
+      }
+      const uint32_t o = max_abs_bits(v);
+      m = o > m ? o : m;
+    }
+    if constexpr (FMT != 0) {
+      const int64_t qg = r * 2 * cpr + c, qu = qg + cpr;  // chunks of the saved [rows, 2 cols] tensor
+      Enc<FMT> eg, eu;
+      encode_mx<FMT, SR>(enc, qg, g, eg);
+      encode_mx<FMT, SR>(enc, qu, u, eu);
+      *reinterpret_cast<uint2*>(codes + 8 * qg) = make_uint2(eg.w[0], eg.w[1]);
+      *reinterpret_cast<uint2*>(codes + 8 * qu) = make_uint2(eu.w[0], eu.w[1]);
+      if ((c & 3) == 0) {
+        scales[qg >> 2] = (uint8_t)eg.sc;
+        scales[qu >> 2] = (uint8_t)eu.sc;
+      }
+    }
+  }
+  if (amax) block_max(m, amax);
+}
+
+// 8 elements of an 8-bit MX format times their block scale, exactly
+template <int FMT>
+__device__ inline void decode8(uint2 w, uint32_t sc, float (&v)[8]) {
+  const float X = e8m0_value(sc);
+  decode4_f32<FMT>(w.x, X, v);
+  decode4_f32<FMT>(w.y, X, v + 4);
+}
+
+template <int DT, int FMT, int YFMT>
+__global__ __launch_bounds__(kThreads) void k_swiglu_bwd(const uint8_t* __restrict__ codes,
+                                                         const uint8_t* __restrict__ scales, int64_t cpr, int64_t Q,
+                                                         const void* __restrict__ dy, int64_t ld_dy,
+                                                         void* __restrict__ dh, int64_t ld_dh,
+                                                         uint8_t* __restrict__ y_codes,
+                                                         uint8_t* __restrict__ y_scales) {
+  const int64_t cols = 8 * cpr;
+  for (int64_t q = (int64_t)blockIdx.x * kThreads + threadIdx.x; q < Q; q += (int64_t)gridDim.x * kThreads) {
+    const int64_t r = q / cpr, c = q - r * cpr;
+    const int64_t qg = r * 2 * cpr + c, qu = qg + cpr;
+    float g[8], u[8], d[8], y[8];
+    decode8<FMT>(*reinterpret_cast<const uint2*>(codes + 8 * qg), scales[qg >> 2], g);
+    decode8<FMT>(*reinterpret_cast<const uint2*>(codes + 8 * qu), scales[qu >> 2], u);
+    load8<DT>(dy, r * ld_dy + 8 * c, d);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float s = sigmoid(g[i]), gs = g[i] * s;
+      const float dg = d[i] * u[i] * (s * fmaf(g[i], 1.0f - s, 1.0f));
+      const float du = d[i] * gs;
+      y[i] = gs * u[i];
+      g[i] = dg;
+      u[i] = du;
+    }
+    store8<DT>(dh, r * ld_dh + 8 * c, g);
+    store8<DT>(dh, r * ld_dh + cols + 8 * c, u);
+    if constexpr (YFMT != 0) {
+      Enc<YFMT> e;
+      encode_mx<YFMT, false>(MxEnc{false, 0, 0}, q, y, e);
+      *reinterpret_cast<uint2*>(y_codes + 8 * q) = make_uint2(e.w[0], e.w[1]);
+      if ((c & 3) == 0) y_scales[q >> 2] = (uint8_t)e.sc;
+    }
+  }
+}
+
+int grid_of(int64_t Q) {
+  const int64_t g = (Q + kThreads - 1) / kThreads;
+  return (int)(g < 2048 ? g : 2048);
+}
+
+template <int DT, int FMT>
+void swiglu_f(const SwigluArgs& a, int64_t Q, hipStream_t s) {
+  const MxEnc enc{false, a.seed, a.counter};
+  if (FMT != 0 && a.sr)
+    hipLaunchKernelGGL((k_swiglu<DT, FMT, FMT != 0>), dim3(grid_of(Q)), dim3(kThreads), 0, s, a.h, a.ld_h,
+                       a.cols / 8, Q, a.y, a.ld_y, a.codes, a.scales, enc, a.amax);
+  else
+    hipLaunchKernelGGL((k_swiglu<DT, FMT, false>), dim3(grid_of(Q)), dim3(kThreads), 0, s, a.h, a.ld_h, a.cols / 8,
+                       Q, a.y, a.ld_y, a.codes, a.scales, enc, a.amax);
+}
+
+template <int DT>
+void swiglu_d(const SwigluArgs& a, int64_t Q, hipStream_t s) {
+  switch (a.fmt) {
+    case FMT_MXFP8: return swiglu_f<DT, FMT_MXFP8>(a, Q, s);
+    case FMT_MXFP8_E5M2: return swiglu_f<DT, FMT_MXFP8_E5M2>(a, Q, s);
+    case FMT_MXINT8: return swiglu_f<DT, FMT_MXINT8>(a, Q, s);
+    default: return swiglu_f<DT, 0>(a, Q, s);
+  }
+}
+
+template <int DT, int FMT>
+void bwd_f(const SwigluBwdArgs& a, int64_t Q, hipStream_t s) {
+#define MXK_SB(Y)                                                                                                  \
+  hipLaunchKernelGGL((k_swiglu_bwd<DT, FMT, Y>), dim3(grid_of(Q)), dim3(kThreads), 0, s, a.codes, a.scales,     \
+                     a.cols / 8, Q, a.dy, a.ld_dy, a.dh, a.ld_dh, a.y_codes, a.y_scales)
+  switch (a.y_fmt) {
+    case FMT_MXFP8: MXK_SB(FMT_MXFP8); break;
+    case FMT_MXFP8_E5M2: MXK_SB(FMT_MXFP8_E5M2); break;
+    case FMT_MXINT8: MXK_SB(FMT_MXINT8); break;
+    default: MXK_SB(0); break;
+  }
+#undef MXK_SB
+}
+
+template <int DT>
+void bwd_d(const SwigluBwdArgs& a, int64_t Q, hipStream_t s) {
+  switch (a.fmt) {
+    case FMT_MXFP8: return bwd_f<DT, FMT_MXFP8>(a, Q, s);
+    case FMT_MXFP8_E5M2: return bwd_f<DT, FMT_MXFP8_E5M2>(a, Q, s);
+    default: return bwd_f<DT, FMT_MXINT8>(a, Q, s);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t s) {
+  if (a.amax) hipLaunchKernelGGL(k_clear, dim3(1), dim3(1), 0, s, a.amax);
+  const int64_t Q = a.rows * (a.cols / 8);
+  if (Q > 0) {
+    if (a.dt == DT_BF16) swiglu_d<DT_BF16>(a, Q, s);
+    else swiglu_d<DT_F32>(a, Q, s);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_swiglu_bwd(const SwigluBwdArgs& a, hipStream_t s) {
+  const int64_t Q = a.rows * (a.cols / 8);
+  if (a.dt == DT_BF16) bwd_d<DT_BF16>(a, Q, s);
+  else bwd_d<DT_F32>(a, Q, s);
+  return hipGetLastError();
+}
+
+}  // namespace mxk
