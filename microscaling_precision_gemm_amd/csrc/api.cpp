@@ -669,7 +669,7 @@ mx_status mx_wgrad_grouped(const void* dY, int64_t ld_dy, int64_t routed_rows, i
                            int32_t dwdt, int64_t ld_dw, uint32_t flags, mx_stream stream) {
   if (!X) return MX_ERR_NULL;
   if (flags & ~MX_WGRAD_ACCUMULATE) return MX_ERR_UNSUPPORTED;
-  if (num_groups < 1 || routed_rows < 0 || N < 0) return MX_ERR_SHAPE;
+  if (num_groups < 1 || routed_rows < 0 || routed_rows > INT32_MAX || N < 0) return MX_ERR_SHAPE;
   mx_status st = check_saved(X, X->rows, X->cols);
   if (st != MX_OK) return st;
   if (row_index ? (routed_rows > 0 && X->rows == 0) : X->rows != routed_rows) return MX_ERR_SHAPE;
@@ -678,6 +678,7 @@ mx_status mx_wgrad_grouped(const void* dY, int64_t ld_dy, int64_t routed_rows, i
   st = check_matrix(dY, MX_BF16, routed_rows, N, ld_dy);
   if (st != MX_OK) return st;
   const int64_t K = X->cols;
+  if (X->rows > INT32_MAX || K > INT32_MAX) return MX_ERR_SHAPE;
   st = check_output(dW, dwdt, num_groups * N, K, ld_dw);
   if (st != MX_OK) return st;
   if (N * K == 0) return MX_OK;

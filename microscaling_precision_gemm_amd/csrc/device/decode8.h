@@ -48,7 +48,9 @@ __device__ inline void decode4_bf16(uint32_t w, uint32_t sc, uint32_t* o) {
     o[0] = pack_bf16(v[0], v[1]);
     o[1] = pack_bf16(v[2], v[3]);
   } else {
+    // the NaN code of both types for a NaN scale
     const float X = u2f(sc << 23);
+    w |= sc == 0xFFu ? 0x7F7F7F7Fu : 0u;
     if constexpr (FMT == FMT_MXFP8) {
       o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, X, false));
       o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, X, true));
@@ -56,7 +58,6 @@ __device__ inline void decode4_bf16(uint32_t w, uint32_t sc, uint32_t* o) {
       o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, X, false));
       o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, X, true));
     }
-    if (sc == 0xFFu) o[0] = o[1] = 0x7FC07FC0u;
   }
 }
 
