@@ -43,10 +43,15 @@ struct WgradParams {
 };
 
 // A stage holds kStep rows of T BF16 columns of each operand.  16-byte chunk c
-// of row r lies at chunk c ^ swz(r) of its row: a transposed read touches 4
-// rows x 64 bytes (and the 4 rows 8 below), which without the swizzle fall on
-// the same banks.
+// of row r lies at chunk place(r, c) of its row: a transposed read touches 4
+// rows x 64 bytes (and the 4 rows 8 below), which without the exchange of bits
+// 1..3 fall on the same banks; bit 0 does the same for the writes of decoded
+// codes, where neighbouring lanes are two chunks apart.
 __device__ inline uint32_t swz(uint32_t r) { return ((r & 3u) << 2) | ((r >> 2) & 2u); }
+template <int T>
+__device__ inline uint32_t place(uint32_t r, uint32_t c) {
+  return c ^ swz(r) ^ (T == 256 ? (c >> 4) & 1u : r & 1u);
+}
 
 __device__ inline void stage_barrier() {
   __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4) | (0 << 8));  // lgkmcnt(0): own LDS accesses done
@@ -138,7 +143,7 @@ template <int FMT, int WT, bool GATHER>
 __device__ inline void load_x(const WgradParams& p, uint32_t tid, int64_t k0, int i, Copy<FMT, WT, GATHER>& c) {
   typedef Copy<FMT, WT, GATHER> C;
   int32_t src = c.src[i];
-  src = src < 0 ? 0 : (src < (int32_t)p.x_rows ? src : (int32_t)p.x_rows - 1);
+  src = min(max(src, 0), (int32_t)p.x_rows - 1);
   uint32_t k = C::xcol(tid);
   k = k0 + k < p.K ? k : 0;  // columns past K are computed and not stored
   c.x[i] = *reinterpret_cast<const uint4*>(p.codes + k0 + ((uint64_t)(uint32_t)src * (uint32_t)p.K + k));
@@ -158,11 +163,10 @@ __device__ inline void put_d(const Group& g, int32_t st, uint32_t tid, int i, co
     w.z = in ? w.z : 0;
     w.w = in ? w.w : 0;
   }
-  *reinterpret_cast<uint4*>(stage + r * C::PITCH + 16u * (C::dcol(tid) / 8 ^ swz(r))) = w;
+  *reinterpret_cast<uint4*>(stage + r * C::PITCH + 16u * place<C::T>(r, C::dcol(tid) / 8)) = w;
 }
 
-// the thread's code chunk i, decoded; the two halves are written in an order
-// that differs between the lanes that would meet on a bank
+// the thread's code chunk i, decoded
 template <bool WHOLE, int FMT, int WT, bool GATHER>
 __device__ inline void put_x(const Group& g, int32_t st, uint32_t tid, int i, const Copy<FMT, WT, GATHER>& c, uint8_t* stage) {
   typedef Copy<FMT, WT, GATHER> C;
@@ -178,12 +182,9 @@ __device__ inline void put_x(const Group& g, int32_t st, uint32_t tid, int i, co
     for (int e = 0; e < 8; ++e) o[e] = in ? o[e] : 0;
   }
   const uint32_t ch = C::xcol(tid) / 8;
-  const uint32_t flip = C::T == 256 ? (tid >> 3) & 1u : r & 1u;
   uint8_t* row = stage + C::HALF + r * C::PITCH;
-  const uint4 first = make_uint4(flip ? o[4] : o[0], flip ? o[5] : o[1], flip ? o[6] : o[2], flip ? o[7] : o[3]);
-  const uint4 second = make_uint4(flip ? o[0] : o[4], flip ? o[1] : o[5], flip ? o[2] : o[6], flip ? o[3] : o[7]);
-  *reinterpret_cast<uint4*>(row + 16u * ((ch + flip) ^ swz(r))) = first;
-  *reinterpret_cast<uint4*>(row + 16u * ((ch + 1u - flip) ^ swz(r))) = second;
+  *reinterpret_cast<uint4*>(row + 16u * place<C::T>(r, ch)) = make_uint4(o[0], o[1], o[2], o[3]);
+  *reinterpret_cast<uint4*>(row + 16u * place<C::T>(r, ch + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 template <int F>
@@ -245,6 +246,26 @@ __device__ inline void copy_share(const WgradParams& p, const Group& g, int32_t 
   }
 }
 
+// Spreads a window's other work over its 16 products: the next fragments
+// first, so that they have landed when the window ends, then the stage writes
+// and the loads.
+template <int I = 0>
+__device__ inline void spread_window() {
+  if constexpr (I < 16) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                          // matrix
+    if constexpr (I < 8) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);     // LDS read
+    __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);                          // VALU
+    if constexpr (I >= 8 && I % 2) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);  // LDS write
+    if constexpr (I >= 8 && I < 13) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // load
+    spread_window<I + 1>();
+  }
+}
+template <int WT>
+__device__ inline void window_end() {
+  if constexpr (WT == 128) spread_window();
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // One stage: windows of 16 rows.  While a window's products run, the next
 // window's fragments are read and a quarter of the next stage is written.  The
 // barrier comes before the last window, when its fragments are in registers:
@@ -260,16 +281,20 @@ __device__ inline void stage_products(const WgradParams& p, const Group& g, int3
   read_frags<WT>(cur, 1, aoff, boff, f[1]);
   copy_share<0, WHOLE, ODD>(p, g, st + 1, tid, n0, k0, c, smem);
   mma(f[0], acc);
+  window_end<WT>();
   read_frags<WT>(cur, 2, aoff, boff, f[0]);
   copy_share<1, WHOLE, ODD>(p, g, st + 1, tid, n0, k0, c, smem);
   mma(f[1], acc);
+  window_end<WT>();
   read_frags<WT>(cur, 3, aoff, boff, f[1]);
   copy_share<2, WHOLE, ODD>(p, g, st + 1, tid, n0, k0, c, smem);
   mma(f[0], acc);
+  window_end<WT>();
   stage_barrier();
   read_frags<WT>(nxt, 0, aoff, boff, f[0]);
   copy_share<3, WHOLE, ODD>(p, g, st + 2, tid, n0, k0, c, smem);
   mma(f[1], acc);
+  window_end<WT>();
 }
 
 // the wave's products: lanes 0..31 and 32..63 each store 32 adjacent columns
@@ -340,8 +365,8 @@ k_wgrad(WgradParams p) {
 #pragma unroll
       for (int i = 0; i < F; ++i) {
         const uint32_t col = 32 * i + 16 * (gr & 1) + 4 * (s & 3);
-        aoff[i] = row * C::PITCH + 16u * (((wn + col) / 8) ^ swz(row)) + 8 * (s & 1);
-        boff[i] = row * C::PITCH + 16u * (((wk + col) / 8) ^ swz(row)) + 8 * (s & 1);
+        aoff[i] = row * C::PITCH + 16u * place<T>(row, (wn + col) / 8) + 8 * (s & 1);
+        boff[i] = row * C::PITCH + 16u * place<T>(row, (wk + col) / 8) + 8 * (s & 1);
       }
     }
     C c;
