@@ -37,27 +37,25 @@ __device__ inline void decode4_f32(uint32_t w, float X, float* v) {
   }
 }
 
-// the same as BF16 pairs (element 2j in the low half of o[j])
+// A block scale as the BF16 decoder uses it.
+struct Scale8 {
+  float x;       // INT8: 2^(sc - 127) / 64; FP8: the exponent field of 2^(sc - 127)
+  uint32_t nan;  // FP8: or-ed into the codes, all NaN codes for a NaN scale
+};
 template <int FMT>
-__device__ inline void decode4_bf16(uint32_t w, uint32_t sc, uint32_t* o) {
+__device__ inline Scale8 scale8(uint32_t sc) {
+  if constexpr (FMT == FMT_MXINT8) return {e8m0_value(sc) * 0.015625f, 0u};
+  else return {u2f(sc << 23), sc == 0xFFu ? 0x7F7F7F7Fu : 0u};
+}
+// codes 2 H and 2 H + 1 of w times the scale, as a BF16 pair
+template <int FMT, int H>
+__device__ inline uint32_t decode2_bf16(uint32_t w, const Scale8& s) {
   if constexpr (FMT == FMT_MXINT8) {
-    const float X = e8m0_value(sc) * 0.015625f;
-    float v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = (float)(int8_t)(uint8_t)(w >> (8 * i)) * X;
-    o[0] = pack_bf16(v[0], v[1]);
-    o[1] = pack_bf16(v[2], v[3]);
+    return pack_bf16((float)(int8_t)(uint8_t)(w >> (16 * H)) * s.x, (float)(int8_t)(uint8_t)(w >> (16 * H + 8)) * s.x);
+  } else if constexpr (FMT == FMT_MXFP8) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w | s.nan, s.x, H != 0));
   } else {
-    // the NaN code of both types for a NaN scale
-    const float X = u2f(sc << 23);
-    w |= sc == 0xFFu ? 0x7F7F7F7Fu : 0u;
-    if constexpr (FMT == FMT_MXFP8) {
-      o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, X, false));
-      o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, X, true));
-    } else {
-      o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, X, false));
-      o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, X, true));
-    }
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w | s.nan, s.x, H != 0));
   }
 }
 
