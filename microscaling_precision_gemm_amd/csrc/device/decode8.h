@@ -37,26 +37,31 @@ __device__ inline void decode4_f32(uint32_t w, float X, float* v) {
   }
 }
 
-// A block scale as the BF16 decoder uses it.
-struct Scale8 {
-  float x;       // INT8: 2^(sc - 127) / 64; FP8: the exponent field of 2^(sc - 127)
-  uint32_t nan;  // FP8: or-ed into the codes, all NaN codes for a NaN scale
-};
-template <int FMT>
-__device__ inline Scale8 scale8(uint32_t sc) {
-  if constexpr (FMT == FMT_MXINT8) return {e8m0_value(sc) * 0.015625f, 0u};
-  else return {u2f(sc << 23), sc == 0xFFu ? 0x7F7F7F7Fu : 0u};
-}
-// codes 2 H and 2 H + 1 of w times the scale, as a BF16 pair
+// Codes 2 H and 2 H + 1 of w times a block scale, as a BF16 pair.  x holds the
+// scale as scale8<FMT>() or scale8_word<FMT>() gives it.  The FP8 conversions
+// look at the exponent field of x alone and give NaN for 255 whatever the code
+// (checked on the device over all codes and scale codes).
 template <int FMT, int H>
-__device__ inline uint32_t decode2_bf16(uint32_t w, const Scale8& s) {
+__device__ inline uint32_t decode2_bf16(uint32_t w, float x) {
   if constexpr (FMT == FMT_MXINT8) {
-    return pack_bf16((float)(int8_t)(uint8_t)(w >> (16 * H)) * s.x, (float)(int8_t)(uint8_t)(w >> (16 * H + 8)) * s.x);
+    return pack_bf16((float)(int8_t)(uint8_t)(w >> (16 * H)) * x, (float)(int8_t)(uint8_t)(w >> (16 * H + 8)) * x);
   } else if constexpr (FMT == FMT_MXFP8) {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w | s.nan, s.x, H != 0));
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, x, H != 0));
   } else {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w | s.nan, s.x, H != 0));
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w, x, H != 0));
   }
+}
+template <int FMT>
+__device__ inline float scale8(uint32_t sc) {
+  if constexpr (FMT == FMT_MXINT8) return e8m0_value(sc) * 0.015625f;
+  else return u2f(sc << 23);
+}
+// the same from byte `shift` / 8 of a word: for FP8 one rotation puts it into
+// the exponent field, and what comes beside it is not looked at
+template <int FMT>
+__device__ inline float scale8_word(uint32_t w, uint32_t shift) {
+  if constexpr (FMT == FMT_MXINT8) return scale8<FMT>((w >> shift) & 0xFFu);
+  else return u2f(__builtin_amdgcn_alignbit(w, w, shift + 9u));
 }
 
 }  // namespace mxk

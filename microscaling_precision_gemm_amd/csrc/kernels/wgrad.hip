@@ -11,6 +11,7 @@
 // (ds_read_b64_tr_b16: 16 lanes turn 4 rows x 16 columns into 4 row values of
 // one column each).
 #include <atomic>
+#include <type_traits>
 
 #include "../device/decode8.h"
 #include "../device/gemm_common.h"
@@ -62,180 +63,252 @@ __device__ __forceinline__ void stage_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// What one thread copies of a stage: DC chunks of 8 dY columns and XC chunks
-// of 16 codes, and which stage row and column they are.
-template <int FMT, int WT, bool GATHER>
+// The variants.  WT: columns of a wave's tile (a workgroup's is T = 2 WT
+// square).  ANY: any N, K, pitch and size of X, otherwise dY in whole 16-byte
+// chunks, K a multiple of 128 (a scale code is then loaded as the aligned word
+// around it) and offsets within 32 bits.  GATHER: X's rows by the row index.
+template <int FMT_, int WT_, bool ANY_, bool GATHER_>
+struct Variant {
+  static constexpr int FMT = FMT_, WT = WT_;
+  static constexpr bool ANY = ANY_, GATHER = GATHER_;
+  static constexpr int F = WT / 32, T = 2 * WT;
+  static constexpr int DC = kStep * T / 8 / 256;   // a thread's chunks of 8 dY columns in a stage,
+  static constexpr int DR = 256 / (T / 8);         // and the rows between them
+  static constexpr int XC = kStep * T / 16 / 256;  // the same for chunks of 16 codes
+  static constexpr int XR = 256 / (T / 16);
+  static constexpr int PITCH = 2 * T;              // bytes of a stage row
+  static constexpr int HALF = kStep * PITCH;       // bytes of an operand's stage
+  static constexpr int SCRATCH = 64 * WT;          // bytes a wave needs to turn its products into rows
+  static constexpr int LDS = 4 * HALF + 4 * SCRATCH;
+};
+
+// One tile and its rows (the same in all lanes).
+struct Unit {
+  uint32_t n0, k0;
+  int32_t e;         // group; -1: there is none
+  int32_t row, cnt;  // its rows, at least one
+  // Stages: at least 3, so that the copies, which run ahead of the products,
+  // never reach past the tile after this one.
+  __device__ __forceinline__ int32_t stages() const { return max((cnt + kStep - 1) / kStep, 3); }
+};
+
+template <class V>
+__device__ __forceinline__ void clear_tile(const WgradParams& p, uint32_t e, uint32_t n0, uint32_t k0) {
+  for (uint32_t q = threadIdx.x; q < V::T * V::T; q += 256) {
+    const int64_t n = (int64_t)n0 + q / V::T, k = (int64_t)k0 + q % V::T;
+    if (n < p.N && k < p.K) {
+      const int64_t off = (e * p.N + n) * p.ld_dw + k;
+      if (p.f32) static_cast<float*>(p.dw)[off] = 0.0f;
+      else static_cast<uint16_t*>(p.dw)[off] = 0;
+    }
+  }
+}
+
+// Unit `id` or the next one of this workgroup that has rows.  The tiles of a
+// group are dealt to the 8 XCDs (workgroup id mod 8) in runs, n fastest, so
+// that the workgroups of an XCD share rows of dY and X in its L2.  A group
+// without rows is passed over; its tiles of dW are cleared on the way.
+template <class V>
+__device__ __forceinline__ Unit seek(const WgradParams& p, uint32_t& id) {
+  const uint32_t tiles = p.tn * p.tk, per = (tiles + 7) / 8;
+  for (; id < p.units; id += gridDim.x) {
+    const uint32_t slot = id >> 3, e = slot / per;
+    const uint32_t in = (id & 7u) * per + (slot - e * per);
+    if (in >= tiles) continue;
+    int64_t lo = 0, hi = p.R;
+    if (p.offsets) {  // clamped into [0, R]
+      lo = p.offsets[e];
+      hi = p.offsets[e + 1];
+      lo = lo < 0 ? 0 : (lo > p.R ? p.R : lo);
+      hi = hi < lo ? lo : (hi > p.R ? p.R : hi);
+    }
+    const uint32_t tk = in / p.tn, n0 = (in - tk * p.tn) * V::T, k0 = tk * V::T;
+    if (hi > lo) return {n0, k0, (int32_t)e, (int32_t)lo, (int32_t)(hi - lo)};
+    if (!p.accumulate) clear_tile<V>(p, e, n0, k0);
+  }
+  return {0, 0, -1, 0, 1};
+}
+
+// A position in the stream of stages.
+struct Cursor {
+  int32_t row, rem;  // first row of the stage, rows of the group from there on
+  int32_t left;      // stages of the tile from this one on
+  __device__ __forceinline__ void start(const Unit& u) {
+    row = u.row;
+    rem = u.cnt;
+    left = u.stages();
+  }
+  // To the next stage; true when that begins `next` (the last tile's last
+  // stage is repeated for ever).  A tile's stages beyond its rows repeat the
+  // last one with rows.
+  __device__ __forceinline__ bool step(const Unit& next) {
+    if (--left == 0) {
+      if (next.e >= 0) {
+        start(next);
+        return true;
+      }
+      left = INT32_MAX;
+    }
+    if (rem > kStep) {
+      row += kStep;
+      rem -= kStep;
+    }
+    return false;
+  }
+};
+
+// What one thread copies.
+template <class V>
 struct Copy {
-  static constexpr int T = 2 * WT;               // tile edge
-  static constexpr int DC = kStep * T / 8 / 256;  // dY chunks
-  static constexpr int XC = kStep * T / 16 / 256; // code chunks
-  static constexpr int PITCH = 2 * T;            // bytes of a stage row
-  static constexpr int HALF = kStep * PITCH;     // bytes of an operand's stage
-
-  static constexpr int DR = 256 / (T / 8);       // rows between a thread's dY chunks
-  static constexpr int XR = 256 / (T / 16);      // and between its code chunks
-
-  u4 d[DC], x[XC];
-  // scale codes: the aligned word that holds one (K a multiple of 128), whose
-  // load needs no widening, or the byte
-  static constexpr bool WORDS = WT == 128;
-  uint32_t sc[XC];
-  int32_t src[XC];  // rows of X the next loads take
-  // LDS offsets of chunk 0 in the buffer that is written (the other chunks
-  // are whole rows below, for dY of 256-wide tiles with bit 1 of the chunk
-  // number exchanged in turn), and the thread's columns
-  uint32_t dput, xput, dcol, xcol, sc_shift;
+  typedef typename std::conditional<V::ANY, uint64_t, uint32_t>::type Off;
+  u4 d[V::DC], x[V::XC];
+  uint32_t sc[V::XC];
+  // where the next loads take it from: byte offsets from uniform bases
+  const char* dbase;
+  const uint8_t* xbase;
+  uint32_t doff[V::DC];
+  Off xoff[V::XC];
+  int32_t ridx;  // GATHER: lane r of the wave holds the row of X of row r of the stage after that
+  uint32_t kk;   // first of the thread's columns of X in the tile, 0 past K
+  // constants: the thread's columns, first rows, and LDS addresses of its
+  // chunk 0 in the buffer that is written (the other chunks lie whole rows
+  // below; for dY of 256-wide tiles bit 1 of the chunk number changes in turn)
+  uint32_t dcol, xcol, drow, xrow;
+  uint32_t dput, dput1, xput, sc_shift;
 
   __device__ __forceinline__ void init(uint32_t tid) {
-    dcol = tid % (T / 8) * 8;
-    xcol = tid % (T / 16) * 16;
-    sc_shift = WORDS ? xcol / 32 % 4 * 8 : 0;
-    const uint32_t dr = tid / (T / 8), xr = tid / (T / 16);
-    dput = dr * PITCH + 16u * place<T>(dr, dcol / 8);
-    xput = HALF + xr * PITCH + 16u * place<T>(xr, xcol / 8);
+    dcol = tid % (V::T / 8) * 8;
+    xcol = tid % (V::T / 16) * 16;
+    drow = tid / (V::T / 8);
+    xrow = tid / (V::T / 16);
+    dput = drow * V::PITCH + 16u * place<V::T>(drow, dcol / 8);
+    dput1 = V::DR == 8 ? dput ^ 32u : dput;
+    xput = V::HALF + xrow * V::PITCH + 16u * place<V::T>(xrow, xcol / 16 * 2);
+    sc_shift = xcol / 32 % 4 * 8;
   }
   __device__ __forceinline__ void flip() {  // to the other buffer
-    dput ^= 2 * HALF;
-    xput ^= 2 * HALF;
+    dput ^= 2 * V::HALF;
+    dput1 ^= 2 * V::HALF;
+    xput ^= 2 * V::HALF;
   }
   __device__ __forceinline__ uint32_t dput_of(int i) const {
-    return (DR == 8 && (i & 1) ? dput ^ 32u : dput) + (uint32_t)(i * DR * PITCH);
+    return ((i & 1) ? dput1 : dput) + (uint32_t)(i * V::DR * V::PITCH);
   }
 };
 
-// One stage of the workgroup's work (the same in all its lanes).
-struct Stage {
-  int32_t row;      // its first row
-  int32_t rem;      // rows of the group from there on, at least 1
-  uint32_t n0, k0;  // the tile
-  int32_t e;        // the group; -1 past the last tile
-};
-
-// Rows past the group repeat its last one; drop_rows() clears them in LDS.
-template <int FMT, int WT, bool GATHER>
-__device__ __forceinline__ void load_src(const WgradParams& p, const Stage& s, uint32_t tid, int i,
-                                         Copy<FMT, WT, GATHER>& c) {
-  typedef Copy<FMT, WT, GATHER> C;
-  const int32_t r = min((int32_t)(tid / (C::T / 16)) + i * C::XR, s.rem - 1);
-  if constexpr (GATHER)
-    c.src[i] = *reinterpret_cast<const int32_t*>(reinterpret_cast<const char*>(p.row_index + s.row) + 4u * (uint32_t)r);
-  else c.src[i] = s.row + r;
+// Row numbers of X for the stage at `at` (rows past the group repeat the last;
+// drop_rows() clears them in LDS).
+template <class V>
+__device__ __forceinline__ void load_rows(const WgradParams& p, const Cursor& at, uint32_t lane, Copy<V>& c) {
+  if constexpr (V::GATHER)
+    c.ridx = *reinterpret_cast<const int32_t*>(reinterpret_cast<const char*>(p.row_index + at.row) +
+                                               4u * (uint32_t)min((int32_t)lane, at.rem - 1));
 }
 
-// What a thread's loads of a stage have in common.
-struct Aim {
-  const char* base;     // dY at the stage's first row and the tile's first column (uniform)
-  uint32_t doff, dlim;  // byte offset of chunk 0, and of the last row of the group
-  int32_t row0, rem;    // the thread's first row, rows of the group
-  uint32_t cols;        // columns of the thread's dY chunk that exist
-  const uint8_t* codes;  // X: row 0 at the thread's columns
-  const uint8_t* scales;
-};
-template <int FMT, int WT, bool GATHER>
-__device__ __forceinline__ Aim aim(const WgradParams& p, const Stage& s, uint32_t tid,
-                                   const Copy<FMT, WT, GATHER>& c) {
-  typedef Copy<FMT, WT, GATHER> C;
-  // 64 rows of a pitch below 2^24 elements: 32-bit offsets
-  const uint32_t pitch = 2u * (uint32_t)p.ld_dy;
-  // columns past N and K are computed from others and not stored
-  const uint32_t cc = s.n0 + c.dcol < (uint32_t)p.N ? 2u * c.dcol : 0u;
-  const uint32_t kk = s.k0 + c.xcol < (uint32_t)p.K ? c.xcol : 0u;
-  Aim a;
-  a.base = reinterpret_cast<const char*>(p.dy + (int64_t)s.row * p.ld_dy + s.n0);
-  a.doff = tid / (C::T / 8) * pitch + cc;
-  a.dlim = (uint32_t)min(s.rem - 1, kStep) * pitch + cc;
-  a.row0 = (int32_t)(tid / (C::T / 8));
-  a.rem = s.rem;
-  a.cols = (uint32_t)p.N - s.n0 - c.dcol;
-  a.codes = p.codes + s.k0 + kk;
-  a.scales = p.scales + s.k0 / 32 + (C::WORDS ? kk / 128 * 4 : kk / 32);
-  return a;
+// Aims the loads at the stage at `at` of tile u.  `fresh`: the tile, or the
+// number of rows, is another than before; the lane offsets of full stages of
+// one tile are the same.
+template <class V>
+__device__ __forceinline__ void aim(const WgradParams& p, const Unit& u, const Cursor& at, bool fresh, Copy<V>& c) {
+  c.dbase = reinterpret_cast<const char*>(p.dy + (int64_t)at.row * p.ld_dy + u.n0);
+  if (fresh || at.rem < kStep) {
+    // columns past N and K are computed from others and not stored
+    const uint32_t cc = u.n0 + c.dcol < (uint32_t)p.N ? 2u * c.dcol : 0u;
+    c.kk = u.k0 + c.xcol < (uint32_t)p.K ? c.xcol : 0u;
+    const uint32_t last = (uint32_t)min(at.rem, kStep) - 1u;
+#pragma unroll
+    for (int i = 0; i < V::DC; ++i) {
+      const uint32_t r = min(c.drow + i * V::DR, last);
+      c.doff[i] = V::ANY ? r : r * 2u * (uint32_t)p.ld_dy + cc;
+    }
+    if constexpr (!V::GATHER) {
+#pragma unroll
+      for (int i = 0; i < V::XC; ++i)
+        c.xoff[i] = (typename Copy<V>::Off)min(c.xrow + i * V::XR, last) * (uint32_t)p.K + c.kk;
+    }
+  }
+  if constexpr (V::GATHER) {
+    c.xbase = p.codes + u.k0;
+    const uint32_t r = (uint32_t)min(max(c.ridx, 0), (int32_t)p.x_rows - 1);
+    if constexpr (V::ANY) {
+#pragma unroll
+      for (int i = 0; i < V::XC; ++i)
+        c.xoff[i] = (uint64_t)lane_read(r, c.xrow + i * V::XR) * (uint32_t)p.K + c.kk;
+    } else {
+      const uint32_t o = r * (uint32_t)p.K;
+#pragma unroll
+      for (int i = 0; i < V::XC; ++i) c.xoff[i] = lane_read(o, c.xrow + i * V::XR) + c.kk;
+    }
+  } else {
+    c.xbase = p.codes + (int64_t)at.row * p.K + u.k0;
+  }
 }
 
-template <bool ODD, int FMT, int WT, bool GATHER>
-__device__ __forceinline__ void load_d(const WgradParams& p, const Aim& a, int i, Copy<FMT, WT, GATHER>& c) {
-  typedef Copy<FMT, WT, GATHER> C;
-  const uint32_t off = min(a.doff + (uint32_t)(i * C::DR) * (2u * (uint32_t)p.ld_dy), a.dlim);
-  if constexpr (ODD) {  // rows may end inside a chunk, or have a large pitch
-    const int64_t row = min((int64_t)a.row0 + i * C::DR, (int64_t)a.rem - 1);
-    const uint16_t* at = reinterpret_cast<const uint16_t*>(a.base) + row * p.ld_dy + c.dcol;
+template <class V>
+__device__ __forceinline__ void load_d(const WgradParams& p, uint32_t n0, int i, Copy<V>& c) {
+  if constexpr (V::ANY) {  // rows may end inside a chunk, or have a large pitch
+    const uint16_t* at = reinterpret_cast<const uint16_t*>(c.dbase) + (int64_t)c.doff[i] * p.ld_dy + c.dcol;
     uint32_t w[4] = {};
 #pragma unroll
-    for (uint32_t e = 0; e < 8; ++e)
-      if ((int32_t)a.cols > (int32_t)e) w[e >> 1] |= (uint32_t)at[e] << (16 * (e & 1));
+    for (int e = 0; e < 8; ++e)
+      if (n0 + c.dcol + e < (uint32_t)p.N) w[e >> 1] |= (uint32_t)at[e] << (16 * (e & 1));
     c.d[i] = u4{w[0], w[1], w[2], w[3]};
   } else {
-    c.d[i] = *reinterpret_cast<const u4*>(a.base + off);
+    c.d[i] = *reinterpret_cast<const u4*>(c.dbase + c.doff[i]);
   }
 }
 
-template <int FMT, int WT, bool GATHER>
-__device__ __forceinline__ void load_x(const WgradParams& p, const Aim& a, int i, Copy<FMT, WT, GATHER>& c) {
-  const uint32_t src = (uint32_t)min(max(c.src[i], 0), (int32_t)p.x_rows - 1);
-  c.x[i] = *reinterpret_cast<const u4*>(a.codes + (uint64_t)src * (uint32_t)p.K);
-  const uint8_t* sc = a.scales + (uint64_t)src * (uint32_t)(p.K / 32);
-  if constexpr (Copy<FMT, WT, GATHER>::WORDS) c.sc[i] = *reinterpret_cast<const uint32_t*>(sc);
-  else c.sc[i] = *sc;
+template <class V>
+__device__ __forceinline__ void load_x(int i, Copy<V>& c) {
+  c.x[i] = *reinterpret_cast<const u4*>(c.xbase + c.xoff[i]);
+}
+// Scale codes: one for 32 codes, so at 1/32 of the code offset from the start
+// (sbase: of the scales at the uniform part of it).
+template <class V>
+__device__ __forceinline__ void load_sc(const WgradParams& p, int i, Copy<V>& c) {
+  const uint8_t* sbase = p.scales + (uint64_t)(c.xbase - p.codes) / 32;
+  if constexpr (V::ANY) c.sc[i] = sbase[c.xoff[i] / 32];
+  else c.sc[i] = *reinterpret_cast<const uint32_t*>(sbase + ((c.xoff[i] >> 5) & ~3u));
 }
 
 // the thread's dY chunk i into LDS
-template <int FMT, int WT, bool GATHER>
-__device__ __forceinline__ void put_d(int i, const Copy<FMT, WT, GATHER>& c) {
+template <class V>
+__device__ __forceinline__ void put_d(int i, const Copy<V>& c) {
   *(lds_u4)c.dput_of(i) = c.d[i];
 }
-
-// The thread's code chunk i on its way: scale, then pair by pair, then into
-// LDS by halves.
-template <int FMT>
+// Its code chunk i on the way: scale, pair by pair, into LDS by halves.
 struct Decoded {
-  Scale8 s;
+  float x;
   uint32_t o[8];
 };
-template <int FMT, int WT, bool GATHER>
-__device__ __forceinline__ void decode_scale(int i, const Copy<FMT, WT, GATHER>& c, Decoded<FMT>& d) {
-  typedef Copy<FMT, WT, GATHER> C;
-  d.s = scale8<FMT>(C::WORDS ? (c.sc[i] >> c.sc_shift) & 0xFFu : c.sc[i]);
+template <class V>
+__device__ __forceinline__ void decode_scale(int i, const Copy<V>& c, Decoded& d) {
+  if constexpr (V::ANY) d.x = scale8<V::FMT>(c.sc[i]);
+  else d.x = scale8_word<V::FMT>(c.sc[i], c.sc_shift);
 }
-template <int P, int FMT, int WT, bool GATHER>
-__device__ __forceinline__ void decode_pair(int i, const Copy<FMT, WT, GATHER>& c, Decoded<FMT>& d) {
-  d.o[P] = decode2_bf16<FMT, P & 1>(c.x[i][P / 2], d.s);
+template <int P, class V>
+__device__ __forceinline__ void decode_pair(int i, const Copy<V>& c, Decoded& d) {
+  d.o[P] = decode2_bf16<V::FMT, P & 1>(c.x[i][P / 2], d.x);
 }
-template <int H, int FMT, int WT, bool GATHER>
-__device__ __forceinline__ void put_x(int i, const Copy<FMT, WT, GATHER>& c, const Decoded<FMT>& d) {
-  typedef Copy<FMT, WT, GATHER> C;
-  *(lds_u4)((c.xput ^ (16u * H)) + i * C::XR * C::PITCH) = u4{d.o[4 * H], d.o[4 * H + 1], d.o[4 * H + 2], d.o[4 * H + 3]};
-}
-template <int FMT, int WT, bool GATHER>
-__device__ __forceinline__ void put_x(int i, const Copy<FMT, WT, GATHER>& c) {
-  Decoded<FMT> d;
-  decode_scale(i, c, d);
-  decode_pair<0>(i, c, d);
-  decode_pair<1>(i, c, d);
-  decode_pair<2>(i, c, d);
-  decode_pair<3>(i, c, d);
-  decode_pair<4>(i, c, d);
-  decode_pair<5>(i, c, d);
-  decode_pair<6>(i, c, d);
-  decode_pair<7>(i, c, d);
-  put_x<0>(i, c, d);
-  put_x<1>(i, c, d);
+template <int H, class V>
+__device__ __forceinline__ void put_x(int i, const Copy<V>& c, const Decoded& d) {
+  *(lds_u4)((c.xput ^ (16u * H)) + i * V::XR * V::PITCH) = u4{d.o[4 * H], d.o[4 * H + 1], d.o[4 * H + 2], d.o[4 * H + 3]};
 }
 
 // Clears the rows from `rem` on of the stage that was just written, in both
 // operands (a row that is not of the group may hold NaN).  Each thread clears
 // what it wrote itself, and a wave's LDS accesses keep their order, so no
 // barrier is needed between.
-template <int FMT, int WT, bool GATHER>
-__device__ __forceinline__ void drop_rows(int32_t rem, uint32_t tid, const Copy<FMT, WT, GATHER>& c) {
-  typedef Copy<FMT, WT, GATHER> C;
+template <class V>
+__device__ __forceinline__ void drop_rows(int32_t rem, const Copy<V>& c) {
   const u4 z = u4{0, 0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < C::DC; ++i)
-    if ((int32_t)(tid / (C::T / 8)) + i * C::DR >= rem) *(lds_u4)c.dput_of(i) = z;
+  for (int i = 0; i < V::DC; ++i)
+    if ((int32_t)c.drow + i * V::DR >= rem) *(lds_u4)c.dput_of(i) = z;
 #pragma unroll
-  for (int i = 0; i < C::XC; ++i)
-    if ((int32_t)(tid / (C::T / 16)) + i * C::XR >= rem) {
-      const uint32_t at = i * C::XR * C::PITCH;
+  for (int i = 0; i < V::XC; ++i)
+    if ((int32_t)c.xrow + i * V::XR >= rem) {
+      const uint32_t at = i * V::XR * V::PITCH;
       *(lds_u4)(c.xput + at) = z;
       *(lds_u4)((c.xput ^ 16u) + at) = z;
     }
@@ -278,22 +351,30 @@ __device__ __forceinline__ void read_frags(int q, const uint32_t (&noff)[WT / 32
 }
 
 // Writes the share W (0..3) of a stage into its buffer and issues the loads of
-// the same share of the stage after it, and of the row numbers of the one
-// after that.
-template <int W, bool ODD, int FMT, int WT, bool GATHER>
-__device__ __forceinline__ void copy_share(const WgradParams& p, const Aim& load, const Stage& src, uint32_t tid,
-                                           Copy<FMT, WT, GATHER>& c) {
-  typedef Copy<FMT, WT, GATHER> C;
+// the same share of the stage after it.
+template <int W, class V>
+__device__ __forceinline__ void copy_share(const WgradParams& p, uint32_t n0, Copy<V>& c) {
 #pragma unroll
-  for (int i = W * C::DC / 4; i < (W + 1) * C::DC / 4; ++i) {
+  for (int i = W * V::DC / 4; i < (W + 1) * V::DC / 4; ++i) {
     put_d(i, c);
-    load_d<ODD>(p, load, i, c);
+    load_d(p, n0, i, c);
   }
 #pragma unroll
-  for (int i = W * C::XC / 4; i < (W + 1) * C::XC / 4; ++i) {
-    put_x(i, c);
-    load_x(p, load, i, c);
-    load_src(p, src, tid, i, c);
+  for (int i = W * V::XC / 4; i < (W + 1) * V::XC / 4; ++i) {
+    Decoded d;
+    decode_scale(i, c, d);
+    decode_pair<0>(i, c, d);
+    decode_pair<1>(i, c, d);
+    decode_pair<2>(i, c, d);
+    decode_pair<3>(i, c, d);
+    put_x<0>(i, c, d);
+    decode_pair<4>(i, c, d);
+    decode_pair<5>(i, c, d);
+    decode_pair<6>(i, c, d);
+    decode_pair<7>(i, c, d);
+    put_x<1>(i, c, d);
+    load_x(i, c);
+    load_sc(p, i, c);
   }
 }
 
@@ -302,16 +383,14 @@ __device__ __forceinline__ void copy_share(const WgradParams& p, const Aim& load
 // share W of the copies.  With one wave on a SIMD the order is the schedule:
 // each product (32 cycles of the matrix unit) is followed by what fits beside
 // it, and nothing moves over it.
-template <int W, bool ODD, int FMT, int WT, bool GATHER, int M = 0>
-__device__ __forceinline__ void window(const WgradParams& p, const Aim& load, const Stage& src, uint32_t tid,
-                                       Copy<FMT, WT, GATHER>& c, int q, const uint32_t (&noff)[WT / 32],
-                                       const uint32_t (&koff)[WT / 32], const Frags<WT / 32>& f, Frags<WT / 32>& next,
-                                       v16f (&acc)[WT / 32][WT / 32], Decoded<FMT>& d) {
-  typedef Copy<FMT, WT, GATHER> C;
-  constexpr int F = WT / 32;
+template <int W, class V, int M = 0>
+__device__ __forceinline__ void window(const WgradParams& p, uint32_t n0, Copy<V>& c, int q,
+                                       const uint32_t (&noff)[V::F], const uint32_t (&koff)[V::F],
+                                       const Frags<V::F>& f, Frags<V::F>& next, v16f (&acc)[V::F][V::F], Decoded& d) {
+  constexpr int F = V::F;
   if constexpr (F == 2) {  // two waves on a SIMD: they fill each other's gaps
-    read_frags<WT>(q, noff, koff, next);
-    copy_share<W, ODD>(p, load, src, tid, c);
+    read_frags<V::WT>(q, noff, koff, next);
+    copy_share<W>(p, n0, c);
 #pragma unroll
     for (int i = 0; i < F; ++i)
 #pragma unroll
@@ -319,53 +398,48 @@ __device__ __forceinline__ void window(const WgradParams& p, const Aim& load, co
         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.k[i], f.n[j], acc[i][j], 0, 0, 0);
     __builtin_amdgcn_sched_barrier(0);
   } else if constexpr (M < F * F) {
-    static_assert(C::DC == 8 && C::XC == 4, "shares of two dY chunks and one code chunk");
+    static_assert(V::DC == 8 && V::XC == 4, "shares of two dY chunks and one code chunk");
     acc[M / F][M % F] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.k[M / F], f.n[M % F], acc[M / F][M % F], 0, 0, 0);
-    read_nth<M, WT>(q, noff, koff, next);
+    read_nth<M, V::WT>(q, noff, koff, next);
     if constexpr (M == 0) decode_scale(W, c, d);
     if constexpr (M >= 1 && M <= 8) decode_pair<(M - 1) & 7>(W, c, d);
     if constexpr (M == 5) put_x<0>(W, c, d);
     if constexpr (M == 9) put_x<1>(W, c, d);
     if constexpr (M == 10) put_d(2 * W, c);
     if constexpr (M == 11) put_d(2 * W + 1, c);
-    if constexpr (M == 12) load_x(p, load, W, c);
-    if constexpr (M == 13) load_d<ODD>(p, load, 2 * W, c);
-    if constexpr (M == 14) load_d<ODD>(p, load, 2 * W + 1, c);
-    if constexpr (M == 15) load_src(p, src, tid, W, c);
+    if constexpr (M == 12) load_x(W, c);
+    if constexpr (M == 13) load_sc(p, W, c);
+    if constexpr (M == 14) load_d(p, n0, 2 * W, c);
+    if constexpr (M == 15) load_d(p, n0, 2 * W + 1, c);
     __builtin_amdgcn_sched_barrier(0);
-    window<W, ODD, FMT, WT, GATHER, M + 1>(p, load, src, tid, c, q, noff, koff, f, next, acc, d);
+    window<W, V, M + 1>(p, n0, c, q, noff, koff, f, next, acc, d);
   }
-}
-
-// 8 columns of a row of dW
-template <int WDT>
-__device__ __forceinline__ void put_row(const WgradParams& p, int64_t off, float (&o)[8]) {
-  if (p.accumulate) {
-    float old[8];
-    load_n<WDT>(p.dw, off, 8, p.vec, old);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] += old[e];
-  }
-  store_n<WDT>(p.dw, off, 8, p.vec, o);
 }
 
 // A wave's tile of products, 32 columns of N at a time and PC of K, through
-// 4 x 32 x PC bytes of LDS of its own into rows of dW (or, past an edge or
-// unaligned, element by element).  Chunk c of 4 columns of row r lies at chunk
-// c ^ (r mod chunks): writes of 16 rows and reads of one row are free of
-// conflicts.
-template <int WT>
-__device__ __forceinline__ void store_tile_rows(const WgradParams& p, const Stage& s, uint32_t wn, uint32_t wk, uint32_t lane,
-                                       const v16f (&acc)[WT / 32][WT / 32], uint8_t* scratch) {
-  constexpr int PC = WT / 2;       // columns of a pass
-  constexpr int CH = PC / 4;       // 16-byte chunks of a scratch row
-  constexpr int RPI = 64 / (CH / 2);  // rows read at once, 8 columns a lane
+// 128 PC bytes of LDS of its own into rows of dW.  Chunk c of 4 columns of row
+// r lies at chunk c ^ (r mod chunks): writes of 16 rows and reads of one row
+// are free of conflicts.  PLAIN: the tile lies inside dW, whose rows are
+// 16-byte aligned, and is not added to; otherwise chunk by chunk with checks.
+template <int WDT, bool PLAIN, class V>
+__device__ __forceinline__ void store_tile(const WgradParams& p, const Unit& u, uint32_t wn, uint32_t wk, uint32_t lane,
+                                           const v16f (&acc)[V::F][V::F], uint32_t scratch) {
+  constexpr int PC = V::WT / 2;                // columns of a pass
+  constexpr int CH = PC / 4;                   // 16-byte chunks of a scratch row
+  constexpr int CPL = WDT == DT_F32 ? 1 : 2;   // chunks a lane stores
+  constexpr int EB = WDT == DT_F32 ? 4 : 2;
+  constexpr int RPI = 64 / (CH / CPL);         // rows stored at once
+  typedef __attribute__((address_space(3))) f4* lds_f4;
   // (opaque, so that the addresses below are not kept over the main loop)
   asm volatile("" : "+v"(lane));
   const uint32_t lr = lane & 31u, lg = lane >> 5;
-  const uint32_t rr = lane / (CH / 2), cc = lane % (CH / 2) * 2;
+  const uint32_t rr = lane / (CH / CPL), cc = lane % (CH / CPL) * CPL;
+  const uint32_t wbase = scratch + lr * (PC * 4), wx = lg ^ (lr & (CH - 1));
+  uint8_t* base = static_cast<uint8_t*>(p.dw) +
+                  (((int64_t)u.e * p.N + u.n0 + wn) * p.ld_dw + u.k0 + wk) * EB;  // uniform
+  const int64_t loff = ((int64_t)rr * p.ld_dw + 4 * cc) * EB;
 #pragma unroll
-  for (int j = 0; j < WT / 32; ++j)
+  for (int j = 0; j < V::F; ++j)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -373,93 +447,50 @@ __device__ __forceinline__ void store_tile_rows(const WgradParams& p, const Stag
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const v16f& a = acc[h * (PC / 32) + i2][j];
-          const uint32_t ch = 8 * i2 + 2 * v + lg;
-          *reinterpret_cast<f4*>(scratch + lr * (PC * 4) + 16u * (ch ^ (lr & (CH - 1)))) =
-              f4{a[4 * v], a[4 * v + 1], a[4 * v + 2], a[4 * v + 3]};
+          *(lds_f4)(wbase + 16u * (wx ^ (uint32_t)(8 * i2 + 2 * v))) = f4{a[4 * v], a[4 * v + 1], a[4 * v + 2], a[4 * v + 3]};
         }
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
       for (int t = 0; t < 32 / RPI; ++t) {
         const uint32_t r = t * RPI + rr;
-        const f4 lo = *reinterpret_cast<const f4*>(scratch + r * (PC * 4) + 16u * (cc ^ (r & (CH - 1))));
-        const f4 hi = *reinterpret_cast<const f4*>(scratch + r * (PC * 4) + 16u * ((cc + 1) ^ (r & (CH - 1))));
-        const int64_t n = (int64_t)s.n0 + wn + 32 * j + r, k = (int64_t)s.k0 + wk + PC * h + 4 * cc;
-        if (n < p.N && k < p.K) {  // (K is a multiple of 32: a chunk is inside or outside)
-          const int64_t off = ((int64_t)s.e * p.N + n) * p.ld_dw + k;
-          float o[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-          if (p.f32) put_row<DT_F32>(p, off, o);
-          else put_row<DT_BF16>(p, off, o);
+        float o[4 * CPL];
+#pragma unroll
+        for (int k = 0; k < CPL; ++k) {
+          const f4 x = *(lds_f4)(scratch + r * (PC * 4) + 16u * ((cc + k) ^ (r & (CH - 1))));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[4 * k + e] = x[e];
+        }
+        uint8_t* at = base + ((int64_t)(32 * j + t * RPI) * p.ld_dw + PC * h) * EB + loff;
+        if constexpr (PLAIN) {
+          if constexpr (WDT == DT_F32) *reinterpret_cast<f4*>(at) = f4{o[0], o[1], o[2], o[3]};
+          else *reinterpret_cast<u4*>(at) = u4{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
+                                              pack_bf16(o[6], o[7])};
+        } else {
+          // (K is a multiple of 32: a lane's columns are all inside or outside)
+          const bool in = (int64_t)u.n0 + wn + 32 * j + r < p.N && (int64_t)u.k0 + wk + PC * h + 4 * cc < p.K;
+          if (in) {
+#pragma unroll
+            for (int e = 0; e < 4 * CPL; ++e) {
+              if (p.accumulate) o[e] += load1<WDT>(at, e);
+              store1<WDT>(at, e, o[e]);
+            }
+          }
         }
       }
       __builtin_amdgcn_wave_barrier();
     }
 }
 
-// The workgroup's tiles, as a sequence of stages.  Units id, id + gridDim.x,
-// ...: the tiles of a group are dealt to the 8 XCDs (workgroup id mod 8) in
-// runs, n fastest, so that the workgroups of an XCD share rows of dY and X in
-// its L2.  A group without rows is passed over; its tiles of dW are cleared on
-// the way.
-template <int T>
-__device__ __forceinline__ void clear_tile(const WgradParams& p, uint32_t e, uint32_t n0, uint32_t k0) {
-  for (uint32_t q = threadIdx.x; q < T * T; q += 256) {
-    const int64_t n = (int64_t)n0 + q / T, k = (int64_t)k0 + q % T;
-    if (n < p.N && k < p.K) {
-      const int64_t off = (e * p.N + n) * p.ld_dw + k;
-      if (p.f32) static_cast<float*>(p.dw)[off] = 0.0f;
-      else static_cast<uint16_t*>(p.dw)[off] = 0;
-    }
-  }
-}
-// the first stage of unit `id` or of the next one that has rows; if there is
-// none, s stays (what is still copied of it is never used) with e = -1
-template <int T>
-__device__ __forceinline__ void seek(const WgradParams& p, uint32_t& id, Stage& s) {
-  const uint32_t tiles = p.tn * p.tk, per = (tiles + 7) / 8;
-  for (; id < p.units; id += gridDim.x) {
-    const uint32_t slot = id >> 3, e = slot / per;
-    const uint32_t in = (id & 7u) * per + (slot - e * per);
-    if (in >= tiles) continue;
-    int64_t lo = 0, hi = p.R;
-    if (p.offsets) {  // clamped into [0, R]
-      lo = p.offsets[e];
-      hi = p.offsets[e + 1];
-      lo = lo < 0 ? 0 : (lo > p.R ? p.R : lo);
-      hi = hi < lo ? lo : (hi > p.R ? p.R : hi);
-    }
-    const uint32_t tk = in / p.tn, n0 = (in - tk * p.tn) * T, k0 = tk * T;
-    if (hi > lo) {
-      s = {(int32_t)lo, (int32_t)(hi - lo), n0, k0, (int32_t)e};
-      return;
-    }
-    if (!p.accumulate) clear_tile<T>(p, e, n0, k0);
-  }
-  s.e = -1;
-}
-template <int T>
-__device__ __forceinline__ void advance(const WgradParams& p, uint32_t& id, Stage& s) {
-  if (s.rem > kStep) {
-    s.row += kStep;
-    s.rem -= kStep;
-  } else if (s.e >= 0) {
-    id += gridDim.x;
-    seek<T>(p, id, s);
-  }
-}
-
 // Stages flow through the pipeline without a break between tiles: while a
 // tile's last products run, the next tile's first stages are being copied.
-template <int FMT, int WT, bool ODD, bool GATHER>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WT == 128 ? 1 : 2, WT == 128 ? 1 : 2))) void
+// The workgroup's LDS is addressed by plain offsets from its start (there is no
+// static allocation), so that changing buffers is one exclusive or.
+template <class V>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(V::WT == 128 ? 1 : 2, V::WT == 128 ? 1 : 2))) void
 k_wgrad(WgradParams p) {
-  typedef Copy<FMT, WT, GATHER> C;
-  constexpr int F = WT / 32, T = C::T;
-  // The workgroup's LDS is addressed by plain offsets from its start (there is
-  // no static allocation), so that changing buffers is one exclusive or.
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  constexpr int F = V::F, T = V::T;
   const uint32_t tid = threadIdx.x, lane = tid & 63u, wid = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const uint32_t wn = (wid >> 1) * WT, wk = (wid & 1u) * WT;
-  uint8_t* scratch = smem + 4 * C::HALF + wid * (64 * WT);
+  const uint32_t wn = (wid >> 1) * V::WT, wk = (wid & 1u) * V::WT;
 
   // fragment addresses: 16 lanes read 4 rows x 16 columns
   uint32_t noff[F], koff[F];
@@ -469,48 +500,54 @@ k_wgrad(WgradParams p) {
 #pragma unroll
     for (int i = 0; i < F; ++i) {
       const uint32_t col = 32 * i + 16 * (gr & 1) + 4 * (s & 3);
-      noff[i] = row * C::PITCH + 16u * place<T>(row, (wn + col) / 8) + 8 * (s & 1);
-      koff[i] = C::HALF + row * C::PITCH + 16u * place<T>(row, (wk + col) / 8) + 8 * (s & 1);
+      noff[i] = row * V::PITCH + 16u * place<T>(row, (wn + col) / 8) + 8 * (s & 1);
+      koff[i] = V::HALF + row * V::PITCH + 16u * place<T>(row, (wk + col) / 8) + 8 * (s & 1);
     }
   }
 
   uint32_t id = blockIdx.x;
-  Stage s0 = {0, 0, 0, 0, 0};  // the stage being multiplied; s1 .. s4 follow it
-  seek<T>(p, id, s0);
-  if (s0.e < 0) return;
-  Stage s1 = s0;
-  advance<T>(p, id, s1);
-  Stage s2 = s1;
-  advance<T>(p, id, s2);
-  Stage s3 = s2;
-  advance<T>(p, id, s3);
-  Stage s4 = s3;
-  advance<T>(p, id, s4);
+  Unit tile = seek<V>(p, id);  // whose products run
+  if (tile.e < 0) return;
+  Unit next = {0, 0, -1, 0, 1};  // the one after it, once the row cursor has come to it
+  Cursor rows, load, put;        // the stages whose row numbers are loaded, that are loaded, that are written
+  rows.start(tile);
+  load.start(tile);
+  put.start(tile);
+  int32_t left = put.left;
+  uint32_t n0 = tile.n0;  // of the tile that is loaded
 
-  C c;
+  Copy<V> c;
   c.init(tid);
+  load_rows(p, rows, lane, c);
+  aim(p, tile, load, true, c);
 #pragma unroll
-  for (int i = 0; i < C::XC; ++i) load_src(p, s0, tid, i, c);
-  {
-    const Aim a0 = aim(p, s0, tid, c), a1 = aim(p, s1, tid, c);
+  for (int i = 0; i < V::DC; ++i) load_d(p, n0, i, c);
 #pragma unroll
-    for (int i = 0; i < C::DC; ++i) load_d<ODD>(p, a0, i, c);
-#pragma unroll
-    for (int i = 0; i < C::XC; ++i) load_x(p, a0, i, c);
-#pragma unroll
-    for (int i = 0; i < C::XC; ++i) load_src(p, s1, tid, i, c);
-    copy_share<0, ODD>(p, a1, s2, tid, c);
-    copy_share<1, ODD>(p, a1, s2, tid, c);
-    copy_share<2, ODD>(p, a1, s2, tid, c);
-    copy_share<3, ODD>(p, a1, s2, tid, c);
+  for (int i = 0; i < V::XC; ++i) {
+    load_x(i, c);
+    load_sc(p, i, c);
   }
-  if (s0.rem < kStep) drop_rows(s0.rem, tid, c);
+  // (a tile has at least 3 stages: no cursor leaves it here)
+  rows.step(next);
+  load_rows(p, rows, lane, c);
+  load.step(next);
+  aim(p, tile, load, false, c);
+  copy_share<0>(p, n0, c);
+  copy_share<1>(p, n0, c);
+  copy_share<2>(p, n0, c);
+  copy_share<3>(p, n0, c);
+  if (put.rem < kStep) drop_rows(put.rem, c);
+  int32_t put_rem = put.rem - kStep;  // rows of the stage that is written; none in stages beyond the rows
+  --put.left;
+  rows.step(next);
+  load_rows(p, rows, lane, c);
+  load.step(next);
+  aim(p, tile, load, false, c);
   stage_barrier();
   Frags<F> f[2];
-  read_frags<WT>(0, noff, koff, f[0]);
+  read_frags<V::WT>(0, noff, koff, f[0]);
   c.flip();
-  Aim a = aim(p, s2, tid, c);  // of the stage after the one that is written
-  copy_share<3, ODD>(p, a, s3, tid, c);
+  copy_share<3>(p, n0, c);
 
   for (;;) {  // tiles
     v16f acc[F][F];
@@ -520,44 +557,57 @@ k_wgrad(WgradParams p) {
       for (int j = 0; j < F; ++j)
 #pragma unroll
         for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-    const Stage tile = s0;
-    bool last, end;
     // Windows of 16 rows.  While a window's products run, the next window's
-    // fragments are read and a quarter of a later stage is written.  The barrier
-    // comes before the last window, when its fragments are in registers: behind
-    // it the stage is free to be overwritten and the next one is complete.
-    Decoded<FMT> d;
+    // fragments are read and a quarter of a later stage is written.  The
+    // barrier comes before the last window, when its fragments are in
+    // registers: behind it the stage is free to be overwritten and the next
+    // one is complete.
+    Decoded d;
     do {
-      window<0, ODD>(p, a, s3, tid, c, 1, noff, koff, f[0], f[1], acc, d);
-      window<1, ODD>(p, a, s3, tid, c, 2, noff, koff, f[1], f[0], acc, d);
-      window<2, ODD>(p, a, s3, tid, c, 3, noff, koff, f[0], f[1], acc, d);
-      if (s1.rem < kStep) drop_rows(s1.rem, tid, c);
-      // the other buffer is read from here on, and this one written
-      a = aim(p, s3, tid, c);
-      c.flip();
+      if (rows.left == 1) {  // the row cursor leaves its tile
+        id += gridDim.x;
+        next = seek<V>(p, id);
+      }
+      rows.step(next);
+      load_rows(p, rows, lane, c);
+      window<0>(p, n0, c, 1, noff, koff, f[0], f[1], acc, d);
+      window<1>(p, n0, c, 2, noff, koff, f[1], f[0], acc, d);
+      window<2>(p, n0, c, 3, noff, koff, f[0], f[1], acc, d);
+      if (put_rem < kStep) drop_rows(put_rem, c);
+      put_rem -= kStep;
+      if (--put.left == 0) {
+        put_rem = next.cnt;
+        put.left = next.e >= 0 ? next.stages() : INT32_MAX;
+      }
+      const bool fresh = load.step(next);
+      if (fresh) n0 = next.n0;
+      aim(p, fresh ? next : tile, load, fresh, c);
+      c.flip();  // the other buffer is read from here on, and this one written
 #pragma unroll
       for (int i = 0; i < F; ++i) {
-        noff[i] ^= 2 * C::HALF;
-        koff[i] ^= 2 * C::HALF;
+        noff[i] ^= 2 * V::HALF;
+        koff[i] ^= 2 * V::HALF;
       }
       stage_barrier();
-      window<3, ODD>(p, a, s4, tid, c, 0, noff, koff, f[1], f[0], acc, d);
-      last = s0.rem <= kStep;
-      end = s1.e < 0;
-      s0 = s1;
-      s1 = s2;
-      s2 = s3;
-      s3 = s4;
-      advance<T>(p, id, s4);
-    } while (!last);
-    store_tile_rows<WT>(p, tile, wn, wk, lane, acc, scratch);
-    if (end) break;
+      window<3>(p, n0, c, 0, noff, koff, f[1], f[0], acc, d);
+    } while (--left != 0);
+    const bool inside = p.vec && !p.accumulate && (int64_t)tile.n0 + T <= p.N && (int64_t)tile.k0 + T <= p.K;
+    const uint32_t scratch = 4 * V::HALF + wid * V::SCRATCH;
+    if (p.f32) {
+      if (inside) store_tile<DT_F32, true, V>(p, tile, wn, wk, lane, acc, scratch);
+      else store_tile<DT_F32, false, V>(p, tile, wn, wk, lane, acc, scratch);
+    } else {
+      if (inside) store_tile<DT_BF16, true, V>(p, tile, wn, wk, lane, acc, scratch);
+      else store_tile<DT_BF16, false, V>(p, tile, wn, wk, lane, acc, scratch);
+    }
+    if (next.e < 0) break;
+    tile = next;
+    left = tile.stages();
   }
 }
 
-template <int FMT, int WT, bool ODD, bool GATHER>
-hipError_t launch_t(const WgradArgs& a, hipStream_t s) {
-  typedef Copy<FMT, WT, GATHER> C;
+template <class V>
+hipError_t launch_v(const WgradArgs& a, hipStream_t s) {
   WgradParams p = {};
   p.dy = a.dy;
   p.ld_dy = a.ld_dy;
@@ -572,16 +622,15 @@ hipError_t launch_t(const WgradArgs& a, hipStream_t s) {
   p.groups = a.groups;
   p.dw = a.dw;
   p.ld_dw = a.ld_dw;
-  p.tn = (uint32_t)((a.N + C::T - 1) / C::T);
-  p.tk = (uint32_t)((a.K + C::T - 1) / C::T);
+  p.tn = (uint32_t)((a.N + V::T - 1) / V::T);
+  p.tk = (uint32_t)((a.K + V::T - 1) / V::T);
   p.f32 = a.dwdt == DT_F32;
   p.accumulate = a.accumulate;
   p.vec = (reinterpret_cast<uintptr_t>(a.dw) & 15u) == 0 && (a.ld_dw * (p.f32 ? 4 : 2)) % 16 == 0;
   const int64_t units = ((int64_t)p.tn * p.tk + 7) / 8 * 8 * a.groups;
   if (units > UINT32_MAX / 2) return hipErrorInvalidValue;
   p.units = (uint32_t)units;
-  constexpr int smem = 4 * C::HALF + 4 * 64 * WT;  // two stages, and 64 WT bytes of scratch a wave
-  auto kern = k_wgrad<FMT, WT, ODD, GATHER>;
+  auto kern = k_wgrad<V>;
   // the dynamic LDS limit is raised once per device
   static std::atomic<uint64_t> attr_done{0};
   int dev = 0;
@@ -589,24 +638,24 @@ hipError_t launch_t(const WgradArgs& a, hipStream_t s) {
   if (e != hipSuccess) return e;
   const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
   if (!bit || !(attr_done.load(std::memory_order_acquire) & bit)) {
-    e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, V::LDS);
     if (e != hipSuccess) return e;
     attr_done.fetch_or(bit, std::memory_order_acq_rel);
   }
   // as many workgroups as the 256 CUs hold at once
-  const uint32_t most = WT == 128 ? 256 : 512;
-  hipLaunchKernelGGL(kern, dim3(p.units < most ? p.units : most), dim3(256), smem, s, p);
+  const uint32_t most = V::WT == 128 ? 256 : 512;
+  hipLaunchKernelGGL(kern, dim3(p.units < most ? p.units : most), dim3(256), V::LDS, s, p);
   return hipGetLastError();
 }
 
 template <int FMT, bool GATHER>
 hipError_t launch_g(const WgradArgs& a, hipStream_t s) {
-  // dY rows that end inside a 16-byte chunk (or of a pitch past 32-bit
-  // offsets) are loaded element by element
-  if (a.N % 8 || a.ld_dy >= (1 << 24)) return launch_t<FMT, 64, true, GATHER>(a, s);
+  if (a.N % 8 || a.ld_dy >= (1 << 24) || a.K % 128 || a.x_rows * a.K >= (int64_t)UINT32_MAX)
+    return launch_v<Variant<FMT, 64, true, GATHER>>(a, s);
   // 256 x 256 tiles when they fill the CUs, else 128 x 128
   const int64_t big = ((a.N + 255) / 256) * ((a.K + 255) / 256) * a.groups;
-  return big >= 256 && a.K % 128 == 0 ? launch_t<FMT, 128, false, GATHER>(a, s) : launch_t<FMT, 64, false, GATHER>(a, s);
+  return big >= 256 ? launch_v<Variant<FMT, 128, false, GATHER>>(a, s)
+                    : launch_v<Variant<FMT, 64, false, GATHER>>(a, s);
 }
 
 template <int FMT>
