@@ -44,6 +44,9 @@ __device__ inline void decode4_f32(uint32_t w, float X, float* v) {
 template <int FMT, int H>
 __device__ inline uint32_t decode2_bf16(uint32_t w, float x) {
   if constexpr (FMT == FMT_MXINT8) {
+    // (opaque: of a word whose every use is a byte the compiler would keep the
+    // bytes, and take them apart as soon as the word is loaded)
+    asm("" : "+v"(w));
     return pack_bf16((float)(int8_t)(uint8_t)(w >> (16 * H)) * x, (float)(int8_t)(uint8_t)(w >> (16 * H + 8)) * x);
   } else if constexpr (FMT == FMT_MXFP8) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, x, H != 0));
@@ -53,7 +56,10 @@ __device__ inline uint32_t decode2_bf16(uint32_t w, float x) {
 }
 template <int FMT>
 __device__ inline float scale8(uint32_t sc) {
-  if constexpr (FMT == FMT_MXINT8) return e8m0_value(sc) * 0.015625f;
+  if constexpr (FMT == FMT_MXINT8) {
+    const float x = __builtin_amdgcn_ldexpf(0.015625f, (int)sc - 127);
+    return sc == 0xFFu ? __builtin_nanf("") : x;
+  }
   else return u2f(sc << 23);
 }
 // the same from byte `shift` / 8 of a word: for FP8 one rotation puts it into
