@@ -17,6 +17,13 @@
 // nothing, adds nothing to S and gets a zero gradient.
 //
 // A group of G lanes holds one token's scores, VPL consecutive ones a lane.
+// Selection works on integer keys of 31 bits or fewer, the score's bits in
+// increasing order above the complement of the expert's number, so keys are
+// distinct and equal scores come out by lower index: the next key is the
+// largest of key - last as an unsigned number (keys not below `last` give less
+// than 2^31, the others more), one subtraction and half a max3 a score.  A BF16
+// score fits whole.  Of an FP32 score the upper 21 bits do; where two of the
+// topk + 1 largest agree in those, the wave selects by comparing scores.
 // The sort needs no atomics whose order matters: within 64 tokens an expert's
 // tokens are the bits of one 64-bit word, so a token's rank is a population
 // count, and the blocks of tokens are put in order by their counts.  S is
@@ -29,8 +36,9 @@ namespace mxk {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWaves = kThreads / 64;
+// threads of a workgroup, for EP experts (padded): one pass over 64 tokens
+// while the sums of its waves fit in LDS
+constexpr int threads_for(int EP) { return EP <= 256 ? 1024 : 512; }
 constexpr int kSub = 64;     // tokens of one bit word
 constexpr int kMaxK = 16;    // slots of a token
 constexpr int64_t kMaxBlocks = 256;
@@ -45,6 +53,7 @@ struct RouteParams {
   int32_t vec;      // rows allow vector loads
   int32_t per;      // tokens of one block (a multiple of kSub)
   int32_t blocks;
+  int32_t pitch;    // experts, rounded up to 8: of the workspace's rows
   int32_t* experts_out;
   float* weights;
   int32_t* slot_row;
@@ -54,7 +63,7 @@ struct RouteParams {
   int64_t* valid;
   float* prob_sum;
   float* loss;
-  // workspace (blocks > 1): counts [blocks][E], sums of p [blocks][E], valid tokens [blocks]
+  // workspace (blocks > 1): counts [blocks][pitch], sums of p [blocks][pitch], valid tokens [blocks]
   uint16_t* part_counts;
   float* part_sums;
   int32_t* part_valid;
@@ -122,130 +131,159 @@ __device__ inline void load_scores(const RouteParams& p, int64_t t, int e0, floa
 
 template <int EP>
 struct RouteShared {
+  static constexpr int kThreads = threads_for(EP), kWaves = kThreads / 64;
   uint64_t mask[EP];          // tokens of the current 64 that chose the expert
   int32_t run[EP];            // tokens before them in the block that did; then the sort's bases
   int32_t total[EP];
   float sums[kWaves][EP];
   int32_t idx[kSub][kMaxK];   // chosen experts, -1 for none
-  float val[kSub][kMaxK];     // their scores
-  float top[kSub], inv[kSub]; // row maximum, 1 / sum of exp
   int32_t valid;
 };
 
-// Tokens [t0, t1) of one block: experts, weights, and in slot_row the rank of
-// each slot among the block's tokens of its expert.  Leaves the block's
-// counts in sh.run, its sums of p in sh.sums[0] and its valid tokens in
-// sh.valid.
+__device__ inline uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+template <int G>
+__device__ inline uint32_t group_umax(uint32_t v) {
+  v = umax(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
+  v = umax(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));
+  v = umax(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));
+  v = umax(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));
+  if constexpr (G == 64) {
+    v = umax(v, lane_read(v, lane_id() ^ 16u));
+    v = umax(v, lane_read(v, lane_id() ^ 32u));
+  }
+  return v;
+}
+
+// key of score x of expert e; 0: never chosen (-inf, NaN)
+template <int DT>
+__device__ inline uint32_t key_of(float x, int e) {
+  const uint32_t b = f2u(x + 0.0f);  // (-0 and 0 are equal)
+  const uint32_t ord = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+  const uint32_t k = (DT == DT_BF16 ? (ord >> 16) << 10 : (ord >> 11) << 10) | (uint32_t)(1023 - e);
+  return x > -__builtin_inff() ? k : 0u;
+}
+
+// The topk largest scores of each group's token: lane j of the group gets the
+// expert of slot j (-1 where there is none) and its score.
 template <int DT, int G, int VPL>
-__device__ inline void choose(const RouteParams& p, int t0, int t1, RouteShared<G * VPL>& sh) {
-  constexpr int EP = G * VPL;
+__device__ inline int select(const RouteParams& p, int64_t t, const float (&x)[VPL], int e0, int gl, float* score) {
+  const int topk = p.topk;
+  uint32_t key[VPL];
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) key[v] = key_of<DT>(x[v], e0 + v);
+  uint32_t last = 0x80000000u, mine = 0;
+  bool unsure = false;
+  const int n = DT == DT_BF16 ? topk : topk + 1;
+  for (int j = 0; j < n; ++j) {
+    uint32_t m = key[0] - last;
+#pragma unroll
+    for (int v = 1; v < VPL; ++v) m = umax(m, key[v] - last);
+    m = group_umax<G>(m);
+    // none left: the keys below `last` are 0 (or `last` is 0 itself)
+    const uint32_t nx = last == 0 ? 0u : last + m;
+    if constexpr (DT == DT_F32) unsure = unsure || (nx != 0 && (nx ^ last) < 1024u);
+    mine = gl == j ? nx : mine;
+    last = nx;
+  }
+  int at = mine && gl < topk ? 1023 - (int)(mine & 1023u) : -1;
+  if constexpr (DT == DT_F32) {
+    if (__ballot(unsure)) {
+      float y[VPL];
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) y[v] = x[v] > -__builtin_inff() ? x[v] : -__builtin_inff();
+      at = -1;
+      for (int j = 0; j < topk; ++j) {
+        float m = y[0];
+#pragma unroll
+        for (int v = 1; v < VPL; ++v) m = __builtin_fmaxf(m, y[v]);
+        m = group_reduce<G>(m, OpMax());
+        int w = 1 << 20;  // the first of this lane's that has it
+#pragma unroll
+        for (int v = VPL - 1; v >= 0; --v) w = y[v] == m ? e0 + v : w;
+        if (!(m > -__builtin_inff())) w = 1 << 20;
+        w = (1 << 20) - (int)group_umax<G>((uint32_t)((1 << 20) - w));  // the lowest of the group's
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) y[v] = w == e0 + v ? -__builtin_inff() : y[v];
+        at = gl == j ? (w < (1 << 20) ? w : -1) : at;
+      }
+    }
+    *score = at >= 0 ? load1<DT>(p.logits, t * p.ld + at) : 0.0f;
+  } else {
+    const uint32_t ord = mine >> 10;  // the whole score
+    *score = at >= 0 ? u2f((ord ^ (ord & 0x8000u ? 0x8000u : 0xFFFFu)) << 16) : 0.0f;
+  }
+  return at;
+}
+
+// 64 tokens from s0 on (those below t1): experts and weights, each expert's
+// bit word, the lanes' sums of p.
+template <int DT, int G, int VPL>
+__device__ inline void choose_64(const RouteParams& p, int s0, int t1, RouteShared<G * VPL>& sh, float (&sum_p)[VPL]) {
+  constexpr int kWaves = threads_for(G * VPL) / 64;
   constexpr int TPI = 64 / G;  // tokens a wave handles at once
-  const int tid = threadIdx.x;
-  const int lane = tid & 63, wave = tid >> 6, gl = lane & (G - 1), grp = lane / G;
+  constexpr int ITS = kSub / kWaves / TPI;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, gl = lane & (G - 1), grp = lane / G;
   const int e0 = gl * VPL;
-  for (int e = tid; e < EP; e += kThreads) {
-    sh.mask[e] = 0;
-    sh.run[e] = 0;
+  int n_valid = 0;
+  float x[2][VPL];
+  bool ok[2];
+  const auto load = [&](int it, float (&y)[VPL], bool& in) {
+    const int t = s0 + wave * (kSub / kWaves) + it * TPI + grp;
+    in = t < t1 && (!p.mask || p.mask[t] != 0);
+    if (in) {
+      load_scores<DT, VPL>(p, t, e0, y);
+    } else {
+#pragma unroll
+      for (int v = 0; v < VPL; ++v) y[v] = -__builtin_inff();
+    }
+  };
+  load(0, x[0], ok[0]);
+#pragma unroll 2
+  for (int it = 0; it < ITS; ++it) {
+    if (it + 1 < ITS) load(it + 1, x[(it + 1) & 1], ok[(it + 1) & 1]);
+    float(&y)[VPL] = x[it & 1];
+    const int lt = wave * (kSub / kWaves) + it * TPI + grp, t = s0 + lt;
+    float m = y[0];
+#pragma unroll
+    for (int v = 1; v < VPL; ++v) m = __builtin_fmaxf(m, y[v]);
+    m = group_reduce<G>(__builtin_fmaxf(m, -__builtin_inff()), OpMax());
+    const float base = m == -__builtin_inff() ? 0.0f : m;
+    float xe;
+    const int e = select<DT, G, VPL>(p, t, y, e0, gl, &xe);
+    float s = 0.0f;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) {
+      y[v] = __builtin_amdgcn_exp2f((y[v] - base) * kLog2e);
+      s += y[v];
+    }
+    s = group_reduce<G>(s, OpAdd());
+    const float inv = s == 0.0f ? 0.0f : 1.0f / s;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) sum_p[v] += y[v] * inv;
+    float w = e >= 0 ? __builtin_amdgcn_exp2f((xe - base) * kLog2e) : 0.0f;
+    if (p.normalize) {
+      const float sw = group_reduce<G>(w, OpAdd());
+      w = e < 0 ? 0.0f : inv == inv ? w / sw : inv;  // a NaN anywhere in the row shows in its weights
+    } else {
+      w = e < 0 ? 0.0f : w * inv;
+    }
+    if (gl == 0) n_valid += ok[it & 1] ? 1 : 0;
+    if (gl < p.topk && t < t1) {
+      sh.idx[lt][gl] = e;
+      p.experts_out[(int64_t)t * p.topk + gl] = e;
+      p.weights[(int64_t)t * p.topk + gl] = w;
+      if (e >= 0) atomicOr(reinterpret_cast<unsigned long long*>(&sh.mask[e]), 1ull << lt);
+    }
   }
-  if (tid == 0) sh.valid = 0;
-  float sum_p[VPL] = {};
-  __syncthreads();
-  for (int s0 = t0; s0 < t1; s0 += kSub) {
-    int n_valid = 0;
-#pragma unroll 1
-    for (int it = 0; it < kSub / kWaves; it += TPI) {
-      const int lt = wave * (kSub / kWaves) + it + grp;  // token within the 64
-      const int t = s0 + lt;
-      const bool ok = t < t1 && (!p.mask || p.mask[t] != 0);
-      float x[VPL];
-      if (ok) {
-        load_scores<DT, VPL>(p, t, e0, x);
-      } else {
-#pragma unroll
-        for (int v = 0; v < VPL; ++v) x[v] = -__builtin_inff();
-      }
-      float m = x[0];
-#pragma unroll
-      for (int v = 1; v < VPL; ++v) m = __builtin_fmaxf(m, x[v]);
-      m = group_reduce<G>(__builtin_fmaxf(m, -__builtin_inff()), OpMax());
-      const float base = m == -__builtin_inff() ? 0.0f : m;
-      float ex[VPL], s = 0.0f;
-#pragma unroll
-      for (int v = 0; v < VPL; ++v) {
-        ex[v] = __builtin_amdgcn_exp2f((x[v] - base) * kLog2e);
-        s += ex[v];
-      }
-      s = group_reduce<G>(s, OpAdd());
-      const float inv = s == 0.0f ? 0.0f : 1.0f / s;
-#pragma unroll
-      for (int v = 0; v < VPL; ++v) sum_p[v] += ex[v] * inv;
-      if (gl == 0) {
-        sh.top[lt] = base;
-        sh.inv[lt] = inv;
-        n_valid += ok ? 1 : 0;
-      }
-      // k times the largest that is left
-      for (int j = 0; j < p.topk; ++j) {
-        float lm = x[0];
-#pragma unroll
-        for (int v = 1; v < VPL; ++v) lm = __builtin_fmaxf(lm, x[v]);
-        lm = __builtin_fmaxf(lm, -__builtin_inff());  // a lane of NaNs has nothing to offer
-        const float gm = j == 0 ? m : group_reduce<G>(lm, OpMax());
-        const uint64_t have = __ballot(lm == gm && gm > -__builtin_inff());
-        const uint64_t mine = G == 64 ? have : (have >> (grp * G)) & ((1ull << (G & 63)) - 1);
-        const int owner = mine ? __builtin_ctzll(mine) : 0;
-        if (gl == owner) {
-          int at = -1;
-          if (mine) {
-            bool open = true;
-#pragma unroll
-            for (int v = 0; v < VPL; ++v) {
-              const bool hit = open && x[v] == gm;
-              at = hit ? e0 + v : at;
-              x[v] = hit ? -__builtin_inff() : x[v];
-              open = open && !hit;
-            }
-            atomicOr(reinterpret_cast<unsigned long long*>(&sh.mask[at]), 1ull << lt);
-          }
-          sh.idx[lt][j] = at;
-          sh.val[lt][j] = gm;
-        }
-      }
-    }
-    if (n_valid) atomicAdd(&sh.valid, n_valid);
-    __syncthreads();
-    for (int i = tid; i < kSub * p.topk; i += kThreads) {
-      const int lt = i / p.topk, j = i - lt * p.topk, t = s0 + lt;
-      if (t >= t1) break;
-      const int e = sh.idx[lt][j];
-      float w = 0.0f;
-      int rank = -1;
-      if (e >= 0) {
-        const float base = sh.top[lt], inv = sh.inv[lt];
-        w = __builtin_amdgcn_exp2f((sh.val[lt][j] - base) * kLog2e);
-        if (p.normalize) {
-          float s = 0.0f;
-          for (int i2 = 0; i2 < p.topk; ++i2)
-            if (sh.idx[lt][i2] >= 0) s += __builtin_amdgcn_exp2f((sh.val[lt][i2] - base) * kLog2e);
-          w = inv == inv ? w / s : inv;  // a NaN anywhere in the row shows in its weights
-        } else {
-          w *= inv;
-        }
-        rank = sh.run[e] + __popcll(sh.mask[e] & ((1ull << lt) - 1));
-      }
-      const int64_t o = (int64_t)t * p.topk + j;
-      p.experts_out[o] = e;
-      p.weights[o] = w;
-      p.slot_row[o] = rank;
-    }
-    __syncthreads();
-    for (int e = tid; e < EP; e += kThreads) {
-      sh.run[e] += __popcll(sh.mask[e]);
-      sh.mask[e] = 0;
-    }
-    __syncthreads();
-  }
-  // sums of p: over the groups of a wave, then over the waves
+  if (n_valid) atomicAdd(&sh.valid, n_valid);
+}
+
+// The block's sums of p into sh.sums[0]: over the groups of a wave, then over
+// the waves.
+template <int G, int VPL>
+__device__ inline void reduce_sums(RouteShared<G * VPL>& sh, float (&sum_p)[VPL]) {
+  constexpr int kThreads = threads_for(G * VPL), kWaves = kThreads / 64;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, gl = lane & (G - 1), grp = lane / G;
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
     float s = sum_p[v];
@@ -253,14 +291,26 @@ __device__ inline void choose(const RouteParams& p, int t0, int t1, RouteShared<
       s += __shfl_xor(s, 16);
       s += __shfl_xor(s, 32);
     }
-    if (grp == 0) sh.sums[wave][e0 + v] = s;
+    if (grp == 0) sh.sums[wave][gl * VPL + v] = s;
   }
   __syncthreads();
-  for (int e = tid; e < EP; e += kThreads) {
+  for (int e = threadIdx.x; e < G * VPL; e += kThreads) {
     float s = sh.sums[0][e];
     for (int w = 1; w < kWaves; ++w) s += sh.sums[w][e];
     sh.sums[0][e] = s;
   }
+  __syncthreads();
+}
+
+template <int EP>
+__device__ inline void clear(RouteShared<EP>& sh) {
+  constexpr int kThreads = threads_for(EP);
+  for (int e = threadIdx.x; e < EP; e += kThreads) {
+    sh.mask[e] = 0;
+    sh.run[e] = 0;
+    sh.total[e] = 0;
+  }
+  if (threadIdx.x == 0) sh.valid = 0;
   __syncthreads();
 }
 
@@ -279,12 +329,14 @@ __device__ inline int prefix_experts(RouteShared<EP>& sh) {
       c[i] = e < EP ? sh.total[e] : 0;
       s += c[i];
     }
+    // inclusive scan over the wave: rows of 16 lanes, then the rows' last lanes
     int at = s;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int o = __shfl_up(at, off);
-      at += lane >= off ? o : 0;
-    }
+    at += __builtin_amdgcn_update_dpp(0, at, 0x111, 0xF, 0xF, false);
+    at += __builtin_amdgcn_update_dpp(0, at, 0x112, 0xF, 0xF, false);
+    at += __builtin_amdgcn_update_dpp(0, at, 0x114, 0xF, 0xF, false);
+    at += __builtin_amdgcn_update_dpp(0, at, 0x118, 0xF, 0xF, false);
+    at += __builtin_amdgcn_update_dpp(0, at, 0x142, 0xA, 0xF, false);
+    at += __builtin_amdgcn_update_dpp(0, at, 0x143, 0xC, 0xF, false);
     if (lane == 63) rows = at;
     at -= s;
 #pragma unroll
@@ -302,6 +354,7 @@ __device__ inline int prefix_experts(RouteShared<EP>& sh) {
 // the sums in sh.sums[0]; sh.total holds the exclusive prefix
 template <int EP>
 __device__ inline void publish(const RouteParams& p, RouteShared<EP>& sh, const int32_t* count, int rows, int valid) {
+  constexpr int kThreads = threads_for(EP), kWaves = kThreads / 64;
   __shared__ float red[kWaves];
   float s = 0.0f;
   for (int e = threadIdx.x; e < p.experts; e += kThreads) {
@@ -322,95 +375,151 @@ __device__ inline void publish(const RouteParams& p, RouteShared<EP>& sh, const 
   }
 }
 
-// rank of a slot -> its routed row, and the row's token; base[e]: the first
-// row of the block's tokens of expert e
-__device__ inline void place(const RouteParams& p, int t0, int t1, const int32_t* base) {
-  const int64_t o1 = (int64_t)t1 * p.topk;
-  for (int64_t o = (int64_t)t0 * p.topk + threadIdx.x; o < o1; o += kThreads) {
-    const int e = p.experts_out[o];
-    if (e < 0) continue;
-    const int row = base[e] + p.slot_row[o];
-    p.slot_row[o] = row;
-    p.row_index[row] = (int32_t)(o / p.topk);
-  }
-}
-
-// Few tokens: everything in one workgroup.
+// At most 64 tokens: everything in one workgroup and one launch.
 template <int DT, int G, int VPL>
-__global__ __launch_bounds__(kThreads) void k_route_one(RouteParams p) {
+__global__ __launch_bounds__(threads_for(G * VPL)) void k_route_one(RouteParams p) {
   constexpr int EP = G * VPL;
+  constexpr int kThreads = threads_for(EP);
   __shared__ RouteShared<EP> sh;
-  choose<DT, G, VPL>(p, 0, p.tokens, sh);
-  for (int e = threadIdx.x; e < EP; e += kThreads) sh.total[e] = sh.run[e];
-  __threadfence_block();
+  clear(sh);
+  float sum_p[VPL] = {};
+  choose_64<DT, G, VPL>(p, 0, p.tokens, sh, sum_p);
+  reduce_sums<G, VPL>(sh, sum_p);
+  for (int e = threadIdx.x; e < EP; e += kThreads) sh.run[e] = sh.total[e] = __popcll(sh.mask[e]);
   __syncthreads();
   const int rows = prefix_experts(sh);
-  place(p, 0, p.tokens, sh.total);
-  for (int r = rows + threadIdx.x; r < p.tokens * p.topk; r += kThreads) p.row_index[r] = -1;
+  const int n = p.tokens * p.topk;
+  for (int o = threadIdx.x; o < n; o += kThreads) {
+    const int t = o / p.topk, e = sh.idx[t][o - t * p.topk];
+    const int row = e >= 0 ? sh.total[e] + __popcll(sh.mask[e] & ((1ull << t) - 1)) : -1;
+    p.slot_row[o] = row;
+    if (row >= 0) p.row_index[row] = t;
+    if (o >= rows) p.row_index[o] = -1;
+  }
   publish(p, sh, sh.run, rows, sh.valid);
 }
 
+// One block of tokens: experts, weights, in slot_row the rank of each slot
+// among the block's tokens of its expert, and the block's counts and sums.
 template <int DT, int G, int VPL>
-__global__ __launch_bounds__(kThreads) void k_route_choose(RouteParams p) {
+__global__ __launch_bounds__(threads_for(G * VPL)) void k_route_choose(RouteParams p) {
   constexpr int EP = G * VPL;
+  constexpr int kThreads = threads_for(EP);
   __shared__ RouteShared<EP> sh;
   const int b = blockIdx.x;
   const int t0 = b * p.per, t1 = t0 + p.per < p.tokens ? t0 + p.per : p.tokens;
-  choose<DT, G, VPL>(p, t0, t1, sh);
-  for (int e = threadIdx.x; e < p.experts; e += kThreads) {
-    p.part_counts[(int64_t)b * p.experts + e] = (uint16_t)sh.run[e];
-    p.part_sums[(int64_t)b * p.experts + e] = sh.sums[0][e];
+  clear(sh);
+  float sum_p[VPL] = {};
+  for (int s0 = t0; s0 < t1; s0 += kSub) {
+    choose_64<DT, G, VPL>(p, s0, t1, sh, sum_p);
+    __syncthreads();
+    const int n = (t1 - s0 < kSub ? t1 - s0 : kSub) * p.topk;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const int lt = i / p.topk, e = sh.idx[lt][i - lt * p.topk];
+      p.slot_row[(int64_t)s0 * p.topk + i] = e >= 0 ? sh.run[e] + __popcll(sh.mask[e] & ((1ull << lt) - 1)) : -1;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < EP; e += kThreads) {
+      sh.run[e] += __popcll(sh.mask[e]);
+      sh.mask[e] = 0;
+    }
+    __syncthreads();
+  }
+  reduce_sums<G, VPL>(sh, sum_p);
+  for (int e = threadIdx.x; e < p.pitch; e += kThreads) {
+    p.part_counts[(int64_t)b * p.pitch + e] = (uint16_t)(e < EP ? sh.run[e] : 0);
+    p.part_sums[(int64_t)b * p.pitch + e] = e < EP ? sh.sums[0][e] : 0.0f;
   }
   if (threadIdx.x == 0) p.part_valid[b] = sh.valid;
 }
 
 // Blocks 0 .. blocks-1 place their tokens' rows; block `blocks` reduces the
-// sums and publishes.  Each adds up the counts of all blocks for itself: 64 K
-// counts at most, which come out of L2.
+// sums and publishes.  Each adds up the counts of all blocks for itself, 8
+// experts a lane and load: 64 K counts of 16 bits at 256 experts, which come
+// out of L2.
 template <int EP>
-__global__ __launch_bounds__(kThreads) void k_route_place(RouteParams p) {
+__global__ __launch_bounds__(threads_for(EP)) void k_route_place(RouteParams p) {
+  constexpr int kThreads = threads_for(EP), kWaves = kThreads / 64;
   __shared__ RouteShared<EP> sh;
-  const int b = blockIdx.x, E = p.experts;
-  for (int e = threadIdx.x; e < EP; e += kThreads) {
-    sh.total[e] = 0;
-    sh.run[e] = 0;
+  const int b = blockIdx.x, tid = threadIdx.x;
+  // this thread's first slot, on its way meanwhile
+  const int t0 = b * p.per, t1 = t0 + p.per < p.tokens ? t0 + p.per : p.tokens;
+  const int64_t o0 = (int64_t)t0 * p.topk + tid, o1 = (int64_t)t1 * p.topk;
+  int e_first = -1, rank_first = 0;
+  if (o0 < o1) {
+    e_first = p.experts_out[o0];
+    rank_first = p.slot_row[o0];
   }
-  if (threadIdx.x == 0) sh.valid = 0;
-  __syncthreads();
-  constexpr int LANES = EP < kThreads ? EP : kThreads;  // threads along the experts
-  constexpr int STEP = kThreads / LANES;                // blocks read at once
-  for (int e = threadIdx.x % LANES; e < E; e += LANES) {
-    int all = 0, before = 0;
-    for (int i = threadIdx.x / LANES; i < p.blocks; i += STEP) {
-      const int c = p.part_counts[(int64_t)i * E + e];
-      all += c;
-      before += i < b ? c : 0;
+  clear(sh);
+  {
+    constexpr int LANES = EP / 8;              // lanes along the experts
+    constexpr int ROWS = kThreads / LANES;     // blocks read at once
+    const int e0 = tid % LANES * 8;
+    int all[8] = {}, before[8] = {};
+    if (e0 < p.pitch) {
+#pragma unroll 4
+      for (int i = tid / LANES; i < p.blocks; i += ROWS) {
+        const uint4 w = *reinterpret_cast<const uint4*>(p.part_counts + (int64_t)i * p.pitch + e0);
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int lo = ww[k] & 0xFFFFu, hi = ww[k] >> 16;
+          all[2 * k] += lo;
+          all[2 * k + 1] += hi;
+          before[2 * k] += i < b ? lo : 0;
+          before[2 * k + 1] += i < b ? hi : 0;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (all[k]) atomicAdd(&sh.total[e0 + k], all[k]);
+        if (before[k]) atomicAdd(&sh.run[e0 + k], before[k]);
+      }
     }
-    atomicAdd(&sh.total[e], all);
-    atomicAdd(&sh.run[e], before);
   }
-  __syncthreads();
   if (b == p.blocks) {
-    // (before == all here: sh.run holds the counts)
-    for (int e = threadIdx.x; e < E; e += kThreads) {
-      float s = 0.0f;
-      for (int i = 0; i < p.blocks; ++i) s += p.part_sums[(int64_t)i * E + e];
-      sh.sums[0][e] = s;
+    // (before == all here: sh.run holds the counts)  The sums: kWaves runs of
+    // blocks, each in order, then the runs in order.
+    const int run = (p.blocks + kWaves - 1) / kWaves;
+    const int i0 = (tid >> 6) * run, i1 = i0 + run < p.blocks ? i0 + run : p.blocks;
+    for (int e = (tid & 63) * 4; e < EP; e += 256) {  // (EP is a multiple of 4)
+      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (e < p.pitch) {
+#pragma unroll 8
+        for (int i = i0; i < i1; ++i) {
+          const float4 v = *reinterpret_cast<const float4*>(p.part_sums + (int64_t)i * p.pitch + e);
+          s.x += v.x;
+          s.y += v.y;
+          s.z += v.z;
+          s.w += v.w;
+        }
+      }
+      *reinterpret_cast<float4*>(&sh.sums[tid >> 6][e]) = s;
     }
-    for (int i = threadIdx.x; i < p.blocks; i += kThreads) atomicAdd(&sh.valid, p.part_valid[i]);
+    for (int i = tid; i < p.blocks; i += kThreads) atomicAdd(&sh.valid, p.part_valid[i]);
   }
+  __syncthreads();
   const int rows = prefix_experts(sh);
   if (b == p.blocks) {
+    for (int e = tid; e < EP; e += kThreads) {
+      float s = sh.sums[0][e];
+      for (int w = 1; w < kWaves; ++w) s += sh.sums[w][e];
+      sh.sums[0][e] = s;
+    }
+    __syncthreads();
     publish(p, sh, sh.run, rows, sh.valid);
     return;
   }
-  for (int e = threadIdx.x; e < E; e += kThreads) sh.run[e] += sh.total[e];
-  __syncthreads();
-  const int t0 = b * p.per, t1 = t0 + p.per < p.tokens ? t0 + p.per : p.tokens;
-  place(p, t0, t1, sh.run);
+  // rank of a slot -> its routed row, and the row's token
+  for (int64_t o = o0; o < o1; o += kThreads) {
+    const int e = o == o0 ? e_first : p.experts_out[o];
+    if (e < 0) continue;
+    const int row = sh.total[e] + sh.run[e] + (o == o0 ? rank_first : p.slot_row[o]);
+    p.slot_row[o] = row;
+    p.row_index[row] = (int32_t)(o / p.topk);
+  }
   const int64_t n = (int64_t)p.tokens * p.topk;
-  for (int64_t r = rows + (int64_t)b * kThreads + threadIdx.x; r < n; r += (int64_t)p.blocks * kThreads)
-    p.row_index[r] = -1;
+  for (int64_t r = rows + (int64_t)b * kThreads + tid; r < n; r += (int64_t)p.blocks * kThreads) p.row_index[r] = -1;
 }
 
 // ---- backward ---------------------------------------------------------------
@@ -549,13 +658,13 @@ void split(int64_t tokens, int64_t* per, int64_t* blocks) {
 template <int DT, int G, int VPL>
 hipError_t route_v(const RouteParams& p, hipStream_t s) {
   if (p.blocks <= 1) {
-    hipLaunchKernelGGL((k_route_one<DT, G, VPL>), dim3(1), dim3(kThreads), 0, s, p);
+    hipLaunchKernelGGL((k_route_one<DT, G, VPL>), dim3(1), dim3(threads_for(G * VPL)), 0, s, p);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((k_route_choose<DT, G, VPL>), dim3(p.blocks), dim3(kThreads), 0, s, p);
+  hipLaunchKernelGGL((k_route_choose<DT, G, VPL>), dim3(p.blocks), dim3(threads_for(G * VPL)), 0, s, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_route_place<G * VPL>), dim3(p.blocks + 1), dim3(kThreads), 0, s, p);
+  hipLaunchKernelGGL((k_route_place<G * VPL>), dim3(p.blocks + 1), dim3(threads_for(G * VPL)), 0, s, p);
   return hipGetLastError();
 }
 
@@ -596,8 +705,8 @@ size_t route_workspace(int64_t tokens, int32_t experts) {
   int64_t per, blocks;
   split(tokens, &per, &blocks);
   if (blocks <= 1) return 0;
-  const size_t cells = (size_t)blocks * (size_t)experts;
-  return (cells * sizeof(float) + (size_t)blocks * sizeof(int32_t) + cells * sizeof(uint16_t) + 15) / 16 * 16;
+  const size_t cells = (size_t)blocks * (size_t)((experts + 7) / 8 * 8);
+  return cells * sizeof(float) + cells * sizeof(uint16_t) + ((size_t)blocks * sizeof(int32_t) + 15) / 16 * 16;
 }
 
 hipError_t launch_route(const RouteArgs& a, void* workspace, hipStream_t s) {
@@ -607,10 +716,11 @@ hipError_t launch_route(const RouteArgs& a, void* workspace, hipStream_t s) {
   p.per = (int32_t)per;
   p.blocks = (int32_t)blocks;
   if (blocks > 1) {
-    const size_t cells = (size_t)blocks * (size_t)a.experts;
+    p.pitch = (a.experts + 7) / 8 * 8;
+    const size_t cells = (size_t)blocks * (size_t)p.pitch;
     p.part_sums = static_cast<float*>(workspace);
-    p.part_valid = reinterpret_cast<int32_t*>(p.part_sums + cells);
-    p.part_counts = reinterpret_cast<uint16_t*>(p.part_valid + blocks);
+    p.part_counts = reinterpret_cast<uint16_t*>(p.part_sums + cells);  // (cells is a multiple of 8)
+    p.part_valid = reinterpret_cast<int32_t*>(p.part_counts + cells);
   }
   return a.dt == DT_BF16 ? route_d<DT_BF16>(a, p, s) : route_d<DT_F32>(a, p, s);
 }
