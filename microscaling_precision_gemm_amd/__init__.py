@@ -373,46 +373,63 @@ def _need(cond, what: str):
 
 def _rows_of(t, rows, cols, what: str) -> int:
     """Row pitch of a [rows, cols] matrix whose columns are adjacent."""
-    _need(t.dim() == 2 and t.shape[0] == rows and t.shape[1] == cols, f"{what}: expected [{rows}, {cols}], got "
-          f"{list(t.shape)}")
-    _need(cols <= 1 or t.stride(1) == 1, f"{what}: columns must be adjacent")
+    if t.shape != (rows, cols):
+        raise MXError(f"{what}: expected [{rows}, {cols}], got {list(t.shape)}")
+    pitch, step = t.stride()
+    if step != 1 and cols > 1:
+        raise MXError(f"{what}: columns must be adjacent")
     # the pitch of a single row is no matter: one that keeps rows aligned
-    return t.stride(0) if rows > 1 else (cols + 7) // 8 * 8
+    return pitch if rows > 1 else (cols + 7) // 8 * 8
 
 
-def _dense(t, dtype, shape, what: str):
-    if t is not None:
-        _need(t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous(),
-              f"{what}: expected a dense {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    return t
+def _dense(t, dtype, shape, what: str) -> int:
+    """Address of a dense tensor of that dtype and shape (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise MXError(f"{what}: expected a dense {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _one(t, what: str) -> int:
+    """Address of one fp32 (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype != _torch().float32 or t.numel() != 1:
+        raise MXError(f"{what}: one fp32 expected")
+    return t.data_ptr()
+
+
+def _stream_of(stream) -> int:
+    torch = _torch()
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
 
 
 class Routing:
     """The device buffers of one routing (the fields of mx_routing in mx.h)
     and the workspace mx_route needs: experts, weights, slot_row [tokens,
     topk]; row_index [tokens * topk]; group_offsets [experts + 1]; counts,
-    prob_sum [experts]; valid, loss [1]."""
+    prob_sum [experts]; valid, loss [1].  The tensors belong to the routing
+    and are not exchanged for others; copy into them instead."""
 
     def __init__(self, tokens: int, experts: int, topk: int, device="cuda"):
         torch = _torch()
         _need(tokens >= 0 and experts >= 1 and topk >= 1, "routing: sizes")
-        self.tokens, self.num_experts, self.topk = int(tokens), int(experts), int(topk)
         new = lambda dtype, *shape: torch.empty(shape, dtype=dtype, device=device)
-        self.experts = new(torch.int32, tokens, topk)
-        self.weights = new(torch.float32, tokens, topk)
-        self.slot_row = new(torch.int32, tokens, topk)
-        self.row_index = new(torch.int32, tokens * topk)
-        self.group_offsets = new(torch.int64, experts + 1)
-        self.counts = new(torch.int64, experts)
-        self.valid = new(torch.int64, 1)
-        self.prob_sum = new(torch.float32, experts)
-        self.loss = new(torch.float32, 1)
-        self.workspace = new(torch.uint8, int(load().mx_route_workspace_bytes(tokens, experts)))
+        fields = dict(
+            tokens=int(tokens), num_experts=int(experts), topk=int(topk),
+            experts=new(torch.int32, tokens, topk), weights=new(torch.float32, tokens, topk),
+            slot_row=new(torch.int32, tokens, topk), row_index=new(torch.int32, tokens * topk),
+            group_offsets=new(torch.int64, experts + 1), counts=new(torch.int64, experts),
+            valid=new(torch.int64, 1), prob_sum=new(torch.float32, experts), loss=new(torch.float32, 1),
+            workspace=new(torch.uint8, int(load().mx_route_workspace_bytes(tokens, experts))))
+        d = _Routing(tokens, experts, topk, *(fields[n].data_ptr() for n in (
+            "experts", "weights", "slot_row", "row_index", "group_offsets", "counts", "valid", "prob_sum", "loss")))
+        fields.update(_desc=d, _ref=ctypes.byref(d))
+        self.__dict__.update(fields)
 
-    def desc(self) -> _Routing:
-        return _Routing(self.tokens, self.num_experts, self.topk, _ptr(self.experts), _ptr(self.weights),
-                        _ptr(self.slot_row), _ptr(self.row_index), _ptr(self.group_offsets), _ptr(self.counts),
-                        _ptr(self.valid), _ptr(self.prob_sum), _ptr(self.loss))
+    def __setattr__(self, name, value):
+        raise AttributeError(f"a routing's {name} is not replaced: copy into it")
 
 
 def routing(tokens: int, experts: int, topk: int, device="cuda") -> Routing:
@@ -428,10 +445,10 @@ def mx_route(logits, out: Routing, token_mask=None, flags: int = 0, stream=None)
     """Route each row of logits [tokens, experts] (bf16 or fp32) to its topk
     largest experts; token_mask: uint8 [tokens], 0 for padding."""
     ld = _rows_of(logits, out.tokens, out.num_experts, "logits")
-    _dense(token_mask, _torch().uint8, (out.tokens,), "token_mask")
-    d = out.desc()
-    _check(load().mx_route(_ptr(logits), _dt(logits), ld, _ptr(token_mask), flags, ctypes.byref(d),
-                           _ptr(out.workspace), out.workspace.numel(), _stream(stream)))
+    mask = _dense(token_mask, _torch().uint8, (out.tokens,), "token_mask")
+    ws = out.workspace
+    _check(load().mx_route(logits.data_ptr(), _dt(logits), ld, mask, flags, out._ref, ws.data_ptr(), ws.numel(),
+                           _stream_of(stream)))
     return out
 
 
@@ -443,12 +460,10 @@ def mx_route_backward(logits, r: Routing, d_weights, d_loss, d_logits, token_mas
     ld = _rows_of(logits, r.tokens, r.num_experts, "logits")
     ld_d = _rows_of(d_logits, r.tokens, r.num_experts, "d_logits")
     _need(d_logits.dtype == logits.dtype, "d_logits: dtype of logits expected")
-    _dense(token_mask, torch.uint8, (r.tokens,), "token_mask")
-    _dense(d_weights, torch.float32, (r.tokens, r.topk), "d_weights")
-    _need(d_loss is None or (d_loss.dtype == torch.float32 and d_loss.numel() == 1), "d_loss: one fp32 expected")
-    d = r.desc()
-    _check(load().mx_route_backward(_ptr(logits), _dt(logits), ld, _ptr(token_mask), flags, ctypes.byref(d),
-                                    _ptr(d_weights), _ptr(d_loss), _ptr(d_logits), ld_d, _stream(stream)))
+    mask = _dense(token_mask, torch.uint8, (r.tokens,), "token_mask")
+    dw = _dense(d_weights, torch.float32, (r.tokens, r.topk), "d_weights")
+    _check(load().mx_route_backward(logits.data_ptr(), _dt(logits), ld, mask, flags, r._ref, dw,
+                                    _one(d_loss, "d_loss"), d_logits.data_ptr(), ld_d, _stream_of(stream)))
     return d_logits
 
 
@@ -460,11 +475,10 @@ def mx_swiglu(h, y, saved: "MXTensor | None" = None, rnd: int = MX_RNE, seed: in
     rows, cols = y.shape
     ld_h, ld_y = _rows_of(h, rows, 2 * cols, "h"), _rows_of(y, rows, cols, "y")
     _need(y.dtype == h.dtype, "y: dtype of h expected")
-    _need(amax is None or (amax.dtype == _torch().float32 and amax.numel() == 1), "amax: one fp32 expected")
     d = saved.desc() if saved is not None else None
-    _check(load().mx_swiglu(_ptr(h), _dt(h), rows, cols, ld_h, _ptr(y), ld_y,
-                            ctypes.byref(d) if d is not None else None, rnd, _Rng(seed, counter), _ptr(amax),
-                            _stream(stream)))
+    _check(load().mx_swiglu(h.data_ptr(), _dt(h), rows, cols, ld_h, y.data_ptr(), ld_y,
+                            ctypes.byref(d) if d is not None else None, rnd, _Rng(seed, counter),
+                            _one(amax, "amax"), _stream_of(stream)))
     return y
 
 
@@ -477,8 +491,8 @@ def mx_swiglu_backward(saved: MXTensor, dy, dh, y_saved: "MXTensor | None" = Non
     _need(dh.dtype == dy.dtype, "dh: dtype of dy expected")
     d = saved.desc()
     dys = y_saved.desc() if y_saved is not None else None
-    _check(load().mx_swiglu_backward(ctypes.byref(d), _ptr(dy), _dt(dy), rows, cols, ld_dy, _ptr(dh), ld_dh,
-                                     ctypes.byref(dys) if dys is not None else None, _stream(stream)))
+    _check(load().mx_swiglu_backward(ctypes.byref(d), dy.data_ptr(), _dt(dy), rows, cols, ld_dy, dh.data_ptr(),
+                                     ld_dh, ctypes.byref(dys) if dys is not None else None, _stream_of(stream)))
     return dh
 
 
@@ -490,11 +504,11 @@ def mx_wgrad_grouped(dY, X: MXTensor, row_index, num_groups: int, group_offsets,
     rows, N = dY.shape
     ld_dy = _rows_of(dY, rows, N, "dY")
     ld_dw = _rows_of(dW, num_groups * N, X.cols, "dW")
-    _dense(row_index, torch.int32, (rows,), "row_index")
-    _dense(group_offsets, torch.int64, (num_groups + 1,), "group_offsets")
+    index = _dense(row_index, torch.int32, (rows,), "row_index")
+    offsets = _dense(group_offsets, torch.int64, (num_groups + 1,), "group_offsets")
     d = X.desc()
-    _check(load().mx_wgrad_grouped(_ptr(dY), ld_dy, rows, N, ctypes.byref(d), _ptr(row_index), num_groups,
-                                   _ptr(group_offsets), _ptr(dW), _dt(dW), ld_dw, flags, _stream(stream)))
+    _check(load().mx_wgrad_grouped(dY.data_ptr(), ld_dy, rows, N, ctypes.byref(d), index, num_groups, offsets,
+                                   dW.data_ptr(), _dt(dW), ld_dw, flags, _stream_of(stream)))
     return dW
 
 
@@ -506,10 +520,10 @@ def mx_combine(Y, slot_row, weights, out, stream=None):
     tokens, topk = slot_row.shape
     rows, cols = Y.shape
     ld_y, ld_out = _rows_of(Y, rows, cols, "Y"), _rows_of(out, tokens, cols, "out")
-    _dense(slot_row, torch.int32, (tokens, topk), "slot_row")
-    _dense(weights, torch.float32, (tokens, topk), "weights")
-    _check(load().mx_combine(_ptr(Y), _dt(Y), rows, cols, ld_y, _ptr(slot_row), _ptr(weights), tokens, topk,
-                             _ptr(out), _dt(out), ld_out, _stream(stream)))
+    slots = _dense(slot_row, torch.int32, (tokens, topk), "slot_row")
+    w = _dense(weights, torch.float32, (tokens, topk), "weights")
+    _check(load().mx_combine(Y.data_ptr(), _dt(Y), rows, cols, ld_y, slots, w, tokens, topk, out.data_ptr(), _dt(out),
+                             ld_out, _stream_of(stream)))
     return out
 
 
@@ -521,9 +535,9 @@ def mx_combine_backward(d_out, Y, slot_row, weights, dY, d_weights, stream=None)
     tokens, topk = slot_row.shape
     cols = d_out.shape[1]
     ld_do = _rows_of(d_out, tokens, cols, "d_out")
-    _dense(slot_row, torch.int32, (tokens, topk), "slot_row")
-    _dense(weights, torch.float32, (tokens, topk), "weights")
-    _dense(d_weights, torch.float32, (tokens, topk), "d_weights")
+    slots = _dense(slot_row, torch.int32, (tokens, topk), "slot_row")
+    w = _dense(weights, torch.float32, (tokens, topk), "weights")
+    dw = _dense(d_weights, torch.float32, (tokens, topk), "d_weights")
     _need(d_weights is None or Y is not None, "d_weights needs Y")
     some = Y if Y is not None else dY
     rows = some.shape[0] if some is not None else 0
@@ -531,7 +545,7 @@ def mx_combine_backward(d_out, Y, slot_row, weights, dY, d_weights, stream=None)
     ld_dy = _rows_of(dY, rows, cols, "dY") if dY is not None else 0
     for t in (Y, dY):
         _need(t is None or t.dtype == d_out.dtype, "Y, dY: dtype of d_out expected")
-    _check(load().mx_combine_backward(_ptr(d_out), _dt(d_out), ld_do, _ptr(Y), ld_y, rows, cols, _ptr(slot_row),
-                                      _ptr(weights), tokens, topk, _ptr(dY), ld_dy, _ptr(d_weights),
-                                      _stream(stream)))
+    _check(load().mx_combine_backward(d_out.data_ptr(), _dt(d_out), ld_do, 0 if Y is None else Y.data_ptr(), ld_y,
+                                      rows, cols, slots, w, tokens, topk, 0 if dY is None else dY.data_ptr(), ld_dy,
+                                      dw, _stream_of(stream)))
     return dY, d_weights

@@ -94,38 +94,50 @@ struct OpAdd {
   __device__ float operator()(float a, float b) const { return a + b; }
 };
 
-// the lane's VPL scores of row t; entries past E are -inf
+// Score v of lane gl of a group: chunks of VQ (up to 16 bytes) consecutive
+// scores, the chunks of the group's lanes side by side, so that a load of the
+// group is one run of memory.
 template <int DT, int VPL>
-__device__ inline void load_scores(const RouteParams& p, int64_t t, int e0, float (&x)[VPL]) {
-  const int64_t off = t * p.ld + e0;
-  if (VPL >= 4 && p.vec && e0 + VPL <= p.experts) {
-    if constexpr (DT == DT_BF16 && VPL >= 8) {
+constexpr int chunk_of() {
+  return VPL < (DT == DT_BF16 ? 8 : 4) ? VPL : (DT == DT_BF16 ? 8 : 4);
+}
+template <int DT, int G, int VPL>
+__device__ inline int expert_of(int gl, int v) {
+  constexpr int VQ = chunk_of<DT, VPL>();
+  return (v / VQ) * (VQ * G) + gl * VQ + v % VQ;
+}
+
+// the lane's VPL scores of row t; entries past E are -inf
+template <int DT, int G, int VPL>
+__device__ inline void load_scores(const RouteParams& p, int64_t t, int gl, float (&x)[VPL]) {
+  constexpr int VQ = chunk_of<DT, VPL>();
 #pragma unroll
-      for (int v = 0; v < VPL; v += 8) {
+  for (int v = 0; v < VPL; v += VQ) {
+    const int e = expert_of<DT, G, VPL>(gl, v);
+    const int64_t off = t * p.ld + e;
+    if (VQ >= 4 && p.vec && e + VQ <= p.experts) {
+      if constexpr (DT == DT_BF16 && VQ == 8) {
         float y[8];
-        load8<DT_BF16>(p.logits, off + v, y);
+        load8<DT_BF16>(p.logits, off, y);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[v + i] = y[i];
-      }
-    } else if constexpr (DT == DT_BF16 && VPL == 4) {
-      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.logits) + off);
-      x[0] = u2f(w.x << 16);
-      x[1] = u2f(w.x & 0xFFFF0000u);
-      x[2] = u2f(w.y << 16);
-      x[3] = u2f(w.y & 0xFFFF0000u);
-    } else if constexpr (DT == DT_F32 && VPL >= 4) {
-#pragma unroll
-      for (int v = 0; v < VPL; v += 4) {
-        const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(p.logits) + off + v);
+      } else if constexpr (DT == DT_BF16 && VQ == 4) {
+        const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.logits) + off);
+        x[v] = u2f(w.x << 16);
+        x[v + 1] = u2f(w.x & 0xFFFF0000u);
+        x[v + 2] = u2f(w.y << 16);
+        x[v + 3] = u2f(w.y & 0xFFFF0000u);
+      } else if constexpr (DT == DT_F32 && VQ == 4) {
+        const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(p.logits) + off);
         x[v] = w.x;
         x[v + 1] = w.y;
         x[v + 2] = w.z;
         x[v + 3] = w.w;
       }
-    }
-  } else {
+    } else {
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) x[v] = e0 + v < p.experts ? load1<DT>(p.logits, off + v) : -__builtin_inff();
+      for (int i = 0; i < VQ; ++i) x[v + i] = e + i < p.experts ? load1<DT>(p.logits, off + i) : -__builtin_inff();
+    }
   }
 }
 
@@ -166,11 +178,11 @@ __device__ inline uint32_t key_of(float x, int e) {
 // The topk largest scores of each group's token: lane j of the group gets the
 // expert of slot j (-1 where there is none) and its score.
 template <int DT, int G, int VPL>
-__device__ inline int select(const RouteParams& p, int64_t t, const float (&x)[VPL], int e0, int gl, float* score) {
+__device__ inline int select(const RouteParams& p, int64_t t, const float (&x)[VPL], int gl, float* score) {
   const int topk = p.topk;
   uint32_t key[VPL];
 #pragma unroll
-  for (int v = 0; v < VPL; ++v) key[v] = key_of<DT>(x[v], e0 + v);
+  for (int v = 0; v < VPL; ++v) key[v] = key_of<DT>(x[v], expert_of<DT, G, VPL>(gl, v));
   uint32_t last = 0x80000000u, mine = 0;
   bool unsure = false;
   const int n = DT == DT_BF16 ? topk : topk + 1;
@@ -199,11 +211,11 @@ __device__ inline int select(const RouteParams& p, int64_t t, const float (&x)[V
         m = group_reduce<G>(m, OpMax());
         int w = 1 << 20;  // the first of this lane's that has it
 #pragma unroll
-        for (int v = VPL - 1; v >= 0; --v) w = y[v] == m ? e0 + v : w;
+        for (int v = VPL - 1; v >= 0; --v) w = y[v] == m ? expert_of<DT, G, VPL>(gl, v) : w;
         if (!(m > -__builtin_inff())) w = 1 << 20;
         w = (1 << 20) - (int)group_umax<G>((uint32_t)((1 << 20) - w));  // the lowest of the group's
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) y[v] = w == e0 + v ? -__builtin_inff() : y[v];
+        for (int v = 0; v < VPL; ++v) y[v] = w == expert_of<DT, G, VPL>(gl, v) ? -__builtin_inff() : y[v];
         at = gl == j ? (w < (1 << 20) ? w : -1) : at;
       }
     }
@@ -223,7 +235,6 @@ __device__ inline void choose_64(const RouteParams& p, int s0, int t1, RouteShar
   constexpr int TPI = 64 / G;  // tokens a wave handles at once
   constexpr int ITS = kSub / kWaves / TPI;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, gl = lane & (G - 1), grp = lane / G;
-  const int e0 = gl * VPL;
   int n_valid = 0;
   float x[2][VPL];
   bool ok[2];
@@ -231,7 +242,7 @@ __device__ inline void choose_64(const RouteParams& p, int s0, int t1, RouteShar
     const int t = s0 + wave * (kSub / kWaves) + it * TPI + grp;
     in = t < t1 && (!p.mask || p.mask[t] != 0);
     if (in) {
-      load_scores<DT, VPL>(p, t, e0, y);
+      load_scores<DT, G, VPL>(p, t, gl, y);
     } else {
 #pragma unroll
       for (int v = 0; v < VPL; ++v) y[v] = -__builtin_inff();
@@ -249,7 +260,7 @@ __device__ inline void choose_64(const RouteParams& p, int s0, int t1, RouteShar
     m = group_reduce<G>(__builtin_fmaxf(m, -__builtin_inff()), OpMax());
     const float base = m == -__builtin_inff() ? 0.0f : m;
     float xe;
-    const int e = select<DT, G, VPL>(p, t, y, e0, gl, &xe);
+    const int e = select<DT, G, VPL>(p, t, y, gl, &xe);
     float s = 0.0f;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
@@ -280,7 +291,7 @@ __device__ inline void choose_64(const RouteParams& p, int s0, int t1, RouteShar
 
 // The block's sums of p into sh.sums[0]: over the groups of a wave, then over
 // the waves.
-template <int G, int VPL>
+template <int DT, int G, int VPL>
 __device__ inline void reduce_sums(RouteShared<G * VPL>& sh, float (&sum_p)[VPL]) {
   constexpr int kThreads = threads_for(G * VPL), kWaves = kThreads / 64;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, gl = lane & (G - 1), grp = lane / G;
@@ -291,7 +302,7 @@ __device__ inline void reduce_sums(RouteShared<G * VPL>& sh, float (&sum_p)[VPL]
       s += __shfl_xor(s, 16);
       s += __shfl_xor(s, 32);
     }
-    if (grp == 0) sh.sums[wave][gl * VPL + v] = s;
+    if (grp == 0) sh.sums[wave][expert_of<DT, G, VPL>(gl, v)] = s;
   }
   __syncthreads();
   for (int e = threadIdx.x; e < G * VPL; e += kThreads) {
@@ -384,7 +395,7 @@ __global__ __launch_bounds__(threads_for(G * VPL)) void k_route_one(RouteParams 
   clear(sh);
   float sum_p[VPL] = {};
   choose_64<DT, G, VPL>(p, 0, p.tokens, sh, sum_p);
-  reduce_sums<G, VPL>(sh, sum_p);
+  reduce_sums<DT, G, VPL>(sh, sum_p);
   for (int e = threadIdx.x; e < EP; e += kThreads) sh.run[e] = sh.total[e] = __popcll(sh.mask[e]);
   __syncthreads();
   const int rows = prefix_experts(sh);
@@ -425,7 +436,7 @@ __global__ __launch_bounds__(threads_for(G * VPL)) void k_route_choose(RoutePara
     }
     __syncthreads();
   }
-  reduce_sums<G, VPL>(sh, sum_p);
+  reduce_sums<DT, G, VPL>(sh, sum_p);
   for (int e = threadIdx.x; e < p.pitch; e += kThreads) {
     p.part_counts[(int64_t)b * p.pitch + e] = (uint16_t)(e < EP ? sh.run[e] : 0);
     p.part_sums[(int64_t)b * p.pitch + e] = e < EP ? sh.sums[0][e] : 0.0f;
@@ -534,95 +545,117 @@ struct RouteBwdParams {
 
 constexpr int kBwdThreads = 256;
 
+// One token of a group on its way in.
+template <int VPL>
+struct RouteIn {
+  float x[VPL];
+  int e;         // lane j: the expert of slot j
+  float dw, xe;  // the gradient of its weight, its score
+  bool ok;
+};
+
+// The terms of the chosen experts go to the lanes that hold those experts'
+// scores through LDS, one word an expert, zero but for the token's topk words:
+// each lane clears again what it wrote.  A group is part of one wave, whose LDS
+// accesses keep their order, so no barrier is needed.
 template <int DT, int G, int VPL>
 __global__ __launch_bounds__(kBwdThreads) void k_route_bwd(RouteBwdParams b) {
-  constexpr int EP = G * VPL;
   constexpr int GROUPS = kBwdThreads / G;
-  __shared__ __attribute__((aligned(16))) float extra[GROUPS][EP];
+  constexpr int VQ = chunk_of<DT, VPL>();
+  __shared__ __attribute__((aligned(16))) float extra[GROUPS][G * VPL];
   const RouteParams& p = b.f;
   const int gl = threadIdx.x & (G - 1), grp = threadIdx.x / G;
-  const int e0 = gl * VPL, k = p.topk;
+  const int k = p.topk;
+  float* mine = extra[grp];
+  const auto load = [&](int64_t t, RouteIn<VPL>& in) {
+    in.ok = t < p.tokens && (!p.mask || p.mask[t] != 0);
+    in.e = -1;
+    in.dw = in.xe = 0.0f;
+    if (in.ok) {
+      if (gl < k) {
+        in.e = p.experts_out[t * k + gl];
+        in.dw = b.d_weights ? b.d_weights[t * k + gl] : 0.0f;
+      }
+      load_scores<DT, G, VPL>(p, t, gl, in.x);
+      in.e = in.e < p.experts ? in.e : -1;
+      if (in.e >= 0) in.xe = load1<DT>(p.logits, t * p.ld + in.e);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) in.x[i] = -__builtin_inff();
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * GROUPS;
+  int64_t t = (int64_t)blockIdx.x * GROUPS + grp;
+  RouteIn<VPL> in;
+  load(t, in);
   const float v = (float)*p.valid;
   const float scale = b.d_loss && v > 0.0f ? *b.d_loss * ((float)p.experts / ((float)k * v)) / v : 0.0f;
   float bal[VPL];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) bal[i] = e0 + i < p.experts ? scale * (float)p.counts[e0 + i] : 0.0f;
-  for (int64_t t0 = (int64_t)blockIdx.x * GROUPS; t0 < p.tokens; t0 += (int64_t)gridDim.x * GROUPS) {
-    const int64_t t = t0 + grp;
-    const bool ok = t < p.tokens && (!p.mask || p.mask[t] != 0);
-    float x[VPL];
-    if (ok) {
-      load_scores<DT, VPL>(p, t, e0, x);
-    } else {
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) x[i] = -__builtin_inff();
-    }
-    // this lane's slot
-    int e = -1;
-    float dw = 0.0f, xe = 0.0f;
-    if (ok && gl < k) {
-      e = p.experts_out[t * k + gl];
-      e = e < p.experts ? e : -1;
-      if (e >= 0) {
-        dw = b.d_weights ? b.d_weights[t * k + gl] : 0.0f;
-        xe = load1<DT>(p.logits, t * p.ld + e);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) extra[grp][e0 + i] = 0.0f;
+  for (int i = 0; i < VPL; ++i) {
+    const int e = expert_of<DT, G, VPL>(gl, i);
+    bal[i] = e < p.experts ? scale * (float)p.counts[e] : 0.0f;
+    mine[e] = 0.0f;
+  }
+  // (the groups of a wave leave the loop together: their lanes are shuffled as one)
+  for (; __ballot(t < p.tokens) != 0; t += step) {
+    float(&x)[VPL] = in.x;
     float m = x[0];
 #pragma unroll
     for (int i = 1; i < VPL; ++i) m = __builtin_fmaxf(m, x[i]);
     m = group_reduce<G>(__builtin_fmaxf(m, -__builtin_inff()), OpMax());
     m = m == -__builtin_inff() ? 0.0f : m;
-    float s = 0.0f;
+    float s = 0.0f, pb = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       x[i] = __builtin_amdgcn_exp2f((x[i] - m) * kLog2e);
       s += x[i];
+      pb = fmaf(x[i], bal[i], pb);
     }
     s = group_reduce<G>(s, OpAdd());
     const float inv = s == 0.0f ? 0.0f : 1.0f / s;
-    float pb = 0.0f;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      x[i] *= inv;
-      pb = fmaf(x[i], bal[i], pb);
-    }
-    pb = group_reduce<G>(pb, OpAdd());
-    float q = e >= 0 ? __builtin_amdgcn_exp2f((xe - m) * kLog2e) : 0.0f;
+    pb = group_reduce<G>(pb, OpAdd()) * inv;
+    const int e = in.e;
+    float q = e >= 0 ? __builtin_amdgcn_exp2f((in.xe - m) * kLog2e) : 0.0f;
     if (p.normalize) {
       const float sq = group_reduce<G>(q, OpAdd());
       q = e >= 0 ? q / sq : 0.0f;
     } else {
       q *= inv;
     }
-    const float qd = group_reduce<G>(q * dw, OpAdd());
+    const float qd = group_reduce<G>(q * in.dw, OpAdd());
     if (!p.normalize) pb += qd;
-    if (e >= 0) extra[grp][e] = p.normalize ? q * (dw - qd) : q * dw;
-    __syncthreads();
+    if (e >= 0) mine[e] = p.normalize ? q * (in.dw - qd) : q * in.dw;
+    __builtin_amdgcn_wave_barrier();
+    float o[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) o[i] = mine[expert_of<DT, G, VPL>(gl, i)];
+    __builtin_amdgcn_wave_barrier();
+    if (e >= 0) mine[e] = 0.0f;
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) o[i] = fmaf(x[i] * inv, bal[i] - pb, o[i]);
+    load(t + step, in);
     if (t < p.tokens) {
-      float o[VPL];
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) o[i] = fmaf(x[i], bal[i] - pb, extra[grp][e0 + i]);
-      const int64_t off = t * b.ld_d + e0;
-      if (VPL >= 8 && b.vec_d && e0 + VPL <= p.experts) {
-        if constexpr (VPL >= 8) {
+      for (int i = 0; i < VPL; i += VQ) {
+        const int e2 = expert_of<DT, G, VPL>(gl, i);
+        const int64_t off = t * b.ld_d + e2;
+        if (VQ * (DT == DT_BF16 ? 2 : 4) == 16 && b.vec_d && e2 + VQ <= p.experts) {
+          if constexpr (DT == DT_BF16 && VQ == 8)
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(b.d_logits) + off) =
+                make_uint4(pack_bf16(o[i], o[i + 1]), pack_bf16(o[i + 2], o[i + 3]), pack_bf16(o[i + 4], o[i + 5]),
+                           pack_bf16(o[i + 6], o[i + 7]));
+          if constexpr (DT == DT_F32 && VQ == 4)
+            *reinterpret_cast<float4*>(static_cast<float*>(b.d_logits) + off) =
+                make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        } else {
 #pragma unroll
-          for (int i = 0; i < VPL; i += 8) {
-            float y[8];
-#pragma unroll
-            for (int h = 0; h < 8; ++h) y[h] = o[i + h];
-            store8<DT>(b.d_logits, off + i, y);
-          }
+          for (int h = 0; h < VQ; ++h)
+            if (e2 + h < p.experts) store1<DT>(b.d_logits, off + h, o[i + h]);
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (e0 + i < p.experts) store1<DT>(b.d_logits, off + i, o[i]);
       }
     }
-    __syncthreads();
   }
 }
 
@@ -672,7 +705,7 @@ template <int DT, int G, int VPL>
 hipError_t route_bwd_v(const RouteBwdParams& p, hipStream_t s) {
   constexpr int GROUPS = kBwdThreads / G;
   const int64_t need = ((int64_t)p.f.tokens + GROUPS - 1) / GROUPS;
-  hipLaunchKernelGGL((k_route_bwd<DT, G, VPL>), dim3((uint32_t)(need < 2048 ? need : 2048)), dim3(kBwdThreads), 0, s,
+  hipLaunchKernelGGL((k_route_bwd<DT, G, VPL>), dim3((uint32_t)(need < 1024 ? need : 1024)), dim3(kBwdThreads), 0, s,
                      p);
   return hipGetLastError();
 }
