@@ -401,8 +401,10 @@ def _one(t, what: str) -> int:
 
 
 def _stream_of(stream) -> int:
-    torch = _torch()
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    torch = _torch()  # (torch.cuda.current_stream() builds an object: 2.7 us against 0.3)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 class Routing:

@@ -17,23 +17,30 @@ __device__ inline float e8m0_value(uint32_t sc) {
   return sc == 0xFFu ? __builtin_nanf("") : (sc == 0u ? u2f(0x00400000u) : u2f(sc << 23));
 }
 
-// 4 codes of w times 2^(sc - 127): FP32
+// 4 codes of w times 2^(sc - 127), exactly, as FP32.  The FP8 conversions give
+// NaN for scale code 255 and the NaN codes (checked on the device over all
+// codes and scale codes, FP32 subnormal results among them).
 template <int FMT>
-__device__ inline void decode4_f32(uint32_t w, float X, float* v) {
+__device__ inline void decode4_f32(uint32_t w, uint32_t sc, float* v) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  if constexpr (FMT == FMT_MXINT8) {
+    const float X = e8m0_value(sc);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t c = (w >> (8 * i)) & 0xFFu;
-    float e;
+    for (int i = 0; i < 4; ++i) v[i] = int8_value((w >> (8 * i)) & 0xFFu) * X;
+  } else {
+    const float X = u2f(sc << 23);
+    f2 a, b;
     if constexpr (FMT == FMT_MXFP8) {
-      const uint32_t mag = c & 0x7Fu;
-      e = mag == 0x7Fu ? __builtin_nanf("") : e4m3_mag_value(mag);
-      if (c & 0x80u) e = -e;
-    } else if constexpr (FMT == FMT_MXFP8_E5M2) {
-      e = e5m2_value(c);
+      a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, X, false);
+      b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, X, true);
     } else {
-      e = int8_value(c);
+      a = __builtin_amdgcn_cvt_scalef32_pk_f32_bf8(w, X, false);
+      b = __builtin_amdgcn_cvt_scalef32_pk_f32_bf8(w, X, true);
     }
-    v[i] = e * X;
+    v[0] = a[0];
+    v[1] = a[1];
+    v[2] = b[0];
+    v[3] = b[1];
   }
 }
 

@@ -25,6 +25,14 @@ namespace mxk {
 namespace {
 
 constexpr int kThreads = 256;
+// With max |y| a workgroup that has a new one does an atomic on one word, and
+// these serialize, so there are few, large workgroups that walk over the tensor
+// and look at the word just before (32768 x 2048 BF16 with an MXFP8
+// checkpoint: 110 us; 122 with a workgroup per 1024 chunks that looked at its
+// start, 206 with one per 512 that did not look; 4099 x 4096 FP32: 47 us, 56
+// with a workgroup per 1024 chunks).
+constexpr int kMaxThreads = 1024, kMaxGrid = 256;
+constexpr int64_t kOneChunks = 4096;  // tensors up to this go to one workgroup
 constexpr float kLog2e = 1.44269504088896340736f;
 
 __device__ inline float sigmoid(float x) {
@@ -33,39 +41,53 @@ __device__ inline float sigmoid(float x) {
 
 __global__ void k_clear(float* p) { *p = 0.0f; }
 
-// bits of the largest |v| of the workgroup into *amax (FP32 bits of
-// non-negative values order as integers; the order of the maxima is no matter)
-__device__ inline void block_max(uint32_t m, float* amax) {
-  __shared__ uint32_t red[kThreads / 64];
+// row and 8-column chunk of chunk q of a matrix with cpr chunks a row
+__device__ inline void locate(int64_t q, int64_t cpr, int64_t* r, int64_t* c) {
+  if (q <= UINT32_MAX && cpr <= UINT32_MAX) *r = (uint32_t)q / (uint32_t)cpr;
+  else *r = q / cpr;
+  *c = q - *r * cpr;
+}
+
+// largest of the workgroup's bit patterns (FP32 bits of non-negative values
+// order as integers; the order of the maxima is no matter), in thread 0
+__device__ inline uint32_t block_max(uint32_t m) {
+  __shared__ uint32_t red[kMaxThreads / 64];
   m = wave_max_u32(m);
   if ((threadIdx.x & 63u) == 0) red[threadIdx.x >> 6] = m;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kThreads / 64; ++w) m = red[w] > m ? red[w] : m;
-    atomicMax(reinterpret_cast<uint32_t*>(amax), m);
-  }
+  if (threadIdx.x == 0)
+    for (uint32_t w = 1; w < blockDim.x / 64; ++w) m = red[w] > m ? red[w] : m;
+  return m;
 }
 
-// FMT 0: nothing is saved.  Q chunks of 8 columns, cpr of them in a row.
-template <int DT, int FMT, bool SR>
-__global__ __launch_bounds__(kThreads) void k_swiglu(const void* __restrict__ h, int64_t ld_h, int64_t cpr,
-                                                     int64_t Q, void* __restrict__ y, int64_t ld_y,
-                                                     uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
-                                                     MxEnc enc, float* __restrict__ amax) {
+// FMT 0: nothing is saved.  Q chunks of 8 columns, cpr of them in a row, one a
+// thread: HBM was fullest with as many small waves as there are chunks (at
+// 32768 x 2048 BF16 without a checkpoint 5.8 TB/s, against 5.6 with two chunks
+// a thread and 5.4 with workgroups that walk over the tensor).  AMAX 0: not
+// wanted; 1: the workgroup is alone, so *amax needs no clearing before and no
+// atomic; 2: *amax is cleared before.
+template <int DT, int FMT, bool SR, int AMAX>
+__global__ __launch_bounds__(AMAX ? kMaxThreads : kThreads) void k_swiglu(
+    const void* __restrict__ h, int64_t ld_h, int64_t cpr, int64_t Q, void* __restrict__ y, int64_t ld_y,
+    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, MxEnc enc, float* __restrict__ amax) {
+  constexpr int T = AMAX ? kMaxThreads : kThreads;
   const int64_t cols = 8 * cpr;
+  uint32_t* const top = reinterpret_cast<uint32_t*>(amax);
   uint32_t m = 0;
-  for (int64_t q = (int64_t)blockIdx.x * kThreads + threadIdx.x; q < Q; q += (int64_t)gridDim.x * kThreads) {
-    const int64_t r = q / cpr, c = q - r * cpr;
+  // (lane quads stand or fall together: Q and a workgroup's chunks are multiples of 4)
+  for (int64_t q = (int64_t)blockIdx.x * T + threadIdx.x; q < Q; q += (int64_t)gridDim.x * T) {
+    int64_t r, c;
+    locate(q, cpr, &r, &c);
     float g[8], u[8], v[8];
     load8<DT>(h, r * ld_h + 8 * c, g);
     load8<DT>(h, r * ld_h + cols + 8 * c, u);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = g[i] * sigmoid(g[i]) * u[i];
+    for (int k = 0; k < 8; ++k) v[k] = g[k] * sigmoid(g[k]) * u[k];
     store8<DT>(y, r * ld_y + 8 * c, v);
-    if (amax) {
+    if constexpr (AMAX != 0) {
       if constexpr (DT == DT_BF16) {  // of the values as stored
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = u2f(pack_bf16(v[i], v[i]) << 16);
+        for (int k = 0; k < 8; ++k) v[k] = u2f(pack_bf16(v[k], v[k]) << 16);
       }
       const uint32_t o = max_abs_bits(v);
       m = o > m ? o : m;
@@ -83,15 +105,20 @@ __global__ __launch_bounds__(kThreads) void k_swiglu(const void* __restrict__ h,
       }
     }
   }
-  if (amax) block_max(m, amax);
+  if constexpr (AMAX != 0) {
+    m = block_max(m);
+    if (threadIdx.x == 0) {
+      if constexpr (AMAX == 1) *top = m;
+      else if (m > __hip_atomic_load(top, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMax(top, m);
+    }
+  }
 }
 
 // 8 elements of an 8-bit MX format times their block scale, exactly
 template <int FMT>
 __device__ inline void decode8(uint2 w, uint32_t sc, float (&v)[8]) {
-  const float X = e8m0_value(sc);
-  decode4_f32<FMT>(w.x, X, v);
-  decode4_f32<FMT>(w.y, X, v + 4);
+  decode4_f32<FMT>(w.x, sc, v);
+  decode4_f32<FMT>(w.y, sc, v + 4);
 }
 
 template <int DT, int FMT, int YFMT>
@@ -103,20 +130,21 @@ __global__ __launch_bounds__(kThreads) void k_swiglu_bwd(const uint8_t* __restri
                                                          uint8_t* __restrict__ y_scales) {
   const int64_t cols = 8 * cpr;
   for (int64_t q = (int64_t)blockIdx.x * kThreads + threadIdx.x; q < Q; q += (int64_t)gridDim.x * kThreads) {
-    const int64_t r = q / cpr, c = q - r * cpr;
+    int64_t r, c;
+    locate(q, cpr, &r, &c);
     const int64_t qg = r * 2 * cpr + c, qu = qg + cpr;
     float g[8], u[8], d[8], y[8];
     decode8<FMT>(*reinterpret_cast<const uint2*>(codes + 8 * qg), scales[qg >> 2], g);
     decode8<FMT>(*reinterpret_cast<const uint2*>(codes + 8 * qu), scales[qu >> 2], u);
     load8<DT>(dy, r * ld_dy + 8 * c, d);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float s = sigmoid(g[i]), gs = g[i] * s;
-      const float dg = d[i] * u[i] * (s * fmaf(g[i], 1.0f - s, 1.0f));
-      const float du = d[i] * gs;
-      y[i] = gs * u[i];
-      g[i] = dg;
-      u[i] = du;
+    for (int k = 0; k < 8; ++k) {
+      const float s = sigmoid(g[k]), gs = g[k] * s;
+      const float dg = d[k] * u[k] * (s * fmaf(g[k], 1.0f - s, 1.0f));
+      const float du = d[k] * gs;
+      y[k] = gs * u[k];
+      g[k] = dg;
+      u[k] = du;
     }
     store8<DT>(dh, r * ld_dh + 8 * c, g);
     store8<DT>(dh, r * ld_dh + cols + 8 * c, u);
@@ -129,20 +157,29 @@ __global__ __launch_bounds__(kThreads) void k_swiglu_bwd(const uint8_t* __restri
   }
 }
 
-int grid_of(int64_t Q) {
-  const int64_t g = (Q + kThreads - 1) / kThreads;
-  return (int)(g < 2048 ? g : 2048);
+// a thread per chunk, up to the largest grid
+int grid_of(int64_t Q, int threads, int64_t most = 1 << 21) {
+  const int64_t g = (Q + threads - 1) / threads;
+  return (int)(g < most ? g : most);
 }
 
 template <int DT, int FMT>
 void swiglu_f(const SwigluArgs& a, int64_t Q, hipStream_t s) {
   const MxEnc enc{false, a.seed, a.counter};
-  if (FMT != 0 && a.sr)
-    hipLaunchKernelGGL((k_swiglu<DT, FMT, FMT != 0>), dim3(grid_of(Q)), dim3(kThreads), 0, s, a.h, a.ld_h,
-                       a.cols / 8, Q, a.y, a.ld_y, a.codes, a.scales, enc, a.amax);
-  else
-    hipLaunchKernelGGL((k_swiglu<DT, FMT, false>), dim3(grid_of(Q)), dim3(kThreads), 0, s, a.h, a.ld_h, a.cols / 8,
-                       Q, a.y, a.ld_y, a.codes, a.scales, enc, a.amax);
+#define MXK_SG(SR, AMAX, GRID, T)                                                                              \
+  hipLaunchKernelGGL((k_swiglu<DT, FMT, SR, AMAX>), dim3(GRID), dim3(T), 0, s, a.h, a.ld_h, a.cols / 8, Q, a.y, \
+                     a.ld_y, a.codes, a.scales, enc, a.amax)
+#define MXK_SGA(SR)                                                               \
+  if (!a.amax) MXK_SG(SR, 0, grid_of(Q, kThreads), kThreads);                     \
+  else if (Q <= kOneChunks) MXK_SG(SR, 1, 1, kMaxThreads);                        \
+  else MXK_SG(SR, 2, grid_of(Q, kMaxThreads, kMaxGrid), kMaxThreads)
+  if (FMT != 0 && a.sr) {
+    MXK_SGA((FMT != 0));
+  } else {
+    MXK_SGA(false);
+  }
+#undef MXK_SGA
+#undef MXK_SG
 }
 
 template <int DT>
@@ -158,7 +195,7 @@ void swiglu_d(const SwigluArgs& a, int64_t Q, hipStream_t s) {
 template <int DT, int FMT>
 void bwd_f(const SwigluBwdArgs& a, int64_t Q, hipStream_t s) {
 #define MXK_SB(Y)                                                                                                  \
-  hipLaunchKernelGGL((k_swiglu_bwd<DT, FMT, Y>), dim3(grid_of(Q)), dim3(kThreads), 0, s, a.codes, a.scales,     \
+  hipLaunchKernelGGL((k_swiglu_bwd<DT, FMT, Y>), dim3(grid_of(Q, kThreads)), dim3(kThreads), 0, s, a.codes, a.scales,     \
                      a.cols / 8, Q, a.dy, a.ld_dy, a.dh, a.ld_dh, a.y_codes, a.y_scales)
   switch (a.y_fmt) {
     case FMT_MXFP8: MXK_SB(FMT_MXFP8); break;
@@ -181,8 +218,8 @@ void bwd_d(const SwigluBwdArgs& a, int64_t Q, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_swiglu(const SwigluArgs& a, hipStream_t s) {
-  if (a.amax) hipLaunchKernelGGL(k_clear, dim3(1), dim3(1), 0, s, a.amax);
   const int64_t Q = a.rows * (a.cols / 8);
+  if (a.amax && (Q == 0 || Q > kOneChunks)) hipLaunchKernelGGL(k_clear, dim3(1), dim3(1), 0, s, a.amax);
   if (Q > 0) {
     if (a.dt == DT_BF16) swiglu_d<DT_BF16>(a, Q, s);
     else swiglu_d<DT_F32>(a, Q, s);
