@@ -557,11 +557,17 @@ mx_status mx_swiglu_backward(const mx_tensor* saved, const void* dy, int32_t dt,
  * group_offsets: as in mx_gemm_grouped (device int64 [num_groups + 1],
  * clamped into [0, routed_rows]); NULL with num_groups == 1 takes all rows.
  * dW [num_groups * N, K]: FP32 or BF16 (dwdt), row pitch ld_dw, element
- * alignment. */
+ * alignment.  Where the tiles of dW are too few for the device, the rows of a
+ * group are summed in parts, which are then added in a fixed order, so equal
+ * calls give equal bits.  workspace: mx_wgrad_workspace_bytes(routed_rows, N, K,
+ * num_groups) bytes of device memory, 16-byte aligned, written before it is
+ * read (NULL when that is 0). */
 #define MX_WGRAD_ACCUMULATE 1u
+size_t mx_wgrad_workspace_bytes(int64_t routed_rows, int64_t N, int64_t K, int32_t num_groups);
 mx_status mx_wgrad_grouped(const void* dY, int64_t ld_dy, int64_t routed_rows, int64_t N, const mx_tensor* X,
                            const int32_t* row_index, int32_t num_groups, const int64_t* group_offsets, void* dW,
-                           int32_t dwdt, int64_t ld_dw, uint32_t flags, mx_stream stream);
+                           int32_t dwdt, int64_t ld_dw, uint32_t flags, void* workspace, size_t workspace_bytes,
+                           mx_stream stream);
 
 /* Combination of routed rows: out[t, :] = sum_j weight[t, j] * Y[slot_row[t,
  * j], :] in FP32, slots in order, rounded once.  Y [rows, cols] (ydt, row pitch

@@ -38,7 +38,7 @@ EXPORTED = [
     "mx_dequantize", "mx_requant_transpose", "mx_hadamard16", "mx_gemm", "mx_gemm_ex",
     "mx_gemm_grouped", "mx_gemm_quantize", "mx_gemm_quantize_a", "mx_quantize_batch", "mx_error_stats",
     "mx_quantize_batch_noalloc", "mx_route_workspace_bytes", "mx_route", "mx_route_backward", "mx_swiglu",
-    "mx_swiglu_backward", "mx_wgrad_grouped", "mx_combine", "mx_combine_backward", "mx_status_string",
+    "mx_swiglu_backward", "mx_wgrad_workspace_bytes", "mx_wgrad_grouped", "mx_combine", "mx_combine_backward", "mx_status_string",
 ]
 
 
@@ -114,7 +114,8 @@ def load():
         "mx_route_backward": (i32, [vp, i32, i64, vp, u32, RP, vp, vp, vp, i64, vp]),
         "mx_swiglu": (i32, [vp, i32, i64, i64, i64, vp, i64, TP, i32, _Rng, vp, vp]),
         "mx_swiglu_backward": (i32, [TP, vp, i32, i64, i64, i64, vp, i64, TP, vp]),
-        "mx_wgrad_grouped": (i32, [vp, i64, i64, i64, TP, vp, i32, vp, vp, i32, i64, u32, vp]),
+        "mx_wgrad_workspace_bytes": (ctypes.c_size_t, [i64, i64, i64, i32]),
+        "mx_wgrad_grouped": (i32, [vp, i64, i64, i64, TP, vp, i32, vp, vp, i32, i64, u32, vp, ctypes.c_size_t, vp]),
         "mx_combine": (i32, [vp, i32, i64, i64, i64, vp, vp, i64, i32, vp, i32, i64, vp]),
         "mx_combine_backward": (i32, [vp, i32, i64, vp, i64, i64, i64, vp, vp, i64, i32, vp, i64, vp, vp]),
         "mx_status_string": (ctypes.c_char_p, [i32]),
@@ -498,9 +499,16 @@ def mx_swiglu_backward(saved: MXTensor, dy, dh, y_saved: "MXTensor | None" = Non
     return dh
 
 
-def mx_wgrad_grouped(dY, X: MXTensor, row_index, num_groups: int, group_offsets, dW, flags: int = 0, stream=None):
+def mx_wgrad_workspace_bytes(routed_rows: int, N: int, K: int, num_groups: int) -> int:
+    return int(load().mx_wgrad_workspace_bytes(routed_rows, N, K, num_groups))
+
+
+def mx_wgrad_grouped(dY, X: MXTensor, row_index, num_groups: int, group_offsets, dW, flags: int = 0, workspace=None,
+                     stream=None):
     """dW [num_groups * N, K] (fp32 or bf16) = per group, dY^T [N, rows] times
-    the 8-bit rows of X (through row_index, if given)."""
+    the 8-bit rows of X (through row_index, if given).  workspace: a uint8
+    tensor of mx_wgrad_workspace_bytes(rows, N, K, num_groups); None takes it
+    from torch's allocator."""
     torch = _torch()
     _need(dY.dim() == 2 and dY.dtype == torch.bfloat16, "dY: a bf16 matrix expected")
     rows, N = dY.shape
@@ -508,9 +516,21 @@ def mx_wgrad_grouped(dY, X: MXTensor, row_index, num_groups: int, group_offsets,
     ld_dw = _rows_of(dW, num_groups * N, X.cols, "dW")
     index = _dense(row_index, torch.int32, (rows,), "row_index")
     offsets = _dense(group_offsets, torch.int64, (num_groups + 1,), "group_offsets")
+    L = load()
+    ws, size = None, 0
+    if workspace is None:
+        size = L.mx_wgrad_workspace_bytes(rows, N, X.cols, num_groups)
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=dY.device)
+            if stream is not None:
+                workspace.record_stream(stream)
+            ws = workspace.data_ptr()
+    else:
+        size = workspace.numel()
+        ws = _dense(workspace, torch.uint8, (size,), "workspace")
     d = X.desc()
-    _check(load().mx_wgrad_grouped(dY.data_ptr(), ld_dy, rows, N, ctypes.byref(d), index, num_groups, offsets,
-                                   dW.data_ptr(), _dt(dW), ld_dw, flags, _stream_of(stream)))
+    _check(L.mx_wgrad_grouped(dY.data_ptr(), ld_dy, rows, N, ctypes.byref(d), index, num_groups, offsets,
+                              dW.data_ptr(), _dt(dW), ld_dw, flags, ws, size, _stream_of(stream)))
     return dW
 
 

@@ -664,12 +664,20 @@ mx_status mx_swiglu_backward(const mx_tensor* saved, const void* dy, int32_t dt,
   return hip_status(mxk::launch_swiglu_bwd(a, reinterpret_cast<hipStream_t>(stream)));
 }
 
+size_t mx_wgrad_workspace_bytes(int64_t routed_rows, int64_t N, int64_t K, int32_t num_groups) {
+  if (routed_rows < 0 || routed_rows > INT32_MAX || N < 1 || N > INT32_MAX || K < 1 || K > INT32_MAX || num_groups < 1)
+    return 0;
+  return mxk::wgrad_workspace_bytes(routed_rows, N, K, num_groups);
+}
+
 mx_status mx_wgrad_grouped(const void* dY, int64_t ld_dy, int64_t routed_rows, int64_t N, const mx_tensor* X,
                            const int32_t* row_index, int32_t num_groups, const int64_t* group_offsets, void* dW,
-                           int32_t dwdt, int64_t ld_dw, uint32_t flags, mx_stream stream) {
+                           int32_t dwdt, int64_t ld_dw, uint32_t flags, void* workspace, size_t workspace_bytes,
+                           mx_stream stream) {
   if (!X) return MX_ERR_NULL;
   if (flags & ~MX_WGRAD_ACCUMULATE) return MX_ERR_UNSUPPORTED;
-  if (num_groups < 1 || routed_rows < 0 || routed_rows > INT32_MAX || N < 0) return MX_ERR_SHAPE;
+  if (num_groups < 1 || routed_rows < 0 || routed_rows > INT32_MAX || N < 0 || N > INT32_MAX)
+    return MX_ERR_SHAPE;
   mx_status st = check_saved(X, X->rows, X->cols);
   if (st != MX_OK) return st;
   if (row_index ? (routed_rows > 0 && X->rows == 0) : X->rows != routed_rows) return MX_ERR_SHAPE;
@@ -682,9 +690,16 @@ mx_status mx_wgrad_grouped(const void* dY, int64_t ld_dy, int64_t routed_rows, i
   st = check_output(dW, dwdt, num_groups * N, K, ld_dw);
   if (st != MX_OK) return st;
   if (N * K == 0) return MX_OK;
+  const size_t need = mxk::wgrad_workspace_bytes(routed_rows, N, K, num_groups);
+  if (need > 0) {
+    if (!workspace) return MX_ERR_NULL;
+    if (workspace_bytes < need) return MX_ERR_SHAPE;
+    if (!aligned16(workspace)) return MX_ERR_ALIGN;
+  }
   const mxk::WgradArgs a = {static_cast<const uint16_t*>(dY), ld_dy, routed_rows, N, X->fmt,
                             static_cast<const uint8_t*>(X->codes), X->scales, X->rows, K, row_index, group_offsets,
-                            num_groups, dW, (int)dwdt, ld_dw, (flags & MX_WGRAD_ACCUMULATE) != 0};
+                            num_groups, dW, (int)dwdt, ld_dw, (flags & MX_WGRAD_ACCUMULATE) != 0,
+                            static_cast<float*>(workspace)};
   return hip_status(mxk::launch_wgrad_grouped(a, reinterpret_cast<hipStream_t>(stream)));
 }
 

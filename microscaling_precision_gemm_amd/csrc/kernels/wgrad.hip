@@ -10,6 +10,7 @@
 // their rows, so the fragments are read transposed out of LDS
 // (ds_read_b64_tr_b16: 16 lanes turn 4 rows x 16 columns into 4 row values of
 // one column each).
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -35,6 +36,7 @@ struct WgradParams {
   const uint8_t* codes;
   const uint8_t* scales;
   int64_t x_rows, K;
+  uint32_t last_word;  // offset of the last 4 scale codes
   const int32_t* row_index;
   const int64_t* offsets;  // nullptr: one group of all rows
   int32_t groups;
@@ -42,6 +44,12 @@ struct WgradParams {
   int64_t ld_dw;
   uint32_t tn, tk;  // tiles along N and K
   uint32_t units;   // tiles of all groups, rounded up for the deal to the XCDs
+  // rows of a part of a group, a multiple of kStep; 0: groups are not split.
+  // Products of parts go to `parts`, a tile after the other, unless a group is
+  // one part; there is place for `slots` tiles.
+  int32_t len;
+  uint32_t slots;
+  float* parts;
   bool f32, accumulate, vec;
 };
 
@@ -63,14 +71,16 @@ __device__ __forceinline__ void stage_barrier() {
   asm volatile("" ::: "memory");
 }
 
+enum Kind { ANY_SHAPE, PLAIN_SHAPE, WHOLE_WORDS };
+
 // The variants.  WT: columns of a wave's tile (a workgroup's is T = 2 WT
-// square).  ANY: any N, K, pitch and size of X, otherwise dY in whole 16-byte
-// chunks, K a multiple of 128 (a scale code is then loaded as the aligned word
-// around it) and offsets within 32 bits.  GATHER: X's rows by the row index.
-template <int FMT_, int WT_, bool ANY_, bool GATHER_>
+// square).  ANY_SHAPE: any N, K, pitch and size of X, otherwise dY in whole 16-byte
+// chunks, at least 4 scale codes and offsets within 32 bits; WHOLE_WORDS: and
+// K a multiple of 128, so that the scale codes of a row of X are aligned words.  GATHER: X's rows by the row index.
+template <int FMT_, int WT_, int KIND, bool GATHER_>
 struct Variant {
   static constexpr int FMT = FMT_, WT = WT_;
-  static constexpr bool ANY = ANY_, GATHER = GATHER_;
+  static constexpr bool ANY = KIND == ANY_SHAPE, WORDS = KIND == WHOLE_WORDS, GATHER = GATHER_;
   static constexpr int F = WT / 32, T = 2 * WT;
   static constexpr int DC = kStep * T / 8 / 256;   // a thread's chunks of 8 dY columns in a stage,
   static constexpr int DR = 256 / (T / 8);         // and the rows between them
@@ -87,6 +97,7 @@ struct Unit {
   uint32_t n0, k0;
   int32_t e;         // group; -1: there is none
   int32_t row, cnt;  // its rows, at least one
+  int32_t slot;      // where its products go in p.parts; -1: to dW
   // Stages: at least 3, so that the copies, which run ahead of the products,
   // never reach past the tile after this one.
   __device__ __forceinline__ int32_t stages() const { return max((cnt + kStep - 1) / kStep, 3); }
@@ -104,6 +115,19 @@ __device__ __forceinline__ void clear_tile(const WgradParams& p, uint32_t e, uin
   }
 }
 
+// The rows of group e, clamped into [0, R].
+__device__ __forceinline__ void group_rows(const WgradParams& p, uint32_t e, int32_t& row, int32_t& cnt) {
+  int64_t lo = 0, hi = p.R;
+  if (p.offsets) {
+    lo = p.offsets[e];
+    hi = p.offsets[e + 1];
+    lo = lo < 0 ? 0 : (lo > p.R ? p.R : lo);
+    hi = hi < lo ? lo : (hi > p.R ? p.R : hi);
+  }
+  row = (int32_t)lo;
+  cnt = (int32_t)(hi - lo);
+}
+
 // Unit `id` or the next one of this workgroup that has rows.  The tiles of a
 // group are dealt to the 8 XCDs (workgroup id mod 8) in runs, n fastest, so
 // that the workgroups of an XCD share rows of dY and X in its L2.  A group
@@ -115,18 +139,68 @@ __device__ __forceinline__ Unit seek(const WgradParams& p, uint32_t& id) {
     const uint32_t slot = id >> 3, e = slot / per;
     const uint32_t in = (id & 7u) * per + (slot - e * per);
     if (in >= tiles) continue;
-    int64_t lo = 0, hi = p.R;
-    if (p.offsets) {  // clamped into [0, R]
-      lo = p.offsets[e];
-      hi = p.offsets[e + 1];
-      lo = lo < 0 ? 0 : (lo > p.R ? p.R : lo);
-      hi = hi < lo ? lo : (hi > p.R ? p.R : hi);
-    }
+    int32_t row, cnt;
+    group_rows(p, e, row, cnt);
     const uint32_t tk = in / p.tn, n0 = (in - tk * p.tn) * V::T, k0 = tk * V::T;
-    if (hi > lo) return {n0, k0, (int32_t)e, (int32_t)lo, (int32_t)(hi - lo)};
+    if (cnt > 0) return {n0, k0, (int32_t)e, row, cnt, -1};
     if (!p.accumulate) clear_tile<V>(p, e, n0, k0);
   }
-  return {0, 0, -1, 0, 1};
+  return {0, 0, -1, 0, 1, -1};
+}
+
+// Parts of the groups g0 .. g0 + 63, a lane each, summed over the lanes up to
+// this one.
+__device__ __forceinline__ int32_t parts_scan(const WgradParams& p, int32_t g0, uint32_t lane, int32_t& n) {
+  int32_t row, cnt = 0;
+  if (g0 + (int32_t)lane < p.groups) group_rows(p, g0 + lane, row, cnt);
+  n = (cnt + p.len - 1) / p.len;
+  int32_t sum = n;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int32_t o = __shfl_up(sum, d);
+    if ((int)lane >= d) sum += o;
+  }
+  return sum;
+}
+
+// Parts of all groups; 0 when they are not split.  (Offsets that break their
+// contract may give groups that share rows, and more parts than there is place
+// for: then no group is split.)
+__device__ __forceinline__ int32_t parts_of_all(const WgradParams& p, uint32_t lane) {
+  int32_t total = 0, n;
+  for (int32_t g0 = 0; g0 < p.groups; g0 += 64) total += __builtin_amdgcn_readlane(parts_scan(p, g0, lane, n), 63);
+  return (uint32_t)total * p.tn * p.tk <= p.slots ? total : 0;
+}
+
+// Group of part `part`, and that part's number within the group, of `of`.
+__device__ __forceinline__ int32_t group_of(const WgradParams& p, uint32_t lane, int32_t& part, int32_t& of) {
+  for (int32_t g0 = 0;; g0 += 64) {
+    int32_t n;
+    const int32_t sum = parts_scan(p, g0, lane, n);
+    const uint64_t past = __ballot(sum > part);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      of = __builtin_amdgcn_readlane(n, l);
+      part -= __builtin_amdgcn_readlane(sum, l) - of;
+      return g0 + l;
+    }
+    part -= __builtin_amdgcn_readlane(sum, 63);
+  }
+}
+
+// The only unit of workgroup `id` when groups are split into `total` parts:
+// part by part, each part's tiles next to one another and on one XCD as above.
+template <class V>
+__device__ __forceinline__ Unit seek_part(const WgradParams& p, uint32_t id, uint32_t lane, int32_t total) {
+  const uint32_t tiles = p.tn * p.tk, units = (uint32_t)total * tiles, per = (units + 7) / 8;
+  const uint32_t slot = (id & 7u) * per + (id >> 3);
+  if ((id >> 3) >= per || slot >= units) return {0, 0, -1, 0, 1, -1};
+  int32_t part = (int32_t)(slot / tiles), of, row, cnt;
+  const uint32_t in = slot - (uint32_t)part * tiles, tk = in / p.tn;
+  const int32_t e = group_of(p, lane, part, of);
+  group_rows(p, e, row, cnt);
+  return {(in - tk * p.tn) * V::T, tk * V::T, e, row + part * p.len, min(cnt - part * p.len, p.len),
+          of > 1 ? (int32_t)slot : -1};
 }
 
 // A position in the stream of stages.
@@ -162,7 +236,7 @@ template <class V>
 struct Copy {
   typedef typename std::conditional<V::ANY, uint64_t, uint32_t>::type Off;
   u4 d[V::DC], x[V::XC];
-  uint32_t sc[V::XC];
+  uint32_t sc[V::XC], sh[V::XC];
   // where the next loads take it from: byte offsets from uniform bases
   const char* dbase;
   const uint8_t* xbase;
@@ -183,8 +257,8 @@ struct Copy {
     xrow = tid / (V::T / 16);
     dput = drow * V::PITCH + 16u * place<V::T>(drow, dcol / 8);
     dput1 = V::DR == 8 ? dput ^ 32u : dput;
-    xput = V::HALF + xrow * V::PITCH + 16u * place<V::T>(xrow, xcol / 16 * 2);
     sc_shift = xcol / 32 % 4 * 8;
+    xput = V::HALF + xrow * V::PITCH + 16u * place<V::T>(xrow, xcol / 16 * 2);
   }
   __device__ __forceinline__ void flip() {  // to the other buffer
     dput ^= 2 * V::HALF;
@@ -205,16 +279,17 @@ __device__ __forceinline__ void load_rows(const WgradParams& p, const Cursor& at
                                                4u * (uint32_t)min((int32_t)lane, at.rem - 1));
 }
 
-// Aims the loads at the stage at `at` of tile u.  `fresh`: the tile, or the
+// Aims the loads at the stage at `at` of a tile at columns n0, k0.  `fresh`: the tile, or the
 // number of rows, is another than before; the lane offsets of full stages of
 // one tile are the same.
 template <class V>
-__device__ __forceinline__ void aim(const WgradParams& p, const Unit& u, const Cursor& at, bool fresh, Copy<V>& c) {
-  c.dbase = reinterpret_cast<const char*>(p.dy + (int64_t)at.row * p.ld_dy + u.n0);
+__device__ __forceinline__ void aim(const WgradParams& p, uint32_t n0, uint32_t k0, const Cursor& at, bool fresh,
+                                    Copy<V>& c) {
+  c.dbase = reinterpret_cast<const char*>(p.dy + (int64_t)at.row * p.ld_dy + n0);
   if (fresh || at.rem < kStep) {
     // columns past N and K are computed from others and not stored
-    const uint32_t cc = u.n0 + c.dcol < (uint32_t)p.N ? 2u * c.dcol : 0u;
-    c.kk = u.k0 + c.xcol < (uint32_t)p.K ? c.xcol : 0u;
+    const uint32_t cc = n0 + c.dcol < (uint32_t)p.N ? 2u * c.dcol : 0u;
+    c.kk = k0 + c.xcol < (uint32_t)p.K ? c.xcol : 0u;
     const uint32_t last = (uint32_t)min(at.rem, kStep) - 1u;
 #pragma unroll
     for (int i = 0; i < V::DC; ++i) {
@@ -228,7 +303,7 @@ __device__ __forceinline__ void aim(const WgradParams& p, const Unit& u, const C
     }
   }
   if constexpr (V::GATHER) {
-    c.xbase = p.codes + u.k0;
+    c.xbase = p.codes + k0;
     const uint32_t r = (uint32_t)min(max(c.ridx, 0), (int32_t)p.x_rows - 1);
     if constexpr (V::ANY) {
 #pragma unroll
@@ -240,7 +315,7 @@ __device__ __forceinline__ void aim(const WgradParams& p, const Unit& u, const C
       for (int i = 0; i < V::XC; ++i) c.xoff[i] = lane_read(o, c.xrow + i * V::XR) + c.kk;
     }
   } else {
-    c.xbase = p.codes + (int64_t)at.row * p.K + u.k0;
+    c.xbase = p.codes + (int64_t)at.row * p.K + k0;
   }
 }
 
@@ -262,13 +337,20 @@ template <class V>
 __device__ __forceinline__ void load_x(int i, Copy<V>& c) {
   c.x[i] = *reinterpret_cast<const u4*>(c.xbase + c.xoff[i]);
 }
-// Scale codes: one for 32 codes, so at 1/32 of the code offset from the start
-// (sbase: of the scales at the uniform part of it).
+// Scale codes: one for 32 codes, so at 1/32 of the code offset from the start.
+// The word from there on is loaded (as bytes the compiler would wait for them
+// at once), or the last word of the scales and the code is shifted down.
 template <class V>
 __device__ __forceinline__ void load_sc(const WgradParams& p, int i, Copy<V>& c) {
-  const uint8_t* sbase = p.scales + (uint64_t)(c.xbase - p.codes) / 32;
-  if constexpr (V::ANY) c.sc[i] = sbase[c.xoff[i] / 32];
-  else c.sc[i] = *reinterpret_cast<const uint32_t*>(sbase + ((c.xoff[i] >> 5) & ~3u));
+  if constexpr (V::ANY) c.sc[i] = p.scales[((uint64_t)(c.xbase - p.codes) + c.xoff[i]) / 32];
+  else if constexpr (V::WORDS) {
+    c.sc[i] = *reinterpret_cast<const uint32_t*>(p.scales + (((uint32_t)(c.xbase - p.codes) + c.xoff[i]) / 32 & ~3u));
+  } else {
+    typedef uint32_t __attribute__((aligned(1))) word;
+    const uint32_t o = (uint32_t)(c.xbase - p.codes) / 32 + c.xoff[i] / 32, in = min(o, p.last_word);
+    c.sc[i] = *reinterpret_cast<const word*>(p.scales + in);
+    c.sh[i] = (o - in) * 8;
+  }
 }
 
 // the thread's dY chunk i into LDS
@@ -284,7 +366,7 @@ struct Decoded {
 template <class V>
 __device__ __forceinline__ void decode_scale(int i, const Copy<V>& c, Decoded& d) {
   if constexpr (V::ANY) d.x = scale8<V::FMT>(c.sc[i]);
-  else d.x = scale8_word<V::FMT>(c.sc[i], c.sc_shift);
+  else d.x = scale8_word<V::FMT>(c.sc[i], V::WORDS ? c.sc_shift : c.sh[i]);
 }
 template <int P, class V>
 __device__ __forceinline__ void decode_pair(int i, const Copy<V>& c, Decoded& d) {
@@ -417,13 +499,14 @@ __device__ __forceinline__ void window(const WgradParams& p, uint32_t n0, Copy<V
 }
 
 // A wave's tile of products, 32 columns of N at a time and PC of K, through
-// 128 PC bytes of LDS of its own into rows of dW.  Chunk c of 4 columns of row
+// 128 PC bytes of LDS of its own into rows at dst.  Chunk c of 4 columns of row
 // r lies at chunk c ^ (r mod chunks): writes of 16 rows and reads of one row
-// are free of conflicts.  PLAIN: the tile lies inside dW, whose rows are
-// 16-byte aligned, and is not added to; otherwise chunk by chunk with checks.
+// are free of conflicts.  PLAIN: all of the tile is stored, its rows are
+// 16-byte aligned, and it is not added to; otherwise chunk by chunk with checks.
 template <int WDT, bool PLAIN, class V>
-__device__ __forceinline__ void store_tile(const WgradParams& p, const Unit& u, uint32_t wn, uint32_t wk, uint32_t lane,
-                                           const v16f (&acc)[V::F][V::F], uint32_t scratch) {
+__device__ __forceinline__ void store_tile(const WgradParams& p, const Unit& u, void* dst, int64_t ld, uint32_t wn,
+                                           uint32_t wk, uint32_t lane, const v16f (&acc)[V::F][V::F],
+                                           uint32_t scratch) {
   constexpr int PC = V::WT / 2;                // columns of a pass
   constexpr int CH = PC / 4;                   // 16-byte chunks of a scratch row
   constexpr int CPL = WDT == DT_F32 ? 1 : 2;   // chunks a lane stores
@@ -435,9 +518,8 @@ __device__ __forceinline__ void store_tile(const WgradParams& p, const Unit& u, 
   const uint32_t lr = lane & 31u, lg = lane >> 5;
   const uint32_t rr = lane / (CH / CPL), cc = lane % (CH / CPL) * CPL;
   const uint32_t wbase = scratch + lr * (PC * 4), wx = lg ^ (lr & (CH - 1));
-  uint8_t* base = static_cast<uint8_t*>(p.dw) +
-                  (((int64_t)u.e * p.N + u.n0 + wn) * p.ld_dw + u.k0 + wk) * EB;  // uniform
-  const int64_t loff = ((int64_t)rr * p.ld_dw + 4 * cc) * EB;
+  uint8_t* base = static_cast<uint8_t*>(dst) + ((int64_t)wn * ld + wk) * EB;  // uniform
+  const int64_t loff = ((int64_t)rr * ld + 4 * cc) * EB;
 #pragma unroll
   for (int j = 0; j < V::F; ++j)
 #pragma unroll
@@ -460,7 +542,7 @@ __device__ __forceinline__ void store_tile(const WgradParams& p, const Unit& u, 
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[4 * k + e] = x[e];
         }
-        uint8_t* at = base + ((int64_t)(32 * j + t * RPI) * p.ld_dw + PC * h) * EB + loff;
+        uint8_t* at = base + ((int64_t)(32 * j + t * RPI) * ld + PC * h) * EB + loff;
         if constexpr (PLAIN) {
           if constexpr (WDT == DT_F32) *reinterpret_cast<f4*>(at) = f4{o[0], o[1], o[2], o[3]};
           else *reinterpret_cast<u4*>(at) = u4{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
@@ -506,20 +588,27 @@ k_wgrad(WgradParams p) {
   }
 
   uint32_t id = blockIdx.x;
-  Unit tile = seek<V>(p, id);  // whose products run
+  Unit tile;  // whose products run
+  const int32_t parts = p.len ? parts_of_all(p, lane) : 0;
+  if (parts) {
+    tile = seek_part<V>(p, id, lane, parts);
+    id = p.units;  // there is no other
+  } else {
+    tile = seek<V>(p, id);
+  }
   if (tile.e < 0) return;
-  Unit next = {0, 0, -1, 0, 1};  // the one after it, once the row cursor has come to it
+  Unit next = {0, 0, -1, 0, 1, -1};  // the one after it, once the row cursor has come to it
   Cursor rows, load, put;        // the stages whose row numbers are loaded, that are loaded, that are written
   rows.start(tile);
   load.start(tile);
   put.start(tile);
   int32_t left = put.left;
-  uint32_t n0 = tile.n0;  // of the tile that is loaded
+  uint32_t n0 = tile.n0, k0 = tile.k0;  // of the tile that is loaded
 
   Copy<V> c;
   c.init(tid);
   load_rows(p, rows, lane, c);
-  aim(p, tile, load, true, c);
+  aim(p, n0, k0, load, true, c);
 #pragma unroll
   for (int i = 0; i < V::DC; ++i) load_d(p, n0, i, c);
 #pragma unroll
@@ -531,7 +620,7 @@ k_wgrad(WgradParams p) {
   rows.step(next);
   load_rows(p, rows, lane, c);
   load.step(next);
-  aim(p, tile, load, false, c);
+  aim(p, n0, k0, load, false, c);
   copy_share<0>(p, n0, c);
   copy_share<1>(p, n0, c);
   copy_share<2>(p, n0, c);
@@ -542,7 +631,7 @@ k_wgrad(WgradParams p) {
   rows.step(next);
   load_rows(p, rows, lane, c);
   load.step(next);
-  aim(p, tile, load, false, c);
+  aim(p, n0, k0, load, false, c);
   stage_barrier();
   Frags<F> f[2];
   read_frags<V::WT>(0, noff, koff, f[0]);
@@ -580,8 +669,11 @@ k_wgrad(WgradParams p) {
         put.left = next.e >= 0 ? next.stages() : INT32_MAX;
       }
       const bool fresh = load.step(next);
-      if (fresh) n0 = next.n0;
-      aim(p, fresh ? next : tile, load, fresh, c);
+      if (fresh) {
+        n0 = next.n0;
+        k0 = next.k0;
+      }
+      aim(p, n0, k0, load, fresh, c);
       c.flip();  // the other buffer is read from here on, and this one written
 #pragma unroll
       for (int i = 0; i < F; ++i) {
@@ -593,12 +685,18 @@ k_wgrad(WgradParams p) {
     } while (--left != 0);
     const bool inside = p.vec && !p.accumulate && (int64_t)tile.n0 + T <= p.N && (int64_t)tile.k0 + T <= p.K;
     const uint32_t scratch = 4 * V::HALF + wid * V::SCRATCH;
-    if (p.f32) {
-      if (inside) store_tile<DT_F32, true, V>(p, tile, wn, wk, lane, acc, scratch);
-      else store_tile<DT_F32, false, V>(p, tile, wn, wk, lane, acc, scratch);
+    int64_t ld = p.ld_dw;
+    void* dst = static_cast<uint8_t*>(p.dw) + (((int64_t)tile.e * p.N + tile.n0) * ld + tile.k0) * (p.f32 ? 4 : 2);
+    if (tile.slot >= 0) {
+      ld = T;
+      dst = p.parts + (int64_t)tile.slot * (T * T);
+    }
+    if (p.f32 || tile.slot >= 0) {
+      if (inside || tile.slot >= 0) store_tile<DT_F32, true, V>(p, tile, dst, ld, wn, wk, lane, acc, scratch);
+      else store_tile<DT_F32, false, V>(p, tile, dst, ld, wn, wk, lane, acc, scratch);
     } else {
-      if (inside) store_tile<DT_BF16, true, V>(p, tile, wn, wk, lane, acc, scratch);
-      else store_tile<DT_BF16, false, V>(p, tile, wn, wk, lane, acc, scratch);
+      if (inside) store_tile<DT_BF16, true, V>(p, tile, dst, ld, wn, wk, lane, acc, scratch);
+      else store_tile<DT_BF16, false, V>(p, tile, dst, ld, wn, wk, lane, acc, scratch);
     }
     if (next.e < 0) break;
     tile = next;
@@ -606,8 +704,107 @@ k_wgrad(WgradParams p) {
   }
 }
 
+// dW of the groups that were split, and of those without rows: the products of
+// a group's parts are added in their order.  A workgroup does 1024 elements of
+// a tile of T x T, a thread 4 of a row.
+__global__ __launch_bounds__(256) void k_wgrad_join(WgradParams p, uint32_t T) {
+  const uint32_t lane = threadIdx.x & 63u, pieces = T * T / 1024, tiles = p.tn * p.tk;
+  const uint32_t at = blockIdx.x / pieces, e = at / tiles, in = at - e * tiles;
+  if (!parts_of_all(p, lane)) return;
+  int32_t first = 0, n = 0;
+  for (int32_t g0 = 0;; g0 += 64) {
+    const int32_t sum = parts_scan(p, g0, lane, n);
+    const int l = (int)min(e - g0, 63u);
+    first += __builtin_amdgcn_readlane(sum, l);
+    if (e < g0 + 64u) {
+      n = __builtin_amdgcn_readlane(n, l);
+      first -= n;
+      break;
+    }
+  }
+  if (n == 1 || (n == 0 && p.accumulate)) return;
+  const uint32_t q = ((blockIdx.x - at * pieces) * 256 + threadIdx.x) * 4;  // in the tile
+  const int64_t row = (int64_t)(in % p.tn) * T + q / T, col = (int64_t)(in / p.tn) * T + q % T;
+  if (row >= p.N || col >= p.K) return;
+  const float* src = p.parts + ((int64_t)first * tiles + in) * T * T + q;
+  const int64_t pitch = (int64_t)tiles * T * T;
+  f4 o = {0, 0, 0, 0};
+  int i = 0;
+  for (; i + 4 <= n; i += 4) {
+    f4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const f4*>(src + (i + j) * pitch);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o += v[j];
+  }
+  for (; i < n; ++i) o += *reinterpret_cast<const f4*>(src + i * pitch);
+  const int64_t off = ((int64_t)e * p.N + row) * p.ld_dw + col;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (p.f32) {
+      float* d = static_cast<float*>(p.dw) + off + k;
+      *d = p.accumulate ? o[k] + *d : o[k];
+    } else {
+      uint8_t* d = static_cast<uint8_t*>(p.dw);
+      store1<DT_BF16>(d, off + k, p.accumulate ? o[k] + load1<DT_BF16>(d, off + k) : o[k]);
+    }
+  }
+}
+
+// The tile of a call and whether the rows of its groups are split: len rows a
+// part (0: no), at most `units` parts of tiles in all (R rows in parts of len
+// make at most (R + groups (len - 1)) / len parts).  Measured, E4M3 to FP32:
+//   rows x N x K, groups     128, whole  128, parts  256, whole  256, parts
+//   32768 x 64 x 1024, 1         351          34         667          43 us
+//   32768 x 2048 x 2048, 1       421         382          -          283
+//   32768 x 1024 x 1024, 4       151          -           -           96
+//   8192 x 256 x 512, 16         15.7         28          -           32
+//   2000 x 1024 x 1024, 20       24           -           32          -
+//   16384 x 512 x 1024, 32       37           -           33          -
+//   32768 x 2048 x 2048, 4       316          -          287          -
+struct Plan {
+  int64_t T, len, units;
+  float us;
+};
+int64_t most_of(int64_t T) { return T == 256 ? 256 : 512; }  // workgroups that the 256 CUs hold at once
+
+// Estimated time of a plan.  A round of tiles at once takes as long as its
+// longest group, so with one round that is taken to be a quarter longer than
+// the mean; more rounds even that out.
+float time_of(int64_t R, int64_t groups, int64_t tiles, int64_t T, int64_t len) {
+  const int64_t most = most_of(T), units = len ? (R + groups * (len - 1) / 2) / len * tiles : groups * tiles;
+  const float stages = std::max((float)(len ? len : (R + groups - 1) / groups) / kStep, 3.0f) + 2;
+  const float full = (float)(units / most), rest = (float)(units % most);
+  const float last = rest == 0 ? 0.0f : T == 256 ? 2.1f : rest > 256 ? 1.25f : 0.85f;
+  const float round = T == 256 ? 2.1f : 1.25f;
+  const float uneven = len || groups == 1 ? 1.0f : 1.0f + 0.25f / (full + (rest > 0));
+  const float join = len ? 5.0f + units * (T * T * 8) / 5e6f : 0.0f;
+  return (full * round + last) * stages * uneven + join;
+}
+
+// The plan with the least time among 128 x 128 tiles, 256 x 256 tiles (if they
+// may be taken) and parts of R / 2, R / 3, R / 4, R / 6, R / 8 ... rows.
+Plan plan_of(int64_t R, int64_t N, int64_t K, int64_t groups, bool large) {
+  Plan best = {};
+  for (int64_t T = 128; T <= (large ? 256 : 128); T *= 2) {
+    const int64_t tiles = ((N + T - 1) / T) * ((K + T - 1) / T);
+    const float us = time_of(R, groups, tiles, T, 0);
+    if (T == 128 || us < best.us) best = {T, 0, 0, us};
+    if (groups > 512) continue;
+    for (int64_t i = 0; i < 18; ++i) {
+      const int64_t n = (i & 1 ? 3 : 2) << (i / 2);
+      const int64_t len = ((R + n - 1) / n + kStep - 1) / kStep * kStep;
+      const int64_t units = (R + groups * (len - 1)) / std::max<int64_t>(len, 1) * tiles;
+      if (len < 3 * kStep || len > INT32_MAX || units > 2 * most_of(T)) break;
+      const float us = time_of(R, groups, tiles, T, len);
+      if (us < best.us) best = {T, len, units, us};
+    }
+  }
+  return best;
+}
+
 template <class V>
-hipError_t launch_v(const WgradArgs& a, hipStream_t s) {
+hipError_t launch_v(const WgradArgs& a, const Plan& plan, hipStream_t s) {
   WgradParams p = {};
   p.dy = a.dy;
   p.ld_dy = a.ld_dy;
@@ -617,6 +814,7 @@ hipError_t launch_v(const WgradArgs& a, hipStream_t s) {
   p.scales = a.scales;
   p.x_rows = a.x_rows;
   p.K = a.K;
+  p.last_word = (uint32_t)(a.x_rows * a.K / 32 - 4);
   p.row_index = a.row_index;
   p.offsets = a.offsets;
   p.groups = a.groups;
@@ -630,6 +828,14 @@ hipError_t launch_v(const WgradArgs& a, hipStream_t s) {
   const int64_t units = ((int64_t)p.tn * p.tk + 7) / 8 * 8 * a.groups;
   if (units > UINT32_MAX / 2) return hipErrorInvalidValue;
   p.units = (uint32_t)units;
+  const uint32_t most = (uint32_t)most_of(V::T);
+  uint32_t grid = p.units < most ? p.units : most;
+  if (plan.len) {
+    p.len = (int32_t)plan.len;
+    p.parts = a.parts;
+    p.slots = (uint32_t)plan.units;
+    grid = (p.slots + 7) / 8 * 8;
+  }
   auto kern = k_wgrad<V>;
   // the dynamic LDS limit is raised once per device
   static std::atomic<uint64_t> attr_done{0};
@@ -642,20 +848,21 @@ hipError_t launch_v(const WgradArgs& a, hipStream_t s) {
     if (e != hipSuccess) return e;
     attr_done.fetch_or(bit, std::memory_order_acq_rel);
   }
-  // as many workgroups as the 256 CUs hold at once
-  const uint32_t most = V::WT == 128 ? 256 : 512;
-  hipLaunchKernelGGL(kern, dim3(p.units < most ? p.units : most), dim3(256), V::LDS, s, p);
+  hipLaunchKernelGGL(kern, dim3(grid), dim3(256), V::LDS, s, p);
+  if (plan.len)
+    hipLaunchKernelGGL(k_wgrad_join, dim3(p.tn * p.tk * (uint32_t)p.groups * (V::T * V::T / 1024)), dim3(256), 0, s, p,
+                       (uint32_t)V::T);
   return hipGetLastError();
 }
 
 template <int FMT, bool GATHER>
 hipError_t launch_g(const WgradArgs& a, hipStream_t s) {
-  if (a.N % 8 || a.ld_dy >= (1 << 24) || a.K % 128 || a.x_rows * a.K >= (int64_t)UINT32_MAX)
-    return launch_v<Variant<FMT, 64, true, GATHER>>(a, s);
-  // 256 x 256 tiles when they fill the CUs, else 128 x 128
-  const int64_t big = ((a.N + 255) / 256) * ((a.K + 255) / 256) * a.groups;
-  return big >= 256 ? launch_v<Variant<FMT, 128, false, GATHER>>(a, s)
-                    : launch_v<Variant<FMT, 64, false, GATHER>>(a, s);
+  if (a.N % 8 || a.ld_dy >= (1 << 24) || a.x_rows * a.K < 128 || a.x_rows * a.K >= (int64_t)UINT32_MAX)
+    return launch_v<Variant<FMT, 64, ANY_SHAPE, GATHER>>(a, plan_of(a.R, a.N, a.K, a.groups, false), s);
+  const Plan plan = plan_of(a.R, a.N, a.K, a.groups, true);
+  if (plan.T == 128) return launch_v<Variant<FMT, 64, PLAIN_SHAPE, GATHER>>(a, plan, s);
+  return a.K % 128 ? launch_v<Variant<FMT, 128, PLAIN_SHAPE, GATHER>>(a, plan, s)
+                   : launch_v<Variant<FMT, 128, WHOLE_WORDS, GATHER>>(a, plan, s);
 }
 
 template <int FMT>
@@ -664,6 +871,14 @@ hipError_t launch_f(const WgradArgs& a, hipStream_t s) {
 }
 
 }  // namespace
+
+size_t wgrad_workspace_bytes(int64_t R, int64_t N, int64_t K, int64_t groups) {
+  const auto bytes = [&](bool large) {
+    const Plan plan = plan_of(R, N, K, groups, large);
+    return (size_t)(plan.units * plan.T * plan.T) * sizeof(float);
+  };
+  return std::max(bytes(false), bytes(true));
+}
 
 hipError_t launch_wgrad_grouped(const WgradArgs& a, hipStream_t s) {
   if (a.fmt == FMT_MXFP8) return launch_f<FMT_MXFP8>(a, s);

@@ -233,7 +233,9 @@ struct WgradArgs {
   int dwdt;
   int64_t ld_dw;
   bool accumulate;
+  float* parts;  // wgrad_workspace_bytes(R, N, K, groups) of them
 };
+size_t wgrad_workspace_bytes(int64_t R, int64_t N, int64_t K, int64_t groups);
 hipError_t launch_wgrad_grouped(const WgradArgs& a, hipStream_t s);
 
 }  // namespace mxk

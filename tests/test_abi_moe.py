@@ -117,8 +117,9 @@ def test_swiglu_backward(mx):
 def test_wgrad(mx):
     L = mx.load()
 
-    def call(x, dy=FAKE, ld=64, rows=4, n=64, index=None, groups=2, off=FAKE, dw=FAKE, dt=1, ldw=128, flags=0):
-        return L.mx_wgrad_grouped(dy, ld, rows, n, x, index, groups, off, dw, dt, ldw, flags, None)
+    def call(x, dy=FAKE, ld=64, rows=4, n=64, index=None, groups=2, off=FAKE, dw=FAKE, dt=1, ldw=128, flags=0,
+             ws=None, size=0):
+        return L.mx_wgrad_grouped(dy, ld, rows, n, x, index, groups, off, dw, dt, ldw, flags, ws, size, None)
 
     ok = saved(mx)
     assert call(None) == NUL and call(ok, dy=None) == NUL and call(ok, dw=None) == NUL
@@ -133,6 +134,15 @@ def test_wgrad(mx):
     assert call(ok, ld=68) == ALIGN and call(ok, dy=FAKE + 2) == ALIGN and call(ok, dw=FAKE + 2) == ALIGN
     assert call(ok, index=FAKE + 2) == ALIGN and call(ok, off=FAKE + 4) == ALIGN
     assert call(ok, n=0, dy=None, dw=None) == 0
+    # one tile of dW and many rows: summed in parts
+    need = mx.mx_wgrad_workspace_bytes(8192, 64, 128, 1)
+    assert need > 0 and need % 4 == 0
+    long = dict(x=saved(mx, rows=8192), rows=8192, groups=1, off=None)
+    assert call(**long) == NUL and call(**long, ws=FAKE, size=need - 1) == SHAPE
+    assert call(**long, ws=FAKE + 8, size=need) == ALIGN
+    for args in ((-1, 64, 128, 1), (8192, 0, 128, 1), (8192, 64, 0, 1), (8192, 64, 128, 0), (0, 64, 128, 1),
+                 (4096, 4096, 4096, 1), (1 << 31, 64, 128, 1)):
+        assert mx.mx_wgrad_workspace_bytes(*args) == 0
 
 
 def test_combine(mx):

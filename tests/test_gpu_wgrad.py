@@ -81,6 +81,81 @@ def test_larger_tiles(rows, groups, N, K):
         check(*case(rows, groups, N, K, fmt, 2), "bf16")
 
 
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp8_e5m2", "mxint8"])
+@pytest.mark.parametrize("rows,groups,N,K", [(5000, 64, 264, 512), (3000, 140, 256, 288), (9000, 70, 392, 512)])
+def test_many_tiles(rows, groups, N, K, fmt):
+    """Enough tiles of 256 x 256 for the larger ones, one or several a workgroup;
+    groups of no, a few and many steps of rows, tiles that lie partly outside."""
+    for gather in (False, True):
+        args = case(rows, groups, N, K, fmt, 11 + gather, gather, empty=(0, 5, groups - 1))
+        check(*args, "bf16" if gather else "f32")
+        check(*args, "f32" if gather else "bf16", pad=5, accumulate=True)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxint8"])
+@pytest.mark.parametrize("rows,groups,N,K,empty", [(8192, 1, 64, 128, ()), (5000, 3, 129, 160, (1,)),
+                                                   (6000, 7, 40, 288, (0, 2, 6)), (20000, 70, 16, 96, (0, 64, 69)),
+                                                   (150000, 70, 16, 96, (0, 64, 69)),
+                                                   (3001, 2, 264, 512, ()), (9000, 5, 1, 64, (4,))])
+def test_few_tiles_and_many_rows(rows, groups, N, K, empty, fmt):
+    """The rows of a group are summed in parts: groups of one part, of many, of
+    none."""
+    assert (rows, groups) == (20000, 70) or mx.mx_wgrad_workspace_bytes(rows, N, K, groups) > 0
+    for gather in (False, True):
+        args = case(rows, groups, N, K, fmt, 21 + gather, gather, empty=empty)
+        check(*args, "bf16" if gather else "f32")
+        check(*args, "f32" if gather else "bf16", pad=5, accumulate=True)
+
+
+def test_parts_with_offsets_that_break_their_contract_and_repeats():
+    dy, X, _, _ = case(6000, 4, 64, 128, "mxfp8", 23)
+    for off in ([-5, 4000, 3000, 9000, 6000], [5000, 6000, 2000, 2000, 1 << 40], [-1, -1, -1, -1, -1],
+                [6000, 0, 6000, 0, 6000], [0, 6000, 0, 6000, 0]):
+        at = torch.tensor(off, dtype=torch.int64, device=dev())
+        outs = []
+        ws = torch.full((mx.mx_wgrad_workspace_bytes(6000, 64, 128, 4),), 0xFF, dtype=torch.uint8, device=dev())
+        for w in (ws, None, ws):
+            dw = torch.full((4 * 64, 128), 3.0, device=dev())
+            mx.mx_wgrad_grouped(dy, X, None, 4, at, dw, workspace=w)
+            torch.cuda.synchronize()
+            outs.append(dw)
+        assert all(torch.equal(o, outs[0]) for o in outs)
+        a, x = dy.cpu().double().numpy(), decoded(X)
+        for e in range(4):
+            lo = min(max(off[e], 0), 6000)
+            hi = min(max(off[e + 1], lo), 6000)
+            assert np.allclose(outs[0][64 * e : 64 * e + 64].cpu().numpy(), a[lo:hi].T @ x[lo:hi], rtol=1e-4, atol=2e-2)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxint8"])
+@pytest.mark.parametrize("rows,groups,N,K", [(9000, 20, 1032, 1024), (6000, 33, 776, 1056), (3000, 36, 640, 576),
+                                             (4000, 45, 33, 2112)])
+def test_tiles_of_a_workgroup_at_other_columns(rows, groups, N, K, fmt):
+    """Several tiles a workgroup, each at other columns than the one before."""
+    for gather in (False, True):
+        check(*case(rows, groups, N, K, fmt, 31 + gather, gather, empty=(3, groups - 2)), "bf16" if gather else "f32")
+
+
+def test_many_tiles_nan_scale_row_index_and_repeats():
+    dy, X, index, off = case(4000, 64, 264, 512, "mxfp8", 13, True)
+    lo, hi = int(off[9]), int(off[10])
+    assert hi > lo
+    X.scales[int(index[lo]), 2] = 0xFF
+    index[lo + 1 :][index[lo + 1 :] == index[lo]] = (int(index[lo]) + 1) % X.rows
+    index[:lo][index[:lo] == index[lo]] = (int(index[lo]) + 1) % X.rows
+    outs = []
+    for _ in range(3):
+        dw = torch.empty(64 * 264, 512, device=dev())
+        mx.mx_wgrad_grouped(dy, X, index, 64, off, dw)
+        torch.cuda.synchronize()
+        outs.append(dw)
+    bad = torch.isnan(outs[0]).cpu().numpy()
+    want = np.zeros_like(bad)
+    want[9 * 264 : 10 * 264, 64:96] = True
+    assert np.array_equal(bad, want)
+    assert all(torch.equal(o.nan_to_num(7.0), outs[0].nan_to_num(7.0)) for o in outs)
+
+
 def test_groups_without_rows_and_accumulation():
     for kind in DT:
         for gather in (False, True):
