@@ -544,9 +544,10 @@ __device__ __forceinline__ void store_tile(const WgradParams& p, const Unit& u, 
         }
         uint8_t* at = base + ((int64_t)(32 * j + t * RPI) * ld + PC * h) * EB + loff;
         if constexpr (PLAIN) {
-          if constexpr (WDT == DT_F32) *reinterpret_cast<f4*>(at) = f4{o[0], o[1], o[2], o[3]};
-          else *reinterpret_cast<u4*>(at) = u4{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
-                                              pack_bf16(o[6], o[7])};
+          // streaming stores: the rows of dY and X stay in the L2
+          if constexpr (WDT == DT_F32) __builtin_nontemporal_store(f4{o[0], o[1], o[2], o[3]}, reinterpret_cast<f4*>(at));
+          else __builtin_nontemporal_store(u4{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
+                                              pack_bf16(o[6], o[7])}, reinterpret_cast<u4*>(at));
         } else {
           // (K is a multiple of 32: a lane's columns are all inside or outside)
           const bool in = (int64_t)u.n0 + wn + 32 * j + r < p.N && (int64_t)u.k0 + wk + PC * h + 4 * cc < p.K;
