@@ -12,6 +12,10 @@
 // Bound by HBM.  A lane takes 8 consecutive gate elements and the 8 up
 // elements beside them, a lane quad one 32-element block of each half, so the
 // block maxima need two DPP steps and h is read once for both results.
+// Measured, 32768 x 2048 BF16: forward 70 us (5.8 TB/s), with an MXFP8
+// checkpoint and max |y| 110 us (4.9 TB/s: few workgroups, see kMaxGrid),
+// backward 92 us (5.9 TB/s), and with the operand of the next weight gradient
+// 108 us (5.6 TB/s).
 #include "../device/codec.h"
 #include "../device/cvt.h"
 #include "../device/decode8.h"

@@ -10,6 +10,18 @@
 // their rows, so the fragments are read transposed out of LDS
 // (ds_read_b64_tr_b16: 16 lanes turn 4 rows x 16 columns into 4 row values of
 // one column each).
+//
+// Bounds.  The matrix unit, where groups are long: 256 x 256 tiles, a wave of
+// 128 x 128 to each SIMD with all of its products in accumulators, every other
+// instruction placed behind a product, run at the power-limited rate of the
+// BF16 instruction on random data (each further 65536 rows x 2048 x 7168: 1566
+// us, 1229 TFLOP/s).  What a tile costs besides is its store: with one wave a
+// SIMD nothing runs beside it, and 256 tiles of 256 KB leave at the rate of
+// HBM.  32768 rows in 32 uneven groups x 2048 x 7168 E4M3, gathered: 1063 us
+// (905 TFLOP/s; 1.88 GB of FP32 output, 3.3 GB past the L2s in).  Spreading the
+// workgroups' phases by waits of 2 .. 36 us did not pay (1200 .. 1230 us
+// against 1217 with even groups).  Short groups are bound by latency: a tile's
+// first loads, three stages and its store are 8 us.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
