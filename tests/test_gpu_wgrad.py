@@ -226,6 +226,29 @@ def test_extreme_scales():
             assert np.all(np.abs(dw.cpu().double().numpy() - want) <= 2.0 ** -19 * np.abs(want) + rows * 2.0 ** -133)
 
 
+def test_gradient_against_differences():
+    """f(W) = sum over the rows r of group e of <dY[r], W_e X[src(r)]> is linear
+    in W, so its difference quotients in 64 bits are exact but for 2^-52 |f| /
+    step, far below the bound of the kernel's sums."""
+    dy, X, index, off = case(90, 3, 16, 64, "mxfp8", 14, True)
+    dw = torch.empty(48, 64, device=dev())
+    mx.mx_wgrad_grouped(dy, X, index, 3, off, dw)
+    torch.cuda.synchronize()
+    a, x, o = dy.cpu().double().numpy(), decoded(X)[index.cpu().numpy()], off.tolist()
+    g = np.random.default_rng(1)
+    W = g.standard_normal((3, 16, 64))
+
+    def f(W):
+        return sum(float(np.sum(a[o[e]:o[e + 1]] * (x[o[e]:o[e + 1]] @ W[e].T))) for e in range(3))
+
+    for _ in range(20):
+        e, n, k = g.integers(3), g.integers(16), g.integers(64)
+        D = np.zeros_like(W)
+        D[e, n, k] = 0.5
+        mag = float(np.sum(np.abs(a[o[e]:o[e + 1], n] * x[o[e]:o[e + 1], k])))
+        assert abs(float(dw[e * 16 + n, k]) - (f(W + D) - f(W - D))) <= 92 * 2.0 ** -23 * mag + 1e-9
+
+
 def test_repeats_bit_for_bit_and_on_another_stream():
     dy, X, index, off = case(3000, 5, 264, 544, "mxfp8", 10, True)
     first = torch.empty(5 * 264, 544, device=dev())
