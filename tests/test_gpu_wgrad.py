@@ -107,6 +107,30 @@ def test_few_tiles_and_many_rows(rows, groups, N, K, empty, fmt):
         check(*args, "f32" if gather else "bf16", pad=5, accumulate=True)
 
 
+@pytest.mark.parametrize("rows,groups,N,K,fmt", [(32768, 1, 2048, 2048, "mxfp8"), (32768, 4, 1024, 1056, "mxint8"),
+                                                 (20000, 3, 1032, 1024, "mxfp8_e5m2")])
+def test_parts_of_large_tiles(rows, groups, N, K, fmt):
+    """Parts where the larger tiles are chosen (the reference on the GPU)."""
+    assert mx.mx_wgrad_workspace_bytes(rows, N, K, groups) > 0
+    g = torch.Generator(device="cuda").manual_seed(rows + groups)
+    X = mx.empty(mx.FORMATS[fmt], rows, K, dev())
+    mx.mx_quantize(torch.randn(rows, K, generator=g, device=dev()), X)
+    x = torch.empty(rows, K, device=dev())
+    mx.mx_dequantize(X, x)
+    dy = torch.randn(rows, N, generator=g, device=dev()).to(torch.bfloat16)
+    cuts = [0] + sorted(torch.randint(0, rows, (groups - 1,), generator=g, device=dev()).tolist()) + [rows]
+    off = None if groups == 1 else torch.tensor(cuts, dtype=torch.int64, device=dev())
+    index = torch.randperm(rows, generator=g, device=dev()).int()
+    for idx in (None, index):
+        dw = torch.empty(groups * N, K, device=dev())
+        mx.mx_wgrad_grouped(dy, X, idx, groups, off, dw)
+        src = x if idx is None else x[idx.long()]
+        for e, (a, b) in enumerate(zip(cuts, cuts[1:])):
+            d, v = dy[a:b].double().t().contiguous(), src[a:b].double()
+            tol = (b - a + 2) * 2.0 ** -23 * (d.abs() @ v.abs())
+            assert ((dw[e * N:(e + 1) * N].double() - d @ v).abs() <= tol).all(), e
+
+
 def test_parts_with_offsets_that_break_their_contract_and_repeats():
     dy, X, _, _ = case(6000, 4, 64, 128, "mxfp8", 23)
     for off in ([-5, 4000, 3000, 9000, 6000], [5000, 6000, 2000, 2000, 1 << 40], [-1, -1, -1, -1, -1],
