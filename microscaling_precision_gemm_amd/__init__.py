@@ -38,7 +38,8 @@ EXPORTED = [
     "mx_dequantize", "mx_requant_transpose", "mx_hadamard16", "mx_gemm", "mx_gemm_ex",
     "mx_gemm_grouped", "mx_gemm_quantize", "mx_gemm_quantize_a", "mx_quantize_batch", "mx_error_stats",
     "mx_quantize_batch_noalloc", "mx_route_workspace_bytes", "mx_route", "mx_route_backward", "mx_swiglu",
-    "mx_swiglu_backward", "mx_wgrad_workspace_bytes", "mx_wgrad_grouped", "mx_combine", "mx_combine_backward", "mx_status_string",
+    "mx_swiglu_backward", "mx_wgrad_workspace_bytes", "mx_wgrad_grouped", "mx_combine",
+    "mx_combine_backward", "mx_status_string",
 ]
 
 

@@ -1,6 +1,6 @@
 // rows.h -- 8-element chunks of BF16 / FP32 rows, used by the kernels around
 // the expert products: loads and stores of a whole chunk (16 or 32 bytes,
-// 16-byte aligned) and of the first n elements of one.
+// 16-byte aligned) and of one element.
 #pragma once
 #include <stdint.h>
 
@@ -15,13 +15,6 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 __device__ inline uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
 }
-
-template <int DT>
-struct Elem;
-template <>
-struct Elem<DT_BF16> { typedef uint16_t T; };
-template <>
-struct Elem<DT_F32> { typedef float T; };
 
 template <int DT>
 __device__ inline float load1(const void* p, int64_t off) {
@@ -62,30 +55,6 @@ __device__ inline void store8(void* __restrict__ p, int64_t off, const float (&v
     float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + off);
     q[0] = make_float4(v[0], v[1], v[2], v[3]);
     q[1] = make_float4(v[4], v[5], v[6], v[7]);
-  }
-}
-
-// The first n (1..8) elements of a chunk; the others read as 0 and are not
-// touched in memory (a row may end exactly at its last column).  `whole`: the
-// chunk is 16-byte aligned and n == 8.
-template <int DT>
-__device__ inline void load_n(const void* __restrict__ p, int64_t off, int n, bool whole, float (&v)[8]) {
-  if (whole) {
-    load8<DT>(p, off, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? load1<DT>(p, off + i) : 0.0f;
-  }
-}
-
-template <int DT>
-__device__ inline void store_n(void* __restrict__ p, int64_t off, int n, bool whole, const float (&v)[8]) {
-  if (whole) {
-    store8<DT>(p, off, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) store1<DT>(p, off + i, v[i]);
   }
 }
 
