@@ -384,6 +384,17 @@ def _rows_of(t, rows, cols, what: str) -> int:
     return pitch if rows > 1 else (cols + 7) // 8 * 8
 
 
+_dtypes = {}
+
+
+def _dtype_of(t) -> int:
+    """_dt of a tensor, looked up."""
+    code = _dtypes.get(t.dtype)
+    if code is None:
+        code = _dtypes[t.dtype] = _dt(t)
+    return code
+
+
 def _dense(t, dtype, shape, what: str) -> int:
     """Address of a dense tensor of that dtype and shape (0 for None)."""
     if t is None:
@@ -402,11 +413,19 @@ def _one(t, what: str) -> int:
     return t.data_ptr()
 
 
+_raw_stream = None  # (torch.cuda.current_stream() builds an object: 2.7 us against 0.2)
+
+
 def _stream_of(stream) -> int:
     if stream is not None:
         return stream.cuda_stream
-    torch = _torch()  # (torch.cuda.current_stream() builds an object: 2.7 us against 0.3)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    global _raw_stream
+    if _raw_stream is None:
+        C = _torch()._C
+        _torch().cuda.current_device()  # (initializes the device)
+        _raw_stream = (C._cuda_getCurrentRawStream, C._cuda_getDevice)
+    get, device = _raw_stream
+    return get(device())
 
 
 class Routing:
@@ -451,7 +470,7 @@ def mx_route(logits, out: Routing, token_mask=None, flags: int = 0, stream=None)
     ld = _rows_of(logits, out.tokens, out.num_experts, "logits")
     mask = _dense(token_mask, _torch().uint8, (out.tokens,), "token_mask")
     ws = out.workspace
-    _check(load().mx_route(logits.data_ptr(), _dt(logits), ld, mask, flags, out._ref, ws.data_ptr(), ws.numel(),
+    _check(load().mx_route(logits.data_ptr(), _dtype_of(logits), ld, mask, flags, out._ref, ws.data_ptr(), ws.numel(),
                            _stream_of(stream)))
     return out
 
@@ -466,7 +485,7 @@ def mx_route_backward(logits, r: Routing, d_weights, d_loss, d_logits, token_mas
     _need(d_logits.dtype == logits.dtype, "d_logits: dtype of logits expected")
     mask = _dense(token_mask, torch.uint8, (r.tokens,), "token_mask")
     dw = _dense(d_weights, torch.float32, (r.tokens, r.topk), "d_weights")
-    _check(load().mx_route_backward(logits.data_ptr(), _dt(logits), ld, mask, flags, r._ref, dw,
+    _check(load().mx_route_backward(logits.data_ptr(), _dtype_of(logits), ld, mask, flags, r._ref, dw,
                                     _one(d_loss, "d_loss"), d_logits.data_ptr(), ld_d, _stream_of(stream)))
     return d_logits
 
@@ -480,7 +499,7 @@ def mx_swiglu(h, y, saved: "MXTensor | None" = None, rnd: int = MX_RNE, seed: in
     ld_h, ld_y = _rows_of(h, rows, 2 * cols, "h"), _rows_of(y, rows, cols, "y")
     _need(y.dtype == h.dtype, "y: dtype of h expected")
     d = saved.desc() if saved is not None else None
-    _check(load().mx_swiglu(h.data_ptr(), _dt(h), rows, cols, ld_h, y.data_ptr(), ld_y,
+    _check(load().mx_swiglu(h.data_ptr(), _dtype_of(h), rows, cols, ld_h, y.data_ptr(), ld_y,
                             ctypes.byref(d) if d is not None else None, rnd, _Rng(seed, counter),
                             _one(amax, "amax"), _stream_of(stream)))
     return y
@@ -495,7 +514,7 @@ def mx_swiglu_backward(saved: MXTensor, dy, dh, y_saved: "MXTensor | None" = Non
     _need(dh.dtype == dy.dtype, "dh: dtype of dy expected")
     d = saved.desc()
     dys = y_saved.desc() if y_saved is not None else None
-    _check(load().mx_swiglu_backward(ctypes.byref(d), dy.data_ptr(), _dt(dy), rows, cols, ld_dy, dh.data_ptr(),
+    _check(load().mx_swiglu_backward(ctypes.byref(d), dy.data_ptr(), _dtype_of(dy), rows, cols, ld_dy, dh.data_ptr(),
                                      ld_dh, ctypes.byref(dys) if dys is not None else None, _stream_of(stream)))
     return dh
 
@@ -531,7 +550,7 @@ def mx_wgrad_grouped(dY, X: MXTensor, row_index, num_groups: int, group_offsets,
         ws = _dense(workspace, torch.uint8, (size,), "workspace")
     d = X.desc()
     _check(L.mx_wgrad_grouped(dY.data_ptr(), ld_dy, rows, N, ctypes.byref(d), index, num_groups, offsets,
-                              dW.data_ptr(), _dt(dW), ld_dw, flags, ws, size, _stream_of(stream)))
+                              dW.data_ptr(), _dtype_of(dW), ld_dw, flags, ws, size, _stream_of(stream)))
     return dW
 
 
@@ -539,14 +558,14 @@ def mx_combine(Y, slot_row, weights, out, stream=None):
     """out [tokens, cols] = sum over the slots of weights * Y[slot_row]
     (weights None: 1)."""
     torch = _torch()
-    _need(Y.dim() == 2 and slot_row.dim() == 2, "Y, slot_row: matrices expected")
-    tokens, topk = slot_row.shape
-    rows, cols = Y.shape
+    slots, y = slot_row.shape, Y.shape
+    _need(len(y) == 2 and len(slots) == 2, "Y, slot_row: matrices expected")
+    (tokens, topk), (rows, cols) = slots, y
     ld_y, ld_out = _rows_of(Y, rows, cols, "Y"), _rows_of(out, tokens, cols, "out")
     slots = _dense(slot_row, torch.int32, (tokens, topk), "slot_row")
     w = _dense(weights, torch.float32, (tokens, topk), "weights")
-    _check(load().mx_combine(Y.data_ptr(), _dt(Y), rows, cols, ld_y, slots, w, tokens, topk, out.data_ptr(), _dt(out),
-                             ld_out, _stream_of(stream)))
+    _check(load().mx_combine(Y.data_ptr(), _dtype_of(Y), rows, cols, ld_y, slots, w, tokens, topk, out.data_ptr(),
+                             _dtype_of(out), ld_out, _stream_of(stream)))
     return out
 
 
@@ -568,7 +587,7 @@ def mx_combine_backward(d_out, Y, slot_row, weights, dY, d_weights, stream=None)
     ld_dy = _rows_of(dY, rows, cols, "dY") if dY is not None else 0
     for t in (Y, dY):
         _need(t is None or t.dtype == d_out.dtype, "Y, dY: dtype of d_out expected")
-    _check(load().mx_combine_backward(d_out.data_ptr(), _dt(d_out), ld_do, 0 if Y is None else Y.data_ptr(), ld_y,
-                                      rows, cols, slots, w, tokens, topk, 0 if dY is None else dY.data_ptr(), ld_dy,
+    _check(load().mx_combine_backward(d_out.data_ptr(), _dtype_of(d_out), ld_do, 0 if Y is None else Y.data_ptr(),
+                                      ld_y, rows, cols, slots, w, tokens, topk, 0 if dY is None else dY.data_ptr(), ld_dy,
                                       dw, _stream_of(stream)))
     return dY, d_weights

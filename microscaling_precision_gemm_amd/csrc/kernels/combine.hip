@@ -10,7 +10,7 @@
 // read (written) once and does not fit a cache, so it goes by streaming
 // accesses.  Measured: 4096 tokens x 8 rows x 7168 BF16 89 us (5.9 TB/s), with
 // 16-byte accesses and a wave for every 16 bytes x 64 of a row; the backward
-// pass of 4001 tokens 177 us (5.5 TB/s, half of it writes); one token 7.2 us, of
+// pass of 4001 tokens 177 us (5.5 TB/s, half of it writes); one token 6.7 us, of
 // which the kernel is 3.4.
 #include "../device/rows.h"
 #include "../device/wave.h"

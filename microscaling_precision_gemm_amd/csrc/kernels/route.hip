@@ -33,7 +33,7 @@
 // forward pass is a chain of a wave's selection steps, the sort's counts and
 // two launches, each with a start and an end of about 2 us.  Measured on the
 // device, top 8: 16384 x 256 BF16 20 us (choosing 11.6, placing 9.4), 4096 x 32
-// FP32 13.3 us (6.5 and 6.9), one token of 32 5.8 us, one launch; backward
+// FP32 13.3 us (6.5 and 6.9), one token of 32 5.4 us, one launch; backward
 // 16384 x 256 FP32 11.8 us (33 MB: 2.8 TB/s).
 #include "../device/rows.h"
 #include "../device/wave.h"
