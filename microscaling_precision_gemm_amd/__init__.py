@@ -9,6 +9,7 @@ built, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -528,7 +529,7 @@ def mx_wgrad_grouped(dY, X: MXTensor, row_index, num_groups: int, group_offsets,
     """dW [num_groups * N, K] (fp32 or bf16) = per group, dY^T [N, rows] times
     the 8-bit rows of X (through row_index, if given).  workspace: a uint8
     tensor of mx_wgrad_workspace_bytes(rows, N, K, num_groups); None takes it
-    from torch's allocator."""
+    from torch's allocator, for the stream of the call."""
     torch = _torch()
     _need(dY.dim() == 2 and dY.dtype == torch.bfloat16, "dY: a bf16 matrix expected")
     rows, N = dY.shape
@@ -541,9 +542,10 @@ def mx_wgrad_grouped(dY, X: MXTensor, row_index, num_groups: int, group_offsets,
     if workspace is None:
         size = L.mx_wgrad_workspace_bytes(rows, N, X.cols, num_groups)
         if size:
-            workspace = torch.empty(size, dtype=torch.uint8, device=dY.device)
-            if stream is not None:
-                workspace.record_stream(stream)
+            # out of the pool of the stream that writes it: a block of another
+            # stream's may still be in use by that stream's queued work
+            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                workspace = torch.empty(size, dtype=torch.uint8, device=dY.device)
             ws = workspace.data_ptr()
     else:
         size = workspace.numel()
