@@ -510,10 +510,11 @@ mx_status mx_route(const void* logits, int32_t ldt, int64_t ld, const uint8_t* t
                    const mx_routing* out, void* workspace, size_t workspace_bytes, mx_stream stream);
 
 /* Gradient of the logits: of the weights (d_weight [tokens, topk] FP32, NULL:
- * zero) and of the balance loss (d_loss, one FP32 on the device, NULL: zero;
- * the counts are constants of the loss).  Reads logits, token_mask, flags as
- * the forward call got them, and expert, counts and valid of `routing` (the
- * other pointers may be NULL).  counts and valid may be sums over several
+ * zero; what it holds in slots without an expert is not looked at) and of the
+ * balance loss (d_loss, one FP32 on the device, NULL: zero; the counts are
+ * constants of the loss).  Reads logits, token_mask, flags as the forward call
+ * got them, and expert, counts and valid of `routing` (the other pointers may
+ * be NULL).  counts and valid may be sums over several
  * devices: the gradient is then that of the loss over all their tokens.
  * d_logits [tokens, experts] has the logits' dtype and row pitch ld_d (element
  * alignment); padding tokens get zeros. */

@@ -586,6 +586,7 @@ __global__ __launch_bounds__(kBwdThreads) void k_route_bwd(RouteBwdParams b) {
       load_scores<DT, G, VPL>(p, t, gl, in.x);
       in.e = in.e < p.experts ? in.e : -1;
       if (in.e >= 0) in.xe = load1<DT>(p.logits, t * p.ld + in.e);
+      else in.dw = 0.0f;  // (a slot without an expert: its gradient may hold anything)
     } else {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) in.x[i] = -__builtin_inff();
