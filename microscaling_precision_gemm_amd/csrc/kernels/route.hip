@@ -624,6 +624,7 @@ __global__ __launch_bounds__(kBwdThreads) void k_route_bwd(RouteBwdParams b) {
     const float inv = s == 0.0f ? 0.0f : 1.0f / s;
     pb = group_reduce<G>(pb, OpAdd()) * inv;
     const int e = in.e;
+    const bool ok = in.ok;
     float q = e >= 0 ? __builtin_amdgcn_exp2f((in.xe - m) * kLog2e) : 0.0f;
     if (p.normalize) {
       const float sq = group_reduce<G>(q, OpAdd());
@@ -642,7 +643,7 @@ __global__ __launch_bounds__(kBwdThreads) void k_route_bwd(RouteBwdParams b) {
     if (e >= 0) mine[e] = 0.0f;
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) o[i] = fmaf(x[i] * inv, bal[i] - pb, o[i]);
+    for (int i = 0; i < VPL; ++i) o[i] = ok ? fmaf(x[i] * inv, bal[i] - pb, o[i]) : 0.0f;  // (d_loss may be infinite)
     load(t + step, in);
     if (t < p.tokens) {
 #pragma unroll

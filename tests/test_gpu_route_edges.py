@@ -4,8 +4,6 @@ import numpy as np
 import pytest
 import torch
 
-from tests import moe_ref
-
 pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():
@@ -49,3 +47,17 @@ def test_gradients_of_empty_slots_are_not_looked_at(T, E, topk, kind, normalize)
     assert bool(torch.isfinite(want).all())
     for junk in (float("nan"), float("inf"), -float("inf"), 3e38):
         assert torch.equal(backward(x, r, m, torch.where(empty, junk, dw), dl, normalize), want), junk
+
+
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("T,E,topk", [(40, 6, 2), (65, 40, 8), (20, 300, 4)])
+def test_padding_gets_zeros_whatever_the_loss(T, E, topk, kind, normalize):
+    """A loss that overflowed shows in the tokens, not in the padding."""
+    mask = np.arange(T) % 3 != 1
+    x, r, m, dw = routed(T, E, topk, kind, 2, normalize, mask=mask)
+    x[1] = float("nan")
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        d = backward(x, r, m, dw, torch.tensor([bad], device=dev()), normalize)
+        assert not bool(d[~torch.from_numpy(mask).to(dev())].any()), bad
+        assert not bool(torch.isfinite(d[torch.from_numpy(mask).to(dev())]).any()), bad
