@@ -35,6 +35,7 @@
 // device, top 8: 16384 x 256 BF16 20 us (choosing 11.6, placing 9.4), 4096 x 32
 // FP32 13.3 us (6.5 and 6.9), one token of 32 5.4 us, one launch; backward
 // 16384 x 256 FP32 11.8 us (33 MB: 2.8 TB/s).
+#include "../device/exp.h"
 #include "../device/rows.h"
 #include "../device/wave.h"
 #include "../launch.h"
@@ -49,7 +50,6 @@ constexpr int threads_for(int EP) { return EP <= 256 ? 1024 : 512; }
 constexpr int kSub = 64;     // tokens of one bit word
 constexpr int kMaxK = 16;    // slots of a token
 constexpr int64_t kMaxBlocks = 256;
-constexpr float kLog2e = 1.44269504088896340736f;
 
 struct RouteParams {
   const void* logits;
@@ -271,14 +271,14 @@ __device__ inline void choose_64(const RouteParams& p, int s0, int t1, RouteShar
     float s = 0.0f;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
-      y[v] = __builtin_amdgcn_exp2f((y[v] - base) * kLog2e);
+      y[v] = exp_nonpos(y[v] - base);
       s += y[v];
     }
     s = group_reduce<G>(s, OpAdd());
     const float inv = s == 0.0f ? 0.0f : 1.0f / s;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) sum_p[v] += y[v] * inv;
-    float w = e >= 0 ? __builtin_amdgcn_exp2f((xe - base) * kLog2e) : 0.0f;
+    float w = e >= 0 ? exp_nonpos(xe - base) : 0.0f;
     if (p.normalize) {
       const float sw = group_reduce<G>(w, OpAdd());
       w = e < 0 ? 0.0f : inv == inv ? w / sw : inv;  // a NaN anywhere in the row shows in its weights
@@ -616,7 +616,7 @@ __global__ __launch_bounds__(kBwdThreads) void k_route_bwd(RouteBwdParams b) {
     float s = 0.0f, pb = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      x[i] = __builtin_amdgcn_exp2f((x[i] - m) * kLog2e);
+      x[i] = exp_nonpos(x[i] - m);
       s += x[i];
       pb = fmaf(x[i], bal[i], pb);
     }
@@ -625,7 +625,7 @@ __global__ __launch_bounds__(kBwdThreads) void k_route_bwd(RouteBwdParams b) {
     pb = group_reduce<G>(pb, OpAdd()) * inv;
     const int e = in.e;
     const bool ok = in.ok;
-    float q = e >= 0 ? __builtin_amdgcn_exp2f((in.xe - m) * kLog2e) : 0.0f;
+    float q = e >= 0 ? exp_nonpos(in.xe - m) : 0.0f;
     if (p.normalize) {
       const float sq = group_reduce<G>(q, OpAdd());
       q = e >= 0 ? q / sq : 0.0f;
