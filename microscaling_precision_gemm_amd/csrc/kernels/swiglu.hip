@@ -19,6 +19,7 @@
 #include "../device/codec.h"
 #include "../device/cvt.h"
 #include "../device/decode8.h"
+#include "../device/exp.h"
 #include "../device/mxenc.h"
 #include "../device/rows.h"
 #include "../device/wave.h"
@@ -37,11 +38,6 @@ constexpr int kThreads = 256;
 // with a workgroup per 1024 chunks).
 constexpr int kMaxThreads = 1024, kMaxGrid = 256;
 constexpr int64_t kOneChunks = 4096;  // tensors up to this go to one workgroup
-constexpr float kLog2e = 1.44269504088896340736f;
-
-__device__ inline float sigmoid(float x) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * x));
-}
 
 __global__ void k_clear(float* p) { *p = 0.0f; }
 

@@ -80,3 +80,42 @@ def test_weights_and_their_gradient(E, topk, normalize):
     torch.cuda.synchronize()
     dx, size = moe_ref.route_backward(want["p"], want["experts"], want["counts"], T, host(dw), 0.0, normalize)
     assert np.all(np.abs(host(d) - dx) <= (2 * ep + 8 * U) * size + 1e-37)
+
+
+def gates(rows, cols, seed):
+    """[gate | up], gates from -80 to 80 (e^80 and its inverse are FP32 numbers)."""
+    g = np.random.default_rng([seed, rows, cols])
+    gate = g.uniform(-80, 80, (rows, cols)) * np.where(g.random((rows, cols)) < 0.5, 1.0, 0.05)
+    return np.concatenate([gate, g.standard_normal((rows, cols))], axis=1).astype(np.float32)
+
+
+def test_activation():
+    rows, cols = 200, 256
+    h = gates(rows, cols, 3)
+    y = torch.empty(rows, cols, device=dev())
+    mx.mx_swiglu(torch.from_numpy(h).to(dev()), y)
+    torch.cuda.synchronize()
+    want = moe_ref.swiglu(h.astype(np.float64))
+    assert np.all(np.abs(host(y) - want) <= 8 * U * np.abs(want)), float(np.max(np.abs(host(y) - want) / np.abs(want) / U))
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp8_e5m2", "mxint8"])
+def test_activation_backward(fmt):
+    rows, cols = 200, 256
+    saved = mx.empty(mx.FORMATS[fmt], rows, 2 * cols, dev())
+    mx.mx_quantize(torch.from_numpy(gates(rows, cols, 4)).to(dev()), saved)
+    h = torch.empty(rows, 2 * cols, device=dev())
+    mx.mx_dequantize(saved, h)
+    dy = torch.randn(rows, cols, generator=torch.Generator(device="cuda").manual_seed(5), device=dev())
+    dh = torch.empty(rows, 2 * cols, device=dev())
+    mx.mx_swiglu_backward(saved, dy, dh)
+    torch.cuda.synchronize()
+    h, d = host(h), host(dy)
+    assert np.abs(h[:, :cols]).max() <= 80
+    g, u = h[:, :cols], h[:, cols:]
+    s = moe_ref.sigmoid(g)
+    inner, rest = 1 + g * (1 - s), moe_ref.sigmoid(-g)
+    tol_gate = U * np.abs(d * u) * s * (np.abs(g) * (5 * s + rest) + 10 * np.abs(inner))
+    tol_up = 8 * U * np.abs(d * g) * s
+    tol = np.concatenate([tol_gate, tol_up], axis=1) + 1e-37
+    assert np.all(np.abs(host(dh) - moe_ref.swiglu_backward(h, d)) <= tol)
