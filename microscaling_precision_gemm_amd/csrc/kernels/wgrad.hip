@@ -104,6 +104,11 @@ struct Variant {
   static constexpr int LDS = 4 * HALF + 4 * SCRATCH;
 };
 
+// a / b rounded up, for 0 <= a and 0 < b (their sum may pass 31 bits)
+__device__ __forceinline__ int32_t parts_of(int32_t a, int32_t b) {
+  return (int32_t)(((uint32_t)a + (uint32_t)b - 1u) / (uint32_t)b);
+}
+
 // One tile and its rows (the same in all lanes).
 struct Unit {
   uint32_t n0, k0;
@@ -112,7 +117,7 @@ struct Unit {
   int32_t slot;      // where its products go in p.parts; -1: to dW
   // Stages: at least 3, so that the copies, which run ahead of the products,
   // never reach past the tile after this one.
-  __device__ __forceinline__ int32_t stages() const { return max((cnt + kStep - 1) / kStep, 3); }
+  __device__ __forceinline__ int32_t stages() const { return max(parts_of(cnt, kStep), 3); }
 };
 
 template <class V>
@@ -165,7 +170,7 @@ __device__ __forceinline__ Unit seek(const WgradParams& p, uint32_t& id) {
 __device__ __forceinline__ int32_t parts_scan(const WgradParams& p, int32_t g0, uint32_t lane, int32_t& n) {
   int32_t row, cnt = 0;
   if (g0 + (int32_t)lane < p.groups) group_rows(p, g0 + lane, row, cnt);
-  n = (cnt + p.len - 1) / p.len;
+  n = parts_of(cnt, p.len);
   int32_t sum = n;
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) {
