@@ -7,7 +7,7 @@
 #include <mutex>
 
 #include "device/codec.h"
-#include "launch.h"
+#include "launch_moe.h"
 
 namespace {
 

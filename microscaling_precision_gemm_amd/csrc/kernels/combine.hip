@@ -14,7 +14,7 @@
 // which the kernel is 3.4.
 #include "../device/rows.h"
 #include "../device/wave.h"
-#include "../launch.h"
+#include "../launch_moe.h"
 
 namespace mxk {
 

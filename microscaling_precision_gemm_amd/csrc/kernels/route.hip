@@ -38,7 +38,7 @@
 #include "../device/exp.h"
 #include "../device/rows.h"
 #include "../device/wave.h"
-#include "../launch.h"
+#include "../launch_moe.h"
 
 namespace mxk {
 

@@ -23,7 +23,7 @@
 #include "../device/mxenc.h"
 #include "../device/rows.h"
 #include "../device/wave.h"
-#include "../launch.h"
+#include "../launch_moe.h"
 
 namespace mxk {
 

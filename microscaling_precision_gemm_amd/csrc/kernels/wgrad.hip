@@ -28,7 +28,7 @@
 
 #include "../device/decode8.h"
 #include "../device/gemm_common.h"
-#include "../launch.h"
+#include "../launch_moe.h"
 
 namespace mxk {
 
