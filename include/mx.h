@@ -460,7 +460,8 @@ mx_status mx_quantize_batch_noalloc(const mx_quantize_job* jobs, int32_t count, 
  * The steps of a mixture-of-experts layer before, between and behind its
  * grouped products ([INK] "A precision choice for each stage": NVFP4 forward
  * in the expert layers, saved tensors kept quantized for the backward pass).
- * All of them are deterministic: equal inputs give equal bits. */
+ * All of them are deterministic: equal inputs that keep to what is said below
+ * give equal bits. */
 
 /* One routing of `tokens` tokens to `experts` experts, topk each (host struct;
  * the pointers are device pointers, dense arrays).  R = tokens * topk slots. */
@@ -583,6 +584,9 @@ mx_status mx_combine(const void* Y, int32_t ydt, int64_t rows, int64_t cols, int
 /* Its gradients, for d_out [tokens, cols]: dY[slot_row[t, j], :] = weight[t,
  * j] * d_out[t, :] (rows that no slot names are not written) and d_weight[t,
  * j] = <d_out[t, :], Y[slot_row[t, j], :]> (0 for a slot without a row).
+ * Where dY is wanted, no two slots may name one row, as mx_route's never do:
+ * dY would hold what one of them gives, not their sum, and which one is not
+ * determined.  (mx_combine, and d_weight alone, take repeated rows.)
  * Either of dY and d_weight may be NULL; Y may be NULL when d_weight is.  d_out,
  * Y and dY have dtype dt and 16-byte aligned rows. */
 mx_status mx_combine_backward(const void* d_out, int32_t dt, int64_t ld_do, const void* Y, int64_t ld_y,

@@ -572,8 +572,9 @@ def mx_combine(Y, slot_row, weights, out, stream=None):
 
 
 def mx_combine_backward(d_out, Y, slot_row, weights, dY, d_weights, stream=None):
-    """Gradients of mx_combine: dY [rows, cols] (None: not wanted) and
-    d_weights [tokens, topk] (None: not wanted; Y may then be None)."""
+    """Gradients of mx_combine: dY [rows, cols] (None: not wanted; otherwise no
+    two slots may name one row, and mx_route's do not) and d_weights [tokens,
+    topk] (None: not wanted; Y may then be None)."""
     torch = _torch()
     _need(d_out.dim() == 2 and slot_row.dim() == 2, "d_out, slot_row: matrices expected")
     tokens, topk = slot_row.shape

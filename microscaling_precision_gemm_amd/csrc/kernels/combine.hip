@@ -5,6 +5,8 @@
 //   d_w[t, j]     = sum_c d_out[t, c] * Y[row, c]
 // A slot without a row (slot_row < 0, or past Y) adds nothing.  Sums are FP32
 // in slot order (out) or in a fixed tree (d_w), so results repeat bit for bit.
+// dY is stored, not added to: the rows that slots name are distinct where it is
+// wanted.
 //
 // Both are bound by HBM: Y (or dY) is k times the size of the token matrix, is
 // read (written) once and does not fit a cache, so it goes by streaming
