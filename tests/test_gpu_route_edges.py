@@ -61,3 +61,42 @@ def test_padding_gets_zeros_whatever_the_loss(T, E, topk, kind, normalize):
         d = backward(x, r, m, dw, torch.tensor([bad], device=dev()), normalize)
         assert not bool(d[~torch.from_numpy(mask).to(dev())].any()), bad
         assert not bool(torch.isfinite(d[torch.from_numpy(mask).to(dev())]).any()), bad
+
+
+@pytest.mark.parametrize("T,E,topk,kind,normalize", [(16385, 256, 8, "f32", True), (40003, 60, 4, "bf16", True),
+                                                     (40003, 24, 3, "f32", False), (5001, 300, 2, "f32", True)])
+def test_a_group_of_lanes_does_several_tokens(T, E, topk, kind, normalize):
+    """More tokens than the grid has groups of lanes (16384 of 16 lanes up to 256
+    experts, 4096 above): a later token gets the bits it gets alone, whatever
+    came before it, padding and rows without a choice among them."""
+    mask = np.random.default_rng(3).random(T) > 0.2
+    x, r, m, dw = routed(T, E, topk, kind, 3, normalize, mask=mask, holes=0.1)
+    x[5::97] = -float("inf")
+    r = mx.mx_route(x, r, token_mask=m, flags=mx.MX_ROUTE_NORMALIZE if normalize else 0)
+    dl = torch.tensor([30.0], device=dev())
+    d = backward(x, r, m, dw, dl, normalize)
+    assert not bool(d[~torch.from_numpy(mask).to(dev())].any())
+    for a in range(0, T, 4001):
+        n = min(4001, T - a)
+        part = mx.routing(n, E, topk, device=dev())
+        for name in ("experts", "counts", "valid"):  # the whole batch's counts: the loss is the batch's
+            whole = getattr(r, name)
+            getattr(part, name).copy_(whole[a:a + n] if name == "experts" else whole)
+        got = backward(x[a:a + n].contiguous(), part, m[a:a + n].contiguous(), dw[a:a + n].contiguous(), dl, normalize)
+        assert torch.equal(d[a:a + n], got), a
+    p = torch.softmax(x.double(), 1).nan_to_num(0.0) * torch.from_numpy(mask).to(dev())[:, None]
+    there = r.experts >= 0
+    at = r.experts.long().clamp(min=0)
+    b = 30.0 * E / (topk * float(r.valid) ** 2) * r.counts.double()
+    w = torch.where(there, dw, 0.0).double()
+    q = torch.zeros_like(p).scatter_add_(1, at, torch.where(there, p.gather(1, at), 0.0))
+    if normalize:
+        q = q / q.sum(1, keepdim=True).clamp(min=1e-300)
+    hot = torch.zeros_like(p).scatter_add_(1, at, w)
+    pb, pa, qd, qa = ((v * c).sum(1, keepdim=True) for v, c in ((p, b), (p, b.abs()), (q, hot), (q, hot.abs())))
+    other = q if normalize else p
+    want = p * (b - pb) + q * hot - other * qd
+    size = p * (b.abs() + pa) + q * hot.abs() + other * qa
+    # p and q to 29 * 2^-24, differences of scores 2^-24 of up to 10, sums and roundings 40 more
+    tol = 128 * 2.0 ** -24 * size + 1e-37 + (2.0 ** -8 * want.abs() if kind == "bf16" else 0)
+    assert bool(((d.double() - want).abs() <= tol).all())
