@@ -598,6 +598,9 @@ __global__ __launch_bounds__(kBwdThreads) void k_route_bwd(RouteBwdParams b) {
   load(t, in);
   const float v = (float)*p.valid;
   const float scale = b.d_loss && v > 0.0f ? *b.d_loss * ((float)p.experts / ((float)k * v)) / v : 0.0f;
+  // some scale * count may not be finite (counts are below 2^63), and 0 times it
+  // is no zero for a padding token
+  const bool wild = __ballot(!(__builtin_fabsf(scale) <= 1e18f)) != 0;
   float bal[VPL];
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
@@ -643,7 +646,11 @@ __global__ __launch_bounds__(kBwdThreads) void k_route_bwd(RouteBwdParams b) {
     if (e >= 0) mine[e] = 0.0f;
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) o[i] = ok ? fmaf(x[i] * inv, bal[i] - pb, o[i]) : 0.0f;  // (d_loss may be infinite)
+    for (int i = 0; i < VPL; ++i) o[i] = fmaf(x[i] * inv, bal[i] - pb, o[i]);
+    if (wild) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) o[i] = ok ? o[i] : 0.0f;
+    }
     load(t + step, in);
     if (t < p.tokens) {
 #pragma unroll
