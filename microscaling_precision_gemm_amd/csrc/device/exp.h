@@ -24,18 +24,16 @@ __device__ inline float exp_nonpos(float x) {
   return fmaf(y, exp_rest(x, t), y);
 }
 
-// 1 / (1 + e^-x) to 5 * 2^-24 relative, 0 below -87.4.  e^-x is 2^t (1 + rest)
-// here with the bracket first, so that an infinite 2^t stays infinite; beyond
-// +-150 nothing changes, and a finite limit keeps the rest finite.  The
-// quotient takes one Newton step, whose divisor is kept finite: of an infinite
-// one the reciprocal is 0 and stays 0.  The sigmoid of NaN is some number (its
-// users multiply by x).
+// 1 / (1 + e^-x) to 5 * 2^-24 relative, 0 below -87.4: there the denominator
+// passes 2^126 and the hardware's reciprocal is 0 (it has no subnormal results),
+// which the Newton step leaves 0.  The limits keep all of it finite; beyond them
+// nothing changes.  The sigmoid of NaN is some number (its users multiply by x).
 __device__ inline float sigmoid(float x) {
-  const float n = __builtin_amdgcn_fmed3f(-x, -150.0f, 150.0f);
-  const float t = n * kLog2e;
-  const float d = fmaf(__builtin_amdgcn_exp2f(t), 1.0f + exp_rest(n, t), 1.0f);
+  const float n = __builtin_amdgcn_fmed3f(-x, -150.0f, 88.0f);
+  const float t = n * kLog2e, y = __builtin_amdgcn_exp2f(t);
+  const float d = fmaf(y, exp_rest(n, t), 1.0f + y);
   const float r = __builtin_amdgcn_rcpf(d);
-  return fmaf(fmaf(-__builtin_fminf(d, 3.402823466e38f), r, 1.0f), r, r);
+  return fmaf(fmaf(-d, r, 1.0f), r, r);
 }
 
 }  // namespace mxk
