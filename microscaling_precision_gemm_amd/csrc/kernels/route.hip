@@ -29,12 +29,19 @@
 // count, and the blocks of tokens are put in order by their counts.  S is
 // summed per block in a fixed order, then over the blocks.
 //
-// The bytes (16384 x 256 BF16: 9 MB, 2 us of HBM) are not what bounds it: the
-// forward pass is a chain of a wave's selection steps, the sort's counts and
-// two launches, each with a start and an end of about 2 us.  Measured on the
-// device, top 8: 16384 x 256 BF16 20 us (choosing 11.6, placing 9.4), 4096 x 32
-// FP32 13.3 us (6.5 and 6.9), one token of 32 5.4 us, one launch; backward
-// 16384 x 256 FP32 11.8 us (33 MB: 2.8 TB/s).
+// The bytes (16384 x 256 BF16: 9 MB, 2 us of HBM) are not what bounds it.  Of
+// two launches each has a start and an end (an empty kernel takes 1.5 to 2 us).
+// Choosing: 900 vector instructions a wave, 4 waves a SIMD, at 16384 x 256 about
+// 6 of its 11.7 us; the rest is one chain of load, selection steps and LDS that
+// nothing runs beside, since a wave has one pass of tokens.  Placing: every
+// workgroup reads the counts of all blocks (33 MB out of the L2s at 256
+// experts) and adds them in LDS, where 84% of its accesses conflict.  At 4096 x
+// 32 both are chains of dependent loads and LDS steps on 64 of the CUs.
+// Measured on the device, top 8: 16384 x 256 BF16 20.5 us (choosing 11.7, placing
+// 9.5), 4096 x 32 FP32 13.4 us (6.5 and 6.9), one token of 32 5.5 us, one launch.
+// Backward, 16384 x 256: FP32 10.4 us (33 MB: 3.2 TB/s), BF16 10.0.  There a
+// group of lanes has one token, and its loads depend on one another: the mask,
+// the chosen experts, their scores; 1024 tokens take 6.7 us.
 #include "../device/exp.h"
 #include "../device/rows.h"
 #include "../device/wave.h"

@@ -12,10 +12,12 @@
 // Bound by HBM.  A lane takes 8 consecutive gate elements and the 8 up
 // elements beside them, a lane quad one 32-element block of each half, so the
 // block maxima need two DPP steps and h is read once for both results.
-// Measured, 32768 x 2048 BF16: forward 70 us (5.8 TB/s), with an MXFP8
-// checkpoint and max |y| 110 us (4.9 TB/s: few workgroups, see kMaxGrid),
-// backward 92 us (5.9 TB/s), and with the operand of the next weight gradient
-// 108 us (5.6 TB/s).
+// Measured, 32768 x 2048 BF16: forward 71 us (5.7 TB/s), with an MXFP8
+// checkpoint 105 us (5.1 TB/s) and max |y| 116 us (4.6 TB/s: few workgroups, see
+// kMaxGrid), backward 99 us (5.5 TB/s), and with the operand of the next weight
+// gradient 114 us (5.3 TB/s).  Of these 2 to 6 us are the sigmoid's corrections:
+// a wave of the backward pass issues 250 vector instructions for 8 elements a
+// lane (200 without them), about two thirds of its time.
 #include "../device/codec.h"
 #include "../device/cvt.h"
 #include "../device/decode8.h"
@@ -35,7 +37,7 @@ constexpr int kThreads = 256;
 // and look at the word just before (32768 x 2048 BF16 with an MXFP8
 // checkpoint: 110 us; 122 with a workgroup per 1024 chunks that looked at its
 // start, 206 with one per 512 that did not look; 4099 x 4096 FP32: 47 us, 56
-// with a workgroup per 1024 chunks).
+// with a workgroup per 1024 chunks; all with a sigmoid that took 6 us less).
 constexpr int kMaxThreads = 1024, kMaxGrid = 256;
 constexpr int64_t kOneChunks = 4096;  // tensors up to this go to one workgroup
 
@@ -63,7 +65,8 @@ __device__ inline uint32_t block_max(uint32_t m) {
 // FMT 0: nothing is saved.  Q chunks of 8 columns, cpr of them in a row, one a
 // thread: HBM was fullest with as many small waves as there are chunks (at
 // 32768 x 2048 BF16 without a checkpoint 5.8 TB/s, against 5.6 with two chunks
-// a thread and 5.4 with workgroups that walk over the tensor).  AMAX 0: not
+// a thread and 5.4 with workgroups that walk over the tensor, all with a shorter
+// sigmoid).  AMAX 0: not
 // wanted; 1: the workgroup is alone, so *amax needs no clearing before and no
 // atomic; 2: *amax is cleared before.
 template <int DT, int FMT, bool SR, int AMAX>

@@ -14,11 +14,11 @@
 // Bounds.  The matrix unit, where groups are long: 256 x 256 tiles, a wave of
 // 128 x 128 to each SIMD with all of its products in accumulators, every other
 // instruction placed behind a product, run at the power-limited rate of the
-// BF16 instruction on random data (each further 65536 rows x 2048 x 7168: 1566
-// us, 1229 TFLOP/s).  What a tile costs besides is its store: with one wave a
+// BF16 instruction on random data (each further 65536 rows x 2048 x 7168 in 32
+// even groups: 1585 us, 1214 TFLOP/s).  What a tile costs besides is its store: with one wave a
 // SIMD nothing runs beside it, and 256 tiles of 256 KB leave at the rate of
-// HBM.  32768 rows in 32 uneven groups x 2048 x 7168 E4M3, gathered: 1063 us
-// (905 TFLOP/s; 1.88 GB of FP32 output, 3.3 GB past the L2s in).  Spreading the
+// HBM.  32768 rows in 32 uneven groups x 2048 x 7168 E4M3, gathered: 1075 us
+// (895 TFLOP/s; 1.88 GB of FP32 output, 3.4 GB past the L2s in).  Spreading the
 // workgroups' phases by waits of 2 .. 36 us did not pay (1200 .. 1230 us
 // against 1217 with even groups).  Short groups are bound by latency: a tile's
 // first loads, three stages and its store are 8 us.
@@ -780,6 +780,8 @@ __global__ __launch_bounds__(256) void k_wgrad_join(WgradParams p, uint32_t T) {
 //   2000 x 1024 x 1024, 20       24           -           32          -
 //   16384 x 512 x 1024, 32       37           -           33          -
 //   32768 x 2048 x 2048, 4       316          -          287          -
+// (the chosen ones with a workspace at hand and 30 calls in a row: 28, 290, 104 to
+// 111, 11 to 14, 24, 32 to 33 and 290 us, by how even the groups are)
 struct Plan {
   int64_t T, len, units;
   float us;
