@@ -594,6 +594,130 @@ mx_status mx_combine_backward(const void* d_out, int32_t dt, int64_t ld_do, cons
                               int64_t tokens, int32_t topk, void* dY, int64_t ld_dy, float* d_weight,
                               mx_stream stream);
 
+/* ---- a dense layer, and a head that scores tokens ---------------------------
+ * The product of activations with block-scaled weights and what follows it, the
+ * gradients of that, dropout, and the log probabilities that a policy gradient
+ * or a serving loop asks of the logits ([MIL] "Recipe 1: End-to-end MXFP8" and
+ * the reinforcement-learning setting it serves).  All of them are
+ * deterministic: equal calls give equal bits. */
+
+/* z s(z) with s the sigmoid (SILU); z erfc(-z / sqrt 2) / 2 (GELU); its form
+ * z s(sqrt(8 / pi) (z + 0.044715 z^3)) (GELU_TANH, z (1 + tanh) / 2). */
+typedef enum { MX_ACT_NONE = 0, MX_ACT_RELU = 1, MX_ACT_SILU = 2, MX_ACT_GELU = 3, MX_ACT_GELU_TANH = 4 } mx_act;
+
+/* Dropout of this section: element (r, c) of a [rows, cols] matrix takes 16 bits
+ * of the stream that mx_rng describes, those of element c % 8 of Philox block
+ * counter + r * ceil(cols / 8) + c / 8 (for cols % 8 == 0 the draws of row-major
+ * index n = r cols + c).  With t = drop * 65536 rounded to the nearest whole
+ * number (ties to even, at most 65535), elements whose 16 bits are below t become
+ * 0 and the others are multiplied by 65536 / (65536 - t).  drop in [0, 1); t = 0
+ * drops nothing.  The mask is never stored: a backward pass draws it again from
+ * the same drop, seed and counter.  A caller that wants disjoint streams advances
+ * `counter` by rows * ceil(cols / 8) per call. */
+
+/* What follows the sum of a product (host struct; the pointers are device
+ * pointers): out = residual + drop(act(z)), z = sum + bias.  A zeroed struct
+ * asks for nothing.  residual and z have the output's dtype; element alignment
+ * is enough for all of them. */
+typedef struct {
+  int32_t act;          /* mx_act */
+  int32_t bias_dt;      /* mx_dtype of bias */
+  const void* bias;     /* [N], NULL: none */
+  const void* residual; /* [M, N], row pitch ld_residual, NULL: none */
+  int64_t ld_residual;
+  void* z;              /* [M, N], row pitch ld_z: receives z, NULL: not kept */
+  int64_t ld_z;
+  double drop;          /* probability, see above */
+  mx_rng rng;
+} mx_epilogue;
+
+/* Linear layer on block-scaled weights: with z[m, n] = sum_k X[m, k] W[n, k] +
+ * bias[n],  out = residual + drop(act(z)), all in FP32 (sums too); z and out are
+ * rounded once each.  X: BF16 [M, K], row pitch ldx, 16-byte aligned rows.  W
+ * [N, K]: MXFP4, MXFP8 (E4M3, E5M2), MXINT8 or NVFP4 in the row layout, its
+ * elements times their block scale taken as BF16 (exact for NVFP4 and for scale
+ * codes 10 .. 239; INT8 to 254), NVFP4's tensor scale applied to the sum.
+ * Products below the normal FP32 range may be lost.  A NaN scale code gives NaN
+ * in its column.  out [M, N] (odt, row pitch ldo, element alignment).  `ep` NULL:
+ * out = z without bias.  out may be the residual itself (same pointer and
+ * pitch); it and z may not overlap each other or any other argument.
+ * Gradients: d_z and d_bias by mx_epilogue_backward, that of the residual is that
+ * of out; X's is mx_linear of d_z by the transposed weights (mx_requant_transpose
+ * or mx_quantize of them), W's is mx_wgrad_grouped of d_z and the 8-bit X.
+ * Requirements: K % 32 == 0, M and N below 2^26, M * N at most 2^35.  M == 0 or
+ * N == 0 enqueues nothing; K == 0 is an empty sum. */
+mx_status mx_linear(const void* X, int64_t ldx, int64_t M, const mx_tensor* W, const mx_epilogue* ep, void* out,
+                    int32_t odt, int64_t ldo, mx_stream stream);
+
+/* Backward pass of such an epilogue: for d_out [rows, cols] and the z that
+ * mx_linear kept (NULL for MX_ACT_NONE), both of dtype dt,
+ *   d_z = drop(d_out * act'(z)),  d_bias[c] = sum_r d_z[r, c]
+ * in FP32; d_z (dtype dt) is rounded once, d_bias (FP32 [cols]) sums the unrounded
+ * values in a fixed order.  relu'(0) = 0.  Either of d_z and d_bias may be NULL;
+ * d_z may be d_out or z itself (same pointer and pitch).  act, drop, rng as the
+ * forward call got them.  Element alignment is enough; 16-byte aligned rows are
+ * faster.  workspace (wanted with d_bias): mx_epilogue_workspace_bytes(rows, cols)
+ * bytes of device memory, 16-byte aligned, written before it is read (NULL when
+ * that is 0).  rows and cols below 2^31. */
+size_t mx_epilogue_workspace_bytes(int64_t rows, int64_t cols);
+mx_status mx_epilogue_backward(const void* d_out, int32_t dt, int64_t rows, int64_t cols, int64_t ld_do, const void* z,
+                               int64_t ld_z, int32_t act, double drop, mx_rng rng, void* d_z, int64_t ld_dz,
+                               float* d_bias, void* workspace, size_t workspace_bytes, mx_stream stream);
+
+/* out = residual + drop(x) (residual NULL: drop(x)), [rows, cols] of dtype dt, in
+ * FP32, rounded once.  The gradient of x is the same call on d_out without a
+ * residual.  out may be x or the residual itself (same pointer and pitch).
+ * Element alignment is enough.  rows and cols below 2^31. */
+mx_status mx_dropout(const void* x, int32_t dt, int64_t rows, int64_t cols, int64_t ld_x, const void* residual,
+                     int64_t ld_residual, double drop, mx_rng rng, void* out, int64_t ld_out, mx_stream stream);
+
+/* What mx_logprob writes for each of `tokens` rows over `vocab` entries, with topk
+ * alternatives (host struct; the pointers are device pointers, dense arrays). */
+typedef struct {
+  int64_t tokens;
+  int64_t vocab;
+  int32_t topk;
+  float* logp;      /* [tokens] log probability of the given token */
+  float* entropy;   /* [tokens] entropy of the row, in nats */
+  float* row_max;   /* [tokens] largest logit m */
+  float* log_sum;   /* [tokens] log sum_v exp(scale (x_v - m)) */
+  int32_t* top_id;  /* [tokens, topk] the largest entries, -1: none */
+  float* top_logp;  /* [tokens, topk] their log probabilities, -inf where top_id is -1 */
+} mx_logprobs;
+
+#define MX_LOGPROB_MAX_TOPK 32
+#define MX_LOGPROB_MAX_TOKENS (1 << 21)
+
+/* Log probabilities under softmax(scale * logits): for each row of logits
+ * [tokens, vocab] (BF16 or FP32, row pitch ld, element alignment) that of entry
+ * target[t], the entropy, and the topk largest entries in descending order, equal
+ * ones by lower index.  Statistics are FP32.  scale (an inverse temperature):
+ * finite and above 0.
+ * target (device int64 [tokens]): a value outside [0, vocab) marks padding, whose
+ * logits are not looked at: 0 in all its results, no alternatives.  NULL: no
+ * token is given and no row is padding (out->logp is then not written and may be
+ * NULL).
+ * An entry of -inf has probability 0, logp -inf, and is never an alternative (nor
+ * is NaN).  A row without any other entry gets row_max = logp = -inf and 0
+ * elsewhere, no alternatives, and a gradient of 0.  A row that holds NaN or +inf
+ * gets NaN log probabilities, entropy and gradient.
+ * Requirements: 0 <= tokens <= MX_LOGPROB_MAX_TOKENS, 1 <= vocab < 2^31, 0 <= topk
+ * <= min(vocab, MX_LOGPROB_MAX_TOPK). */
+mx_status mx_logprob(const void* logits, int32_t ldt, int64_t ld, const int64_t* target, float scale,
+                     const mx_logprobs* out, mx_stream stream);
+
+/* Gradient of the logits for d_logp and d_entropy ([tokens] FP32 each, NULL: zero;
+ * d_logp of a call without target is not looked at), with p the probabilities:
+ *   d_logits[t, v] = scale (d_logp[t] (delta(v, target[t]) - p_v)
+ *                           - d_entropy[t] p_v (log p_v + entropy[t]))
+ * (the alternatives are constants).  Reads entropy, row_max and log_sum of
+ * `saved`, and logits, target and scale as the forward call got them.  d_logits
+ * [tokens, vocab] has the logits' dtype and row pitch ld_d (element alignment) and
+ * may be logits itself (same pointer and pitch); padding gets zeros. */
+mx_status mx_logprob_backward(const void* logits, int32_t ldt, int64_t ld, const int64_t* target, float scale,
+                              const mx_logprobs* saved, const float* d_logp, const float* d_entropy, void* d_logits,
+                              int64_t ld_d, mx_stream stream);
+
 /* Human-readable name of a status code (static string). */
 const char* mx_status_string(int32_t status);
 

@@ -28,10 +28,15 @@ MX_NOALLOC_MAX_JOBS = 256
 MX_ROUTE_NORMALIZE = 1
 MX_ROUTE_MAX_EXPERTS, MX_ROUTE_MAX_TOPK, MX_ROUTE_MAX_TOKENS = 1024, 16, 1 << 23
 MX_WGRAD_ACCUMULATE = 1
+MX_ACT_NONE, MX_ACT_RELU, MX_ACT_SILU, MX_ACT_GELU, MX_ACT_GELU_TANH = 0, 1, 2, 3, 4
+MX_LOGPROB_MAX_TOPK, MX_LOGPROB_MAX_TOKENS = 32, 1 << 21
 
 FORMATS = {"mxfp8": MX_MXFP8_E4M3, "mxfp4": MX_MXFP4_E2M1, "nvfp4": MX_NVFP4, "mxint8": MX_MXINT8,
            "s2f6": MX_MXINT8, "mxfp8_e5m2": MX_MXFP8_E5M2, "mxfp6_e3m2": MX_MXFP6_E3M2,
            "mxfp6_e2m3": MX_MXFP6_E2M3}
+
+ACTIVATIONS = {"none": MX_ACT_NONE, "relu": MX_ACT_RELU, "silu": MX_ACT_SILU, "gelu": MX_ACT_GELU,
+               "gelu_tanh": MX_ACT_GELU_TANH}
 
 # every function declared in include/mx.h
 EXPORTED = [
@@ -40,7 +45,8 @@ EXPORTED = [
     "mx_gemm_grouped", "mx_gemm_quantize", "mx_gemm_quantize_a", "mx_quantize_batch", "mx_error_stats",
     "mx_quantize_batch_noalloc", "mx_route_workspace_bytes", "mx_route", "mx_route_backward", "mx_swiglu",
     "mx_swiglu_backward", "mx_wgrad_workspace_bytes", "mx_wgrad_grouped", "mx_combine",
-    "mx_combine_backward", "mx_status_string",
+    "mx_combine_backward", "mx_linear", "mx_epilogue_workspace_bytes", "mx_epilogue_backward", "mx_dropout",
+    "mx_logprob", "mx_logprob_backward", "mx_status_string",
 ]
 
 
@@ -72,6 +78,18 @@ class _Routing(ctypes.Structure):
                 ("valid", ctypes.c_void_p), ("prob_sum", ctypes.c_void_p), ("loss", ctypes.c_void_p)]
 
 
+class _Epilogue(ctypes.Structure):
+    _fields_ = [("act", ctypes.c_int32), ("bias_dt", ctypes.c_int32), ("bias", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64), ("z", ctypes.c_void_p),
+                ("ld_z", ctypes.c_int64), ("drop", ctypes.c_double), ("rng", _Rng)]
+
+
+class _Logprobs(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("topk", ctypes.c_int32),
+                ("logp", ctypes.c_void_p), ("entropy", ctypes.c_void_p), ("row_max", ctypes.c_void_p),
+                ("log_sum", ctypes.c_void_p), ("top_id", ctypes.c_void_p), ("top_logp", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -94,6 +112,7 @@ def load():
     vp, i32, i64, u32, u64, u16 = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
                                    ctypes.c_uint32, ctypes.c_uint64, ctypes.c_uint16)
     TP, RP = ctypes.POINTER(_Tensor), ctypes.POINTER(_Routing)
+    EP, LP, f32, f64 = ctypes.POINTER(_Epilogue), ctypes.POINTER(_Logprobs), ctypes.c_float, ctypes.c_double
     sig = {
         "mx_codes_bytes": (ctypes.c_size_t, [i32, i64, i64]),
         "mx_scales_bytes": (ctypes.c_size_t, [i32, i64, i64]),
@@ -120,6 +139,13 @@ def load():
         "mx_wgrad_grouped": (i32, [vp, i64, i64, i64, TP, vp, i32, vp, vp, i32, i64, u32, vp, ctypes.c_size_t, vp]),
         "mx_combine": (i32, [vp, i32, i64, i64, i64, vp, vp, i64, i32, vp, i32, i64, vp]),
         "mx_combine_backward": (i32, [vp, i32, i64, vp, i64, i64, i64, vp, vp, i64, i32, vp, i64, vp, vp]),
+        "mx_linear": (i32, [vp, i64, i64, TP, EP, vp, i32, i64, vp]),
+        "mx_epilogue_workspace_bytes": (ctypes.c_size_t, [i64, i64]),
+        "mx_epilogue_backward": (i32, [vp, i32, i64, i64, i64, vp, i64, i32, f64, _Rng, vp, i64, vp, vp,
+                                       ctypes.c_size_t, vp]),
+        "mx_dropout": (i32, [vp, i32, i64, i64, i64, vp, i64, f64, _Rng, vp, i64, vp]),
+        "mx_logprob": (i32, [vp, i32, i64, vp, f32, LP, vp]),
+        "mx_logprob_backward": (i32, [vp, i32, i64, vp, f32, LP, vp, vp, vp, i64, vp]),
         "mx_status_string": (ctypes.c_char_p, [i32]),
     }
     for name, (res, args) in sig.items():
@@ -594,3 +620,147 @@ def mx_combine_backward(d_out, Y, slot_row, weights, dY, d_weights, stream=None)
                                       ld_y, rows, cols, slots, w, tokens, topk, 0 if dY is None else dY.data_ptr(), ld_dy,
                                       dw, _stream_of(stream)))
     return dY, d_weights
+
+
+# ---- a dense layer, and a head that scores tokens ---------------------------
+def _stream_at(t, stream) -> int:
+    """_stream_of for a call on t, which has to be on the current device (a launch
+    goes to that one)."""
+    s = _stream_of(stream)
+    here = _raw_stream[1]() if _raw_stream else _torch().cuda.current_device()
+    _need(t.get_device() == here and (stream is None or stream.device_index == here),
+          "tensors and streams of the current device expected")
+    return s
+
+
+def mx_linear(x, W: MXTensor, out, bias=None, act: int = MX_ACT_NONE, z=None, residual=None, drop: float = 0.0,
+              seed: int = 0, counter: int = 0, stream=None):
+    """out [M, N] (bf16 or fp32) = residual + drop(act(x W^T + bias)) for x bf16
+    [M, K] and block-scaled weights W [N, K] (row layout); `z` receives x W^T +
+    bias.  bias: bf16 or fp32 [N]; z, residual: dtype of out."""
+    _need(x.dim() == 2 and x.dtype == _torch().bfloat16, "x: a bf16 matrix expected")
+    M, N = x.shape[0], W.rows
+    ldx, ldo = _rows_of(x, M, W.cols, "x"), _rows_of(out, M, N, "out")
+    e = _Epilogue(act=act, drop=drop, rng=_Rng(seed, counter))
+    if bias is not None:
+        _need(bias.shape == (N,) and bias.is_contiguous(), "bias: a dense vector of N expected")
+        e.bias, e.bias_dt = bias.data_ptr(), _dtype_of(bias)
+    if residual is not None:
+        _need(residual.dtype == out.dtype, "residual: dtype of out expected")
+        e.residual, e.ld_residual = residual.data_ptr(), _rows_of(residual, M, N, "residual")
+    if z is not None:
+        _need(z.dtype == out.dtype, "z: dtype of out expected")
+        e.z, e.ld_z = z.data_ptr(), _rows_of(z, M, N, "z")
+    d = W.desc()
+    _check(load().mx_linear(x.data_ptr(), ldx, M, ctypes.byref(d), ctypes.byref(e), out.data_ptr(), _dtype_of(out), ldo,
+                            _stream_at(x, stream)))
+    return out
+
+
+def mx_epilogue_workspace_bytes(rows: int, cols: int) -> int:
+    return int(load().mx_epilogue_workspace_bytes(rows, cols))
+
+
+def mx_epilogue_backward(d_out, z, d_z, d_bias=None, act: int = MX_ACT_NONE, drop: float = 0.0, seed: int = 0,
+                         counter: int = 0, workspace=None, stream=None):
+    """d_z [rows, cols] = drop(d_out * act'(z)) and d_bias (fp32 [cols]) = the sum
+    of its rows (either may be None), for the z, act, drop, seed and counter of
+    mx_linear (z None: no activation).  workspace: a uint8 tensor of
+    mx_epilogue_workspace_bytes(rows, cols); None takes it from torch's
+    allocator, for the stream of the call."""
+    torch = _torch()
+    _need(d_out.dim() == 2, "d_out: a matrix expected")
+    rows, cols = d_out.shape
+    ld_do = _rows_of(d_out, rows, cols, "d_out")
+    _need(z is not None or act == MX_ACT_NONE, "z: wanted with an activation")
+    for t in (z, d_z):
+        _need(t is None or t.dtype == d_out.dtype, "z, d_z: dtype of d_out expected")
+    ld_z = _rows_of(z, rows, cols, "z") if z is not None else 0
+    ld_dz = _rows_of(d_z, rows, cols, "d_z") if d_z is not None else 0
+    db = _dense(d_bias, torch.float32, (cols,), "d_bias")
+    L = load()
+    ws, size = None, 0
+    if workspace is not None:
+        size = workspace.numel()
+        ws = _dense(workspace, torch.uint8, (size,), "workspace")
+    elif d_bias is not None:
+        size = L.mx_epilogue_workspace_bytes(rows, cols)
+        if size:
+            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                workspace = torch.empty(size, dtype=torch.uint8, device=d_out.device)
+            ws = workspace.data_ptr()
+    _check(L.mx_epilogue_backward(d_out.data_ptr(), _dtype_of(d_out), rows, cols, ld_do,
+                                  0 if z is None else z.data_ptr(), ld_z, act, drop, _Rng(seed, counter),
+                                  0 if d_z is None else d_z.data_ptr(), ld_dz, db, ws, size,
+                                  _stream_at(d_out, stream)))
+    return d_z, d_bias
+
+
+def mx_dropout(x, out, drop: float, seed: int = 0, counter: int = 0, residual=None, stream=None):
+    """out = residual + drop(x) (bf16 or fp32); the gradient of x is the same call
+    on d_out without a residual."""
+    _need(x.dim() == 2, "x: a matrix expected")
+    rows, cols = x.shape
+    ld_x, ld_out = _rows_of(x, rows, cols, "x"), _rows_of(out, rows, cols, "out")
+    ld_r = _rows_of(residual, rows, cols, "residual") if residual is not None else 0
+    for t in (out, residual):
+        _need(t is None or t.dtype == x.dtype, "out, residual: dtype of x expected")
+    _check(load().mx_dropout(x.data_ptr(), _dtype_of(x), rows, cols, ld_x,
+                             0 if residual is None else residual.data_ptr(), ld_r, drop, _Rng(seed, counter),
+                             out.data_ptr(), ld_out, _stream_at(x, stream)))
+    return out
+
+
+class Logprobs:
+    """The device buffers of one scoring (the fields of mx_logprobs in mx.h):
+    logp, entropy, row_max, log_sum [tokens]; top_id, top_logp [tokens, topk].
+    The tensors belong to the scoring and are not exchanged for others; copy
+    into them instead."""
+
+    def __init__(self, tokens: int, vocab: int, topk: int = 0, device="cuda"):
+        torch = _torch()
+        _need(tokens >= 0 and vocab >= 1 and 0 <= topk <= min(vocab, MX_LOGPROB_MAX_TOPK), "logprobs: sizes")
+        new = lambda dtype, *shape: torch.empty(shape, dtype=dtype, device=device)
+        fields = dict(tokens=int(tokens), vocab=int(vocab), topk=int(topk))
+        for n in ("logp", "entropy", "row_max", "log_sum"):
+            fields[n] = new(torch.float32, tokens)
+        fields.update(top_id=new(torch.int32, tokens, topk), top_logp=new(torch.float32, tokens, topk))
+        d = _Logprobs(tokens, vocab, topk, *(fields[n].data_ptr() for n in (
+            "logp", "entropy", "row_max", "log_sum", "top_id", "top_logp")))
+        fields.update(_desc=d, _ref=ctypes.byref(d))
+        self.__dict__.update(fields)
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"a scoring's {name} is not replaced: copy into it")
+
+
+def logprobs(tokens: int, vocab: int, topk: int = 0, device="cuda") -> Logprobs:
+    """Allocate the buffers of a scoring of `tokens` rows over `vocab` entries."""
+    return Logprobs(tokens, vocab, topk, device)
+
+
+def mx_logprob(logits, target, out: Logprobs, scale: float = 1.0, stream=None) -> Logprobs:
+    """Score each row of logits [tokens, vocab] (bf16 or fp32) under softmax(scale
+    * logits): the log probability of target (int64 [tokens]; outside [0, vocab):
+    padding; None: no token is given), the entropy, and the topk largest."""
+    ld = _rows_of(logits, out.tokens, out.vocab, "logits")
+    at = _dense(target, _torch().int64, (out.tokens,), "target")
+    _check(load().mx_logprob(logits.data_ptr(), _dtype_of(logits), ld, at, scale, out._ref, _stream_at(logits, stream)))
+    return out
+
+
+def mx_logprob_backward(logits, target, saved: Logprobs, d_logp, d_entropy, d_logits, scale: float = 1.0,
+                        stream=None):
+    """Gradient of the logits from d_logp and d_entropy (fp32 [tokens] or None),
+    for the scoring `saved` of the same logits, target and scale; d_logits may
+    be logits itself."""
+    torch = _torch()
+    ld = _rows_of(logits, saved.tokens, saved.vocab, "logits")
+    ld_d = _rows_of(d_logits, saved.tokens, saved.vocab, "d_logits")
+    _need(d_logits.dtype == logits.dtype, "d_logits: dtype of logits expected")
+    at = _dense(target, torch.int64, (saved.tokens,), "target")
+    dl = _dense(d_logp, torch.float32, (saved.tokens,), "d_logp")
+    dh = _dense(d_entropy, torch.float32, (saved.tokens,), "d_entropy")
+    _check(load().mx_logprob_backward(logits.data_ptr(), _dtype_of(logits), ld, at, scale, saved._ref, dl, dh,
+                                      d_logits.data_ptr(), ld_d, _stream_at(logits, stream)))
+    return d_logits

@@ -31,6 +31,9 @@ SOURCES = [
     os.path.join(CSRC, "kernels", "swiglu.hip"),
     os.path.join(CSRC, "kernels", "wgrad.hip"),
     os.path.join(CSRC, "kernels", "combine.hip"),
+    os.path.join(CSRC, "kernels", "linear.hip"),
+    os.path.join(CSRC, "kernels", "epilogue.hip"),
+    os.path.join(CSRC, "kernels", "logprob.hip"),
 ]
 
 # -ffp-contract=off: the quantizers' FP32 scale arithmetic must round once per

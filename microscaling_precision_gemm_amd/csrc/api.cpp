@@ -4,9 +4,11 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <mutex>
 
 #include "device/codec.h"
+#include "launch_dense.h"
 #include "launch_moe.h"
 
 namespace {
@@ -738,6 +740,153 @@ mx_status mx_combine_backward(const void* d_out, int32_t dt, int64_t ld_do, cons
   if (tokens == 0 || (!dY && !d_weight)) return MX_OK;
   return hip_status(mxk::launch_combine_bwd(d_out, dt, ld_do, Y, ld_y, rows, slot_row, weight, tokens, topk, cols,
                                             dY, ld_dy, d_weight, reinterpret_cast<hipStream_t>(stream)));
+}
+
+// ---- a dense layer, and a head that scores tokens ---------------------------
+namespace {
+bool valid_act(int32_t a) { return a >= MX_ACT_NONE && a <= MX_ACT_GELU_TANH; }
+
+mx_status make_drop(double drop, mx_rng rng, mxk::Drop* d) {
+  if (!(drop >= 0.0 && drop < 1.0)) return MX_ERR_UNSUPPORTED;
+  const double steps = std::nearbyint(drop * 65536.0);
+  d->threshold = steps > 65535.0 ? 65535u : (uint32_t)steps;
+  d->factor = (float)(65536.0 / (65536.0 - (double)d->threshold));
+  d->seed = rng.seed;
+  d->counter = rng.counter;
+  return MX_OK;
+}
+
+// The sizes of a scoring and the arguments both passes share.
+mx_status make_logprob_args(const void* logits, int32_t ldt, int64_t ld, const int64_t* target, float scale,
+                            const mx_logprobs* p, mxk::LogprobArgs* a) {
+  if (!p) return MX_ERR_NULL;
+  if (!valid_dt(ldt)) return MX_ERR_FORMAT;
+  if (!(scale > 0.0f) || std::isinf(scale)) return MX_ERR_UNSUPPORTED;
+  if (p->tokens < 0 || p->tokens > MX_LOGPROB_MAX_TOKENS || p->vocab < 1 || p->vocab > INT32_MAX || p->topk < 0 ||
+      p->topk > MX_LOGPROB_MAX_TOPK || p->topk > p->vocab || ld < p->vocab)
+    return MX_ERR_SHAPE;
+  if (p->tokens > 0 && (!logits || !p->entropy || !p->row_max || !p->log_sum)) return MX_ERR_NULL;
+  if (!elem_aligned(logits, dt_bytes(ldt)) || !elem_aligned(target, 8) || !elem_aligned(p->entropy, 4) ||
+      !elem_aligned(p->row_max, 4) || !elem_aligned(p->log_sum, 4))
+    return MX_ERR_ALIGN;
+  *a = {logits, (int)ldt, ld, p->tokens, p->vocab, target, scale, p->topk, target ? p->logp : nullptr, p->entropy,
+        p->row_max, p->log_sum, p->top_id, p->top_logp};
+  return MX_OK;
+}
+}  // namespace
+
+mx_status mx_linear(const void* X, int64_t ldx, int64_t M, const mx_tensor* W, const mx_epilogue* ep, void* out,
+                    int32_t odt, int64_t ldo, mx_stream stream) {
+  if (!W) return MX_ERR_NULL;
+  mx_status st = check_tensor(W, W->rows, W->cols);
+  if (st != MX_OK) return st;
+  if ((!saved_fmt(W->fmt) && W->fmt != MX_MXFP4_E2M1 && W->fmt != MX_NVFP4) || W->layout != MX_LAYOUT_ROWS)
+    return MX_ERR_UNSUPPORTED;
+  const int64_t N = W->rows, K = W->cols, most = (int64_t)1 << 26;
+  if (M < 0 || K % 32 || M >= most || N >= most || M * N > ((int64_t)1 << 35)) return MX_ERR_SHAPE;
+  st = check_matrix(X, MX_BF16, M, K, ldx);
+  if (st != MX_OK) return st;
+  st = check_output(out, odt, M, N, ldo);
+  if (st != MX_OK) return st;
+  const mx_epilogue none = {};
+  const mx_epilogue& e = ep ? *ep : none;
+  if (!valid_act(e.act) || (e.bias && !valid_dt(e.bias_dt))) return MX_ERR_FORMAT;
+  if (!elem_aligned(e.bias, dt_bytes(e.bias_dt))) return MX_ERR_ALIGN;
+  if (e.residual) {
+    st = check_output(e.residual, odt, M, N, e.ld_residual);
+    if (st != MX_OK) return st;
+  }
+  if (e.z) {
+    st = check_output(e.z, odt, M, N, e.ld_z);
+    if (st != MX_OK) return st;
+  }
+  mxk::LinearArgs a = {static_cast<const uint16_t*>(X), ldx, M, N, K, W->fmt, static_cast<const uint8_t*>(W->codes),
+                       W->scales, W->tensor_scale,
+                       {e.bias, (int)e.bias_dt, e.act, e.z, e.ld_z, e.residual, e.ld_residual, out, ldo, (int)odt, {}}};
+  st = make_drop(e.drop, e.rng, &a.ep.drop);
+  if (st != MX_OK) return st;
+  if (M * N == 0) return MX_OK;
+  return hip_status(mxk::launch_linear(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t mx_epilogue_workspace_bytes(int64_t rows, int64_t cols) {
+  if (rows < 0 || rows > INT32_MAX || cols < 0 || cols > INT32_MAX) return 0;
+  return mxk::epilogue_workspace(rows, cols);
+}
+
+mx_status mx_epilogue_backward(const void* d_out, int32_t dt, int64_t rows, int64_t cols, int64_t ld_do, const void* z,
+                               int64_t ld_z, int32_t act, double drop, mx_rng rng, void* d_z, int64_t ld_dz,
+                               float* d_bias, void* workspace, size_t workspace_bytes, mx_stream stream) {
+  if (rows > INT32_MAX || cols > INT32_MAX) return MX_ERR_SHAPE;
+  mx_status st = check_output(d_out, dt, rows, cols, ld_do);
+  if (st != MX_OK) return st;
+  if (!valid_act(act)) return MX_ERR_FORMAT;
+  if (act != MX_ACT_NONE) {
+    st = check_output(z, dt, rows, cols, ld_z);
+    if (st != MX_OK) return st;
+  }
+  if (d_z) {
+    st = check_output(d_z, dt, rows, cols, ld_dz);
+    if (st != MX_OK) return st;
+  }
+  if (!elem_aligned(d_bias, 4)) return MX_ERR_ALIGN;
+  mxk::EpilogueBwdArgs a = {d_out, (int)dt, ld_do, rows, cols, z, ld_z, act, {}, d_z, ld_dz, d_bias,
+                            static_cast<float*>(workspace)};
+  st = make_drop(drop, rng, &a.drop);
+  if (st != MX_OK) return st;
+  if (d_bias) {
+    const size_t need = mxk::epilogue_workspace(rows, cols);
+    if (need > 0) {
+      if (!workspace) return MX_ERR_NULL;
+      if (workspace_bytes < need) return MX_ERR_SHAPE;
+      if (!aligned16(workspace)) return MX_ERR_ALIGN;
+    }
+  }
+  if (cols == 0 || (rows == 0 && !d_bias) || (!d_z && !d_bias)) return MX_OK;
+  return hip_status(mxk::launch_epilogue_bwd(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+mx_status mx_dropout(const void* x, int32_t dt, int64_t rows, int64_t cols, int64_t ld_x, const void* residual,
+                     int64_t ld_residual, double drop, mx_rng rng, void* out, int64_t ld_out, mx_stream stream) {
+  if (rows > INT32_MAX || cols > INT32_MAX) return MX_ERR_SHAPE;
+  mx_status st = check_output(x, dt, rows, cols, ld_x);
+  if (st != MX_OK) return st;
+  st = check_output(out, dt, rows, cols, ld_out);
+  if (st != MX_OK) return st;
+  if (residual) {
+    st = check_output(residual, dt, rows, cols, ld_residual);
+    if (st != MX_OK) return st;
+  }
+  mxk::DropoutArgs a = {x, ld_x, rows, cols, residual, ld_residual, out, ld_out, (int)dt, {}};
+  st = make_drop(drop, rng, &a.drop);
+  if (st != MX_OK) return st;
+  if (rows * cols == 0) return MX_OK;
+  return hip_status(mxk::launch_dropout(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+mx_status mx_logprob(const void* logits, int32_t ldt, int64_t ld, const int64_t* target, float scale,
+                     const mx_logprobs* out, mx_stream stream) {
+  mxk::LogprobArgs a;
+  const mx_status st = make_logprob_args(logits, ldt, ld, target, scale, out, &a);
+  if (st != MX_OK) return st;
+  if (a.tokens == 0) return MX_OK;
+  if ((target && !out->logp) || (a.topk > 0 && (!a.top_id || !a.top_logp))) return MX_ERR_NULL;
+  if (!elem_aligned(a.logp, 4) || !elem_aligned(a.top_id, 4) || !elem_aligned(a.top_logp, 4)) return MX_ERR_ALIGN;
+  return hip_status(mxk::launch_logprob(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+mx_status mx_logprob_backward(const void* logits, int32_t ldt, int64_t ld, const int64_t* target, float scale,
+                              const mx_logprobs* saved, const float* d_logp, const float* d_entropy, void* d_logits,
+                              int64_t ld_d, mx_stream stream) {
+  mxk::LogprobArgs a;
+  mx_status st = make_logprob_args(logits, ldt, ld, target, scale, saved, &a);
+  if (st != MX_OK) return st;
+  st = check_output(d_logits, ldt, a.tokens, a.vocab, ld_d);
+  if (st != MX_OK) return st;
+  if (!elem_aligned(d_logp, 4) || !elem_aligned(d_entropy, 4)) return MX_ERR_ALIGN;
+  if (a.tokens == 0) return MX_OK;
+  return hip_status(
+      mxk::launch_logprob_bwd(a, d_logp, d_entropy, d_logits, ld_d, reinterpret_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,153 @@
+// epilogue.hip -- dropout, and the backward pass of a product's epilogue
+//   out = residual + drop(act(z)):   d_z = drop'(d_out) act'(z),  d_bias = sum_r d_z[r, :]
+// The mask is drawn again from its counters and never stored.
+#include <type_traits>
+
+#include "../device/act.h"
+#include "../device/chunk8.h"
+
+namespace mxk {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+template <int DT>
+__global__ __launch_bounds__(kThreads) void k_dropout(DropoutArgs a, uint32_t per_row, bool vec_x, bool vec_r,
+                                                      bool vec_o) {
+  const int64_t total = a.M * per_row;
+  for (int64_t q = (int64_t)blockIdx.x * kThreads + threadIdx.x; q < total; q += (int64_t)gridDim.x * kThreads) {
+    const int64_t r = q / per_row, c = (q - r * per_row) * 8;
+    const int n = (int)(a.N - c < 8 ? a.N - c : 8);
+    float v[8], w[8];
+    load_chunk<DT>(a.x, r * a.ld_x + c, n, vec_x, v);
+    if (a.residual) load_chunk<DT>(a.residual, r * a.ld_r + c, n, vec_r, w);
+    if (a.drop.threshold) drop_chunk(a.drop, (uint64_t)q, v);
+    if (a.residual) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = w[i] + v[i];
+    }
+    store_chunk<DT>(a.out, r * a.ld_o + c, n, vec_o, v);
+  }
+}
+
+// A workgroup takes `tx` chunks of 8 columns and a run of rows, kThreads / tx at
+// a time; each thread sums its columns, then the threads of one chunk are added in
+// order through LDS.
+struct BwdPlan {
+  uint32_t tx;         // chunks side by side, a power of two
+  uint32_t stripes;    // workgroups along the columns
+  uint32_t parts;      // runs of rows
+  int64_t rows;        // rows of a run
+};
+
+inline BwdPlan plan_bwd(int64_t M, int64_t N) {
+  const int64_t chunks = (N + 7) / 8;
+  BwdPlan p;
+  p.tx = 1;
+  while (p.tx < kThreads && p.tx < chunks) p.tx *= 2;
+  p.stripes = (uint32_t)((chunks + p.tx - 1) / p.tx);
+  const int64_t ty = kThreads / p.tx;
+  int64_t parts = (2048 + p.stripes - 1) / p.stripes;           // workgroups that fill the card
+  const int64_t most = (M + 8 * ty - 1) / (8 * ty);             // at least 8 rows a thread
+  parts = parts < most ? parts : most;
+  p.rows = (M + parts - 1) / parts;
+  p.parts = (uint32_t)((M + p.rows - 1) / p.rows);
+  return p;
+}
+
+template <int DT>
+__global__ __launch_bounds__(kThreads) void k_epilogue_bwd(EpilogueBwdArgs a, BwdPlan p, float* sums, bool vec_do,
+                                                           bool vec_z, bool vec_dz) {
+  __shared__ float part[kThreads][9];
+  const uint32_t tx = threadIdx.x & (p.tx - 1), ty = threadIdx.x / p.tx, ny = kThreads / p.tx;
+  const int64_t chunk = (int64_t)blockIdx.x * p.tx + tx, c = chunk * 8;
+  const int64_t per_row = (a.N + 7) / 8;
+  const int n = (int)(a.N - c < 8 ? a.N - c : 8);
+  const int64_t r0 = (int64_t)blockIdx.y * p.rows, r1 = r0 + p.rows < a.M ? r0 + p.rows : a.M;
+  float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (n > 0)
+    with_act(a.act, [&](auto kind) {
+      constexpr int ACT = decltype(kind)::value;
+      for (int64_t r = r0 + ty; r < r1; r += ny) {
+        float d[8], z[8];
+        load_chunk<DT>(a.d_out, r * a.ld_do + c, n, vec_do, d);
+        if constexpr (ACT != ACT_NONE) load_chunk<DT>(a.z, r * a.ld_z + c, n, vec_z, z);
+        if constexpr (ACT != ACT_NONE) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d[i] *= act_slope<ACT>(z[i]);
+        }
+        if (a.drop.threshold) drop_chunk(a.drop, (uint64_t)(r * per_row + chunk), d);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] += d[i];
+        if (a.d_z) store_chunk<DT>(a.d_z, r * a.ld_dz + c, n, vec_dz, d);
+      }
+    });
+  if (!sums) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) part[threadIdx.x][i] = sum[i];
+  __syncthreads();
+  if (ty == 0 && n > 0) {
+    for (uint32_t y = 1; y < ny; ++y)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += part[y * p.tx + tx][i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) sums[(int64_t)blockIdx.y * a.N + c + i] = sum[i];
+  }
+}
+
+// d_bias[c] = the sum over the runs of rows, in order
+__global__ __launch_bounds__(kThreads) void k_join_sums(const float* __restrict__ parts, uint32_t n, int64_t N,
+                                                        float* __restrict__ out) {
+  const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (c >= N) return;
+  float s = 0.0f;
+  for (uint32_t i = 0; i < n; ++i) s += parts[i * N + c];
+  out[c] = s;
+}
+
+}  // namespace
+
+hipError_t launch_dropout(const DropoutArgs& a, hipStream_t s) {
+  const int64_t per_row = (a.N + 7) / 8;
+  const int64_t blocks = (a.M * per_row + kThreads - 1) / kThreads;
+  const dim3 grid((uint32_t)(blocks < 65536 ? blocks : 65536));
+  const bool vx = rows_aligned16(a.x, a.ld_x, a.dt), vr = rows_aligned16(a.residual, a.ld_r, a.dt),
+             vo = rows_aligned16(a.out, a.ld_o, a.dt);
+  if (a.dt == DT_BF16)
+    hipLaunchKernelGGL((k_dropout<DT_BF16>), grid, dim3(kThreads), 0, s, a, (uint32_t)per_row, vx, vr, vo);
+  else
+    hipLaunchKernelGGL((k_dropout<DT_F32>), grid, dim3(kThreads), 0, s, a, (uint32_t)per_row, vx, vr, vo);
+  return hipGetLastError();
+}
+
+size_t epilogue_workspace(int64_t M, int64_t N) {
+  if (M == 0 || N == 0) return 0;
+  const BwdPlan p = plan_bwd(M, N);
+  return p.parts > 1 ? (size_t)p.parts * (size_t)N * sizeof(float) : 0;
+}
+
+hipError_t launch_epilogue_bwd(const EpilogueBwdArgs& a, hipStream_t s) {
+  const BwdPlan p = a.M > 0 ? plan_bwd(a.M, a.N) : BwdPlan{1, 0, 0, 0};
+  float* sums = !a.d_bias ? nullptr : p.parts > 1 ? a.parts : a.d_bias;
+  if (p.parts > 0) {
+    const dim3 grid(p.stripes, p.parts);
+    const bool vd = rows_aligned16(a.d_out, a.ld_do, a.dt), vz = rows_aligned16(a.z, a.ld_z, a.dt),
+               vo = rows_aligned16(a.d_z, a.ld_dz, a.dt);
+    if (a.dt == DT_BF16)
+      hipLaunchKernelGGL((k_epilogue_bwd<DT_BF16>), grid, dim3(kThreads), 0, s, a, p, sums, vd, vz, vo);
+    else
+      hipLaunchKernelGGL((k_epilogue_bwd<DT_F32>), grid, dim3(kThreads), 0, s, a, p, sums, vd, vz, vo);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (a.d_bias && p.parts != 1) {
+    hipLaunchKernelGGL(k_join_sums, dim3((uint32_t)((a.N + kThreads - 1) / kThreads)), dim3(kThreads), 0, s, a.parts,
+                       p.parts, a.N, a.d_bias);
+    return hipGetLastError();
+  }
+  return hipSuccess;
+}
+
+}  // namespace mxk

@@ -1,0 +1,328 @@
+// logprob.hip -- log probabilities of given tokens, with the entropy of each row
+// and its largest entries, and their gradient.  For a row x, s the scale, m its
+// largest entry, d_v = s (x_v - m) and S = sum_v e^d_v:
+//   log p_v = d_v - log S,   H = log S - (sum_v e^d_v d_v) / S
+//   d_x_v   = s (d_logp (delta_v,target - p_v) - d_entropy p_v (log p_v + H))
+// One pass over the row: a lane keeps the largest entry it has seen and both sums
+// relative to it, and rescales them when it changes.  d is held at -150 and above:
+// e^d is 0 there, and 0 times it too, so entries of minus infinity add nothing.
+//
+// The k largest entries: a wave keeps its list one key a lane, sorted; a key is
+// the entry's value in an order of integers above its index's complement, so equal
+// entries go by lower index.  Entries no larger than the list's k-th are passed
+// over 512 at a time.
+#include "../device/chunk8.h"
+#include "../device/exp.h"
+#include "../device/wave.h"
+
+namespace mxk {
+
+namespace {
+
+constexpr float kLn2 = 0.693147180559945309417f;
+constexpr float kLowest = -3.402823466e38f;  // where a running maximum starts
+
+// An integer order of FP32 values (-0 as 0); -inf, NaN: 0.
+__device__ inline uint32_t order_of(float x) {
+  const uint32_t u = f2u(x + 0.0f);
+  const uint32_t o = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+  return x > -__builtin_inff() ? o : 0u;
+}
+__device__ inline float value_of(uint32_t o) { return u2f(o & 0x80000000u ? o ^ 0x80000000u : ~o); }
+
+__device__ inline uint64_t lane_read64(uint64_t v, uint32_t src) {
+  return (uint64_t)lane_read((uint32_t)(v >> 32), src) << 32 | lane_read((uint32_t)v, src);
+}
+__device__ inline uint64_t uniform64(uint64_t v, int lane) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+         (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+
+// The k largest keys seen by a wave, one a lane in falling order (0: none).
+struct TopList {
+  uint64_t key = 0;
+  uint64_t kth = 0;  // the k-th (uniform)
+  __device__ void insert(uint64_t c, uint32_t lane, int k) {
+    if (c <= kth) return;
+    const uint32_t at = (uint32_t)__popcll(__builtin_amdgcn_ballot_w64(key > c));
+    const uint64_t above = lane_read64(key, lane - 1u);
+    key = lane < at ? key : lane == at ? c : above;
+    kth = uniform64(key, k - 1);
+  }
+};
+
+// The largest 16-bit prefix T (as the top half of a word, the rest 0) such that at
+// least k lanes have v >= T; 0 if fewer lanes have any.
+__device__ inline uint32_t kth_prefix(uint32_t v, int k) {
+  uint32_t t = 0;
+#pragma unroll
+  for (int b = 31; b >= 16; --b) {
+    const uint32_t c = t | (1u << b);
+    if (__popcll(__builtin_amdgcn_ballot_w64(v >= c)) >= k) t = c;
+  }
+  return t;
+}
+
+// Takes a strip of 512 entries, 8 consecutive ones a lane, the lane's first at
+// index `base`.
+__device__ inline void take_strip(TopList& list, const float (&v)[8], float largest, int64_t base, uint32_t lane,
+                                  int k) {
+  uint32_t bound = (uint32_t)(list.kth >> 32);
+  const uint32_t mine = order_of(largest);
+  const uint64_t some = __builtin_amdgcn_ballot_w64(mine > bound);
+  if (some == 0) return;
+  if (__popcll(some) > k) {  // many: only what the k-th largest of the lanes' maxima allows can stay
+    const uint32_t t = kth_prefix(mine, k);
+    bound = t > bound ? t : bound;
+  }
+  bound = bound > 0 ? bound : 1u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t o = order_of(v[i]);
+    uint64_t rest = __builtin_amdgcn_ballot_w64(o >= bound);
+    while (rest) {
+      const int src = __builtin_ctzll(rest);
+      rest &= rest - 1;
+      const uint32_t value = (uint32_t)__builtin_amdgcn_readlane((int)o, src);
+      const uint32_t index = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)base, src) + i;
+      list.insert((uint64_t)value << 32 | ~index, lane, k);
+    }
+  }
+}
+
+// Running statistics: the largest entry, the sum of e^d and of e^d d / ln 2.
+struct Stats {
+  float m = kLowest, s = 0.0f, w = 0.0f;
+  // the same relative to a maximum `to` >= m; c = scale / ln 2
+  __device__ void move(float to, float c) {
+    const float d = __builtin_elementwise_maximum((m - to) * c, -216.0f);
+    const float f = __builtin_amdgcn_exp2f(d);
+    w = f * fmaf(d, s, w);
+    s *= f;
+    m = to;
+  }
+  __device__ void add(const float (&v)[8], float largest, float c) {
+    move(fmaxf(m, largest), c);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float d = __builtin_elementwise_maximum((v[i] - m) * c, -216.0f);
+      const float e = __builtin_amdgcn_exp2f(d);
+      s += e;
+      w = fmaf(e, d, w);
+    }
+  }
+  __device__ void join(float m2, float s2, float w2, float c) {
+    const float to = fmaxf(m, m2);
+    move(to, c);
+    Stats o;
+    o.m = m2;
+    o.s = s2;
+    o.w = w2;
+    o.move(to, c);
+    s += o.s;
+    w += o.w;
+  }
+};
+
+// Entries 8 q - shift .. 8 q - shift + 7 of a row, those outside it as -inf; a
+// chunk inside it is 16-byte aligned.
+template <int DT>
+__device__ inline void load_part(const void* row, int64_t first, int64_t vocab, float (&v)[8]) {
+  if (first >= 0 && first + 8 <= vocab) return load8<DT>(row, first, v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t at = first + i;
+    v[i] = at >= 0 && at < vocab ? load1<DT>(row, at) : -__builtin_inff();
+  }
+}
+// entries by which a row starts past a 16-byte boundary
+template <int DT>
+__device__ inline int shift_of(const void* row) {
+  return (int)((reinterpret_cast<uintptr_t>(row) & 15u) / (DT == DT_BF16 ? 2 : 4));
+}
+__device__ inline float max8(const float (&v)[8]) {
+  return fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
+}
+
+// One workgroup a row.
+template <int DT, int NW>
+__global__ __launch_bounds__(NW * 64) void k_logprob(LogprobArgs a) {
+  __shared__ float part[3][NW];
+  __shared__ uint64_t keys[NW * kMaxAlternatives];
+  __shared__ uint32_t rank[NW * kMaxAlternatives];
+  const int64_t t = blockIdx.x;
+  const uint32_t lane = threadIdx.x & 63u, wid = threadIdx.x >> 6;
+  const int k = a.topk;
+  const int64_t target = a.target ? a.target[t] : 0;
+  if (target < 0 || target >= a.vocab) {  // padding
+    if (threadIdx.x == 0) {
+      if (a.logp) a.logp[t] = 0.0f;
+      a.entropy[t] = 0.0f;
+      a.row_max[t] = 0.0f;
+      a.log_sum[t] = 0.0f;
+    }
+    if ((int)threadIdx.x < k) {
+      a.top_id[t * k + threadIdx.x] = -1;
+      a.top_logp[t * k + threadIdx.x] = -__builtin_inff();
+    }
+    return;
+  }
+  const char* row = static_cast<const char*>(a.logits) + t * a.ld * (DT == DT_BF16 ? 2 : 4);
+  const int shift = shift_of<DT>(row);
+  const int64_t chunks = (a.vocab + shift + 7) / 8;
+  const float c = a.scale * kLog2e;
+  Stats st;
+  TopList list;
+  for (int64_t q0 = 0; q0 < chunks; q0 += NW * 64) {
+    const int64_t first = (q0 + threadIdx.x) * 8 - shift;
+    float v[8];
+    load_part<DT>(row, first, a.vocab, v);
+    const float largest = max8(v);
+    st.add(v, largest, c);
+    if (k > 0) take_strip(list, v, largest, first, lane, k);
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) {
+    const float m2 = u2f(lane_read(f2u(st.m), lane ^ off)), s2 = u2f(lane_read(f2u(st.s), lane ^ off)),
+                w2 = u2f(lane_read(f2u(st.w), lane ^ off));
+    // (the lower lane's first in both, so that both get the same bits)
+    Stats o;
+    const bool low = (lane & off) == 0;
+    o.m = low ? st.m : m2;
+    o.s = low ? st.s : s2;
+    o.w = low ? st.w : w2;
+    o.join(low ? m2 : st.m, low ? s2 : st.s, low ? w2 : st.w, c);
+    st = o;
+  }
+  if (lane == 0) {
+    part[0][wid] = st.m;
+    part[1][wid] = st.s;
+    part[2][wid] = st.w;
+  }
+  if ((int)lane < k) {
+    keys[wid * k + lane] = list.key;
+    rank[wid * k + lane] = 0;
+  }
+  __syncthreads();
+  Stats all;
+  all.m = part[0][0];
+  all.s = part[1][0];
+  all.w = part[2][0];
+#pragma unroll
+  for (int i = 1; i < NW; ++i) all.join(part[0][i], part[1][i], part[2][i], c);
+  // s is 0 only where no entry is above -inf (the largest one adds 1)
+  const bool none = all.s == 0.0f;
+  const float m = none ? -__builtin_inff() : all.m;
+  const float log_sum = none ? 0.0f : logf(all.s);
+  if (threadIdx.x == 0) {
+    a.row_max[t] = m;
+    a.log_sum[t] = log_sum;
+    a.entropy[t] = none ? 0.0f : log_sum - kLn2 * (all.w / all.s);
+    if (a.logp) a.logp[t] = none ? -__builtin_inff() : a.scale * (load1<DT>(row, target) - m) - log_sum;
+  }
+  if (k == 0) return;
+  // a key's place is the number of larger ones; each wave counts its own list
+  for (uint32_t i = lane; i < (uint32_t)(NW * k); i += 64) {
+    const uint64_t key = keys[i];
+    uint32_t larger = 0;
+    for (int j = 0; j < k; ++j) larger += keys[wid * k + j] > key;
+    if (larger) atomicAdd(&rank[i], larger);
+  }
+  __syncthreads();
+  for (uint32_t i = threadIdx.x; i < (uint32_t)(NW * k); i += NW * 64) {
+    const uint64_t key = keys[i];
+    if (key && rank[i] < (uint32_t)k) {
+      a.top_id[t * k + rank[i]] = (int32_t)~(uint32_t)key;
+      a.top_logp[t * k + rank[i]] = a.scale * (value_of((uint32_t)(key >> 32)) - m) - log_sum;
+    }
+  }
+  if (wid == 0) {
+    int there = 0;
+    for (uint32_t i = lane; i < (uint32_t)(NW * k); i += 64) there += keys[i] != 0;
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) there += (int)lane_read((uint32_t)there, lane ^ off);
+    if ((int)lane < k && (int)lane >= there) {
+      a.top_id[t * k + lane] = -1;
+      a.top_logp[t * k + lane] = -__builtin_inff();
+    }
+  }
+}
+
+constexpr int kBwdChunks = 4;                     // chunks of 8 a thread
+constexpr int64_t kBwdPart = 256 * kBwdChunks;    // chunks of a workgroup
+
+template <int DT>
+__global__ __launch_bounds__(256) void k_logprob_bwd(LogprobArgs a, const float* __restrict__ d_logp,
+                                                     const float* __restrict__ d_entropy, void* d_logits, int64_t ld_d,
+                                                     uint32_t parts) {
+  constexpr int EB = DT == DT_BF16 ? 2 : 4;
+  const int64_t total = a.tokens * parts;
+  for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
+    const int64_t t = id / parts, q0 = (id - t * parts) * kBwdPart + threadIdx.x;
+    const char* row = static_cast<const char*>(a.logits) + t * a.ld * EB;
+    char* out = static_cast<char*>(d_logits) + t * ld_d * EB;
+    const int shift = shift_of<DT>(out);
+    const bool vec_in = shift_of<DT>(row) == shift;
+    const int64_t target = a.target ? a.target[t] : -1;
+    const float m = a.row_max[t], log_sum = a.log_sum[t], H = a.entropy[t];
+    const bool nothing = (a.target && (target < 0 || target >= a.vocab)) || m == -__builtin_inff();
+    const float dl = a.target && d_logp ? a.scale * d_logp[t] : 0.0f;
+    const float dh = d_entropy ? a.scale * d_entropy[t] : 0.0f;
+#pragma unroll
+    for (int u = 0; u < kBwdChunks; ++u) {
+      const int64_t first = (q0 + u * 256) * 8 - shift;
+      if (first >= a.vocab) break;
+      float v[8];
+      const bool whole = first >= 0 && first + 8 <= a.vocab;
+      if (nothing) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+      } else {
+        if (whole && vec_in) load8<DT>(row, first, v);
+        else
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            v[i] = first + i >= 0 && first + i < a.vocab ? load1<DT>(row, first + i) : -__builtin_inff();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float lp = __builtin_elementwise_maximum(fmaf(a.scale, v[i] - m, -log_sum), -150.0f);
+          const float p = exp_nonpos(lp);
+          const float d = -p * fmaf(dh, lp + H, dl);
+          v[i] = first + i == target ? d + dl : d;
+        }
+      }
+      if (whole) store8<DT>(out, first, v);
+      else
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (first + i >= 0 && first + i < a.vocab) store1<DT>(out, first + i, v[i]);
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_logprob(const LogprobArgs& a, hipStream_t s) {
+  const dim3 grid((uint32_t)a.tokens);
+#define MXK_LP(DT) hipLaunchKernelGGL((k_logprob<DT, 16>), grid, dim3(1024), 0, s, a)
+  if (a.dt == DT_BF16) MXK_LP(DT_BF16);
+  else MXK_LP(DT_F32);
+#undef MXK_LP
+  return hipGetLastError();
+}
+
+hipError_t launch_logprob_bwd(const LogprobArgs& a, const float* d_logp, const float* d_entropy, void* d_logits,
+                              int64_t ld_d, hipStream_t s) {
+  const int64_t parts = ((a.vocab + 14) / 8 + kBwdPart - 1) / kBwdPart;  // (a row may start inside a chunk)
+  const int64_t total = a.tokens * parts;
+  const dim3 grid((uint32_t)(total < (1 << 22) ? total : (1 << 22)));
+  if (a.dt == DT_BF16)
+    hipLaunchKernelGGL((k_logprob_bwd<DT_BF16>), grid, dim3(256), 0, s, a, d_logp, d_entropy, d_logits, ld_d,
+                       (uint32_t)parts);
+  else
+    hipLaunchKernelGGL((k_logprob_bwd<DT_F32>), grid, dim3(256), 0, s, a, d_logp, d_entropy, d_logits, ld_d,
+                       (uint32_t)parts);
+  return hipGetLastError();
+}
+
+}  // namespace mxk
