@@ -783,7 +783,7 @@ mx_status mx_linear(const void* X, int64_t ldx, int64_t M, const mx_tensor* W, c
   if ((!saved_fmt(W->fmt) && W->fmt != MX_MXFP4_E2M1 && W->fmt != MX_NVFP4) || W->layout != MX_LAYOUT_ROWS)
     return MX_ERR_UNSUPPORTED;
   const int64_t N = W->rows, K = W->cols, most = (int64_t)1 << 26;
-  if (M < 0 || K % 32 || M >= most || N >= most || M * N > ((int64_t)1 << 35)) return MX_ERR_SHAPE;
+  if (M < 0 || K % 32 || K > INT32_MAX || M >= most || N >= most || M * N > ((int64_t)1 << 35)) return MX_ERR_SHAPE;
   st = check_matrix(X, MX_BF16, M, K, ldx);
   if (st != MX_OK) return st;
   st = check_output(out, odt, M, N, ldo);
