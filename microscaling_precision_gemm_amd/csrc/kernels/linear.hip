@@ -176,32 +176,37 @@ hipError_t launch_direct(const LinearArgs& a, hipStream_t s) {
 }
 
 // ---- operands through LDS ---------------------------------------------------
-// A workgroup takes a tile of BM tokens x BN columns, each wave WM x WN of it
-// (v_mfma_f32_32x32x16_bf16).  A stage holds 64 elements of K of every row:
-// 128 bytes of X, 32 or 64 bytes of codes, copied to LDS by 16-byte
-// global-to-LDS loads, three stages in a ring, so that one barrier a stage is
-// enough: behind it the stage has landed for all waves and the one before it is
-// no longer read.  Lane half h takes elements 32 h .. 32 h + 31 of a stage
-// (one block), 8 of them for each of four instructions; W is decoded from the
-// codes as it leaves LDS.  The 16-byte chunks of a row are exchanged by row
-// number on their way in, so that 16 neighbouring rows' chunks lie in all banks.
+// A workgroup takes a tile of BM tokens x BN columns, each wave a part of it
+// (v_mfma_f32_32x32x16_bf16).  A step is 64 elements of K: 128 bytes of every row
+// of X, and 64 bytes of every weight row for one step (8-bit codes) or two
+// (4-bit).  Both come by 16-byte global-to-LDS copies, three steps (or units of
+// codes) in a ring, so that one barrier a step is enough: behind it the next step
+// has landed for all waves and this one is no longer read.  Lane half h takes
+// elements 32 h .. 32 h + 31 of a step (one block), 8 of them for each of four
+// instructions; W is decoded from the codes as it leaves LDS.
+//
+// One copy instruction fills 1 KB of LDS in lane order: 8 rows of X or 16 of
+// codes, each of them whole and in order, since lanes out of order cost the L1
+// twice the requests (974 requests a step and 65% of the cycles with products;
+// a permutation of chunks and 32-byte pieces of codes did that).  The rows of one
+// copy are BM / 8 (BN / 16) apart and the copies 1040 bytes, so that 16
+// neighbouring rows, which are read together, lie in all banks.
 typedef float v16f __attribute__((ext_vector_type(16)));
 
-template <int FMT, int BM, int BN>
-struct Stage {
-  static constexpr int kXBytes = BM * 128;
-  static constexpr int kRow = 2 * kBlockBytes<FMT>;  // code bytes of a row
-  static constexpr int kBytes = kXBytes + BN * kRow;
-  static constexpr int kCount = 3;
-};
+constexpr uint32_t kCopyPitch = 1040;
 
-// slot of chunk c among the chunks of row r
-__device__ inline uint32_t x_slot(uint32_t r, uint32_t c) { return r * 8 + (c ^ ((r >> 1) & 7u)); }
-template <int FMT>
-__device__ inline uint32_t w_slot(uint32_t r, uint32_t c) {
-  if constexpr (kFourBit<FMT>) return r * 2 + (c ^ ((r >> 3) & 1u));
-  else return r * 4 + (c ^ ((r >> 2) & 3u));
-}
+template <int BM, int BN>
+struct Ring {
+  static constexpr uint32_t kXBytes = BM / 8 * kCopyPitch, kWBytes = BN / 16 * kCopyPitch;
+  static constexpr uint32_t kCount = 3, kBytes = kCount * (kXBytes + kWBytes);
+  // byte offsets of chunk c (16 bytes) of row r
+  static __device__ uint32_t x(uint32_t r, uint32_t c) {
+    return r % (BM / 8) * kCopyPitch + r / (BM / 8) * 128 + c * 16;
+  }
+  static __device__ uint32_t w(uint32_t r, uint32_t c) {
+    return r % (BN / 16) * kCopyPitch + r / (BN / 16) * 64 + c * 16;
+  }
+};
 
 // Tile of workgroup `id`: the ids of one XCD (id mod 8) take neighbouring tiles,
 // in groups of 4 tiles of tokens.
@@ -230,15 +235,33 @@ __device__ inline void stage_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// Order a region as MF matrix instructions with D LDS reads behind the first
+// ones, and M vector-memory and V vector instructions spread between them.
+__device__ inline void region() { __builtin_amdgcn_sched_barrier(0); }
+template <int MF, int D, int M, int V, int I = 0>
+__device__ inline void spread() {
+  if constexpr (I < MF) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    constexpr int d = I < MF / 2 ? ((I + 1) * D + MF / 2 - 1) / (MF / 2) - (I * D + MF / 2 - 1) / (MF / 2) : 0;
+    constexpr int m = ((I + 1) * M + MF - 1) / MF - (I * M + MF - 1) / MF;
+    constexpr int v = ((I + 1) * V + MF - 1) / MF - (I * V + MF - 1) / MF;
+    if constexpr (d > 0) __builtin_amdgcn_sched_group_barrier(0x100, d, 0);
+    if constexpr (m > 0) __builtin_amdgcn_sched_group_barrier(0x010, m, 0);
+    if constexpr (v > 0) __builtin_amdgcn_sched_group_barrier(0x002, v, 0);
+    spread<MF, D, M, V, I + 1>();
+  }
+}
+
 template <int FMT, int BM, int BN, int WAVES_M, int WAVES_N>
 __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_linear_tile(LinearArgs a, EpilogueVec vec,
                                                                           uint32_t tiles_m, uint32_t tiles_n) {
-  using S = Stage<FMT, BM, BN>;
+  using R = Ring<BM, BN>;
   constexpr int NW = WAVES_M * WAVES_N, TM = BM / WAVES_M / 32, TN = BN / WAVES_N / 32;
-  constexpr int kXCopies = BM * 8 / 64 / NW, kWCopies = BN * S::kRow / 1024 / NW;  // of 1 KB, a wave
-  constexpr int kCopies = kXCopies + kWCopies;
-  static_assert(BM * 8 % (64 * NW) == 0 && BN * S::kRow % (1024 * NW) == 0, "copies of a stage");
+  constexpr int kWCopies = BN / 16 / NW;  // of a unit, a wave
+  constexpr bool kTwoSteps = kFourBit<FMT>;  // a unit of codes is two steps
+  static_assert(BM / 8 == 4 * NW && BN / 16 == kWCopies * NW && kWCopies == 2, "copies of a wave");
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  uint8_t* const wring = smem + R::kCount * R::kXBytes;
   uint32_t ti, tj;
   tile_at(blockIdx.x, tiles_m, tiles_n, &ti, &tj);
   const int64_t m0 = (int64_t)ti * BM, n0 = (int64_t)tj * BN;
@@ -247,54 +270,52 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_linear_tile(Linea
   const uint32_t wm = wid / WAVES_N * (BM / WAVES_M), wn = wid % WAVES_N * (BN / WAVES_N);
   const uint32_t l = lane & 31u, h = lane >> 5;
   const int64_t row_bytes = a.K / 32 * kBlockBytes<FMT>;
-  const uint32_t steps = (uint32_t)(a.K / 64);
+  const uint32_t pairs = (uint32_t)(a.K / 128);  // of steps
+  const uint32_t units = kTwoSteps ? pairs : 2 * pairs;
 
-  // this lane's source of each of the wave's copies: slot 64 i + lane of a
-  // stage's X (or codes) holds the chunk that x_slot (w_slot) puts there; rows
-  // past the last are the last one (their results are not stored)
-  const uint8_t* src[kCopies];
+  // this lane's source of each of the wave's copies; rows past the last are the
+  // last one (their results are not stored)
+  const uint8_t* xsrc[4];
+  const uint8_t* wsrc[kWCopies];
 #pragma unroll
-  for (int i = 0; i < kXCopies; ++i) {
-    const uint32_t slot = (wid * kXCopies + i) * 64 + lane, r = slot / 8, c = slot % 8 ^ ((r >> 1) & 7u);
-    const int64_t m = m0 + r < a.M ? m0 + r : a.M - 1;
-    src[i] = reinterpret_cast<const uint8_t*>(a.x + m * a.ld_x) + c * 16;
+  for (int i = 0; i < 4; ++i) {
+    const int64_t m = m0 + (wid * 4 + i) + lane / 8 * (BM / 8);
+    xsrc[i] = reinterpret_cast<const uint8_t*>(a.x + (m < a.M ? m : a.M - 1) * a.ld_x) + lane % 8 * 16;
   }
 #pragma unroll
   for (int i = 0; i < kWCopies; ++i) {
-    constexpr uint32_t kPer = S::kRow / 16;
-    const uint32_t slot = (wid * kWCopies + i) * 64 + lane, r = slot / kPer;
-    const uint32_t c = slot % kPer ^ (kFourBit<FMT> ? (r >> 3) & 1u : (r >> 2) & 3u);
-    const int64_t n = n0 + r < a.N ? n0 + r : a.N - 1;
-    src[kXCopies + i] = a.codes + n * row_bytes + c * 16;
+    const int64_t n = n0 + (wid * kWCopies + i) + lane / 4 * (BN / 16);
+    wsrc[i] = a.codes + (n < a.N ? n : a.N - 1) * row_bytes + lane % 4 * 16;
   }
-  // stage `step` into its place in the ring; past the last one the last again,
-  // into a place that is not read
-  auto copy_stage = [&](uint32_t step) {
-    uint8_t* to = smem + (step % S::kCount) * S::kBytes;
-    const uint32_t from = step < steps ? step : steps - 1;
-#pragma unroll
-    for (int i = 0; i < kXCopies; ++i)
-      __builtin_amdgcn_global_load_lds((global_ptr)(src[i] + from * 128u), (lds_ptr)(to + (wid * kXCopies + i) * 1024),
-                                       16, 0, 0);
-#pragma unroll
-    for (int i = 0; i < kWCopies; ++i)
-      __builtin_amdgcn_global_load_lds((global_ptr)(src[kXCopies + i] + from * (uint32_t)S::kRow),
-                                       (lds_ptr)(to + S::kXBytes + (wid * kWCopies + i) * 1024), 16, 0, 0);
+  // one copy of a step's X, or of a unit's codes, into their places in the ring;
+  // past the last the last one again, which is then not used
+  auto copy_x = [&](uint32_t step, auto num) {
+    constexpr int i = decltype(num)::value;
+    const uint32_t from = step < 2 * pairs ? step : 2 * pairs - 1;
+    __builtin_amdgcn_global_load_lds((global_ptr)(xsrc[i] + from * 128u),
+                                     (lds_ptr)(smem + step % R::kCount * R::kXBytes + (wid * 4 + i) * kCopyPitch), 16, 0, 0);
   };
+  auto copy_w = [&](uint32_t unit, auto num) {
+    constexpr int i = decltype(num)::value;
+    const uint32_t from = unit < units ? unit : units - 1;
+    __builtin_amdgcn_global_load_lds(
+        (global_ptr)(wsrc[i] + from * 64u),
+        (lds_ptr)(wring + unit % R::kCount * R::kWBytes + (wid * kWCopies + i) * kCopyPitch), 16, 0, 0);
+  };
+  constexpr std::integral_constant<int, 0> s0;
+  constexpr std::integral_constant<int, 1> s1;
+  constexpr std::integral_constant<int, 2> s2;
+  constexpr std::integral_constant<int, 3> s3;
 
-  // scale bytes of this lane's weight rows: a word holds 4 blocks of 32 (two
-  // stages), or NVFP4's 4 blocks of 16 (one)
-  constexpr uint32_t kPerWord = FMT == FMT_NVFP4 ? 1 : 2;
-  const uint8_t* srow[TN];
+  // scale bytes of this lane's weight rows for a pair of steps: four blocks of
+  // 32, or NVFP4's eight of 16
+  using ScaleWord = std::conditional_t<FMT == FMT_NVFP4, uint64_t, uint32_t>;
+  const ScaleWord* srow[TN];
 #pragma unroll
   for (int j = 0; j < TN; ++j) {
-    int64_t n = n0 + wn + 32 * j + l;
-    n = n < a.N ? n : a.N - 1;
-    srow[j] = a.scales + n * (a.K / (FMT == FMT_NVFP4 ? 16 : 32));
+    const int64_t n = n0 + wn + 32 * j + l;
+    srow[j] = reinterpret_cast<const ScaleWord*>(a.scales) + (n < a.N ? n : a.N - 1) * (int64_t)pairs;
   }
-  uint32_t sc[TN], next[TN];
-#pragma unroll
-  for (int j = 0; j < TN; ++j) next[j] = *reinterpret_cast<const uint32_t*>(srow[j]);
 
   v16f acc[TM][TN];
 #pragma unroll
@@ -304,60 +325,124 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_linear_tile(Linea
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
-  copy_stage(0);
-  copy_stage(1);
-  for (uint32_t st = 0; st < steps; ++st) {
-    wait_loads<kCopies>();  // all but the next stage's copies
-    stage_barrier();
-    if (st % kPerWord == 0) {
-      const uint32_t w = st / kPerWord + 1 < steps / kPerWord ? st / kPerWord + 1 : st / kPerWord;
+  // What follows is one slice (16 elements of K, 8 a lane half) ahead of the
+  // products: its X fragments and decoded weights are in registers when its
+  // instructions start, also across the barrier.
+  uint32_t cw[TN][8], sc[TN];
+  ScaleWord scales[TN];  // of a pair of steps
+  bf16x8 xf[2][TM], wf[2][TN];
+  auto read_codes = [&](uint32_t st) {
+    const uint8_t* ws = wring + (kTwoSteps ? st / 2 : st) % R::kCount * R::kWBytes;
 #pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        sc[j] = next[j];
-        next[j] = *reinterpret_cast<const uint32_t*>(srow[j] + w * 4);
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int b = 0; b < (kTwoSteps ? 1 : 2); ++b) {
+        const word4 c =
+            *reinterpret_cast<const word4*>(ws + R::w(wn + 32 * j + l, kTwoSteps ? st % 2 * 2 + h : 2 * h + b));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) cw[j][4 * b + q] = c[q];
       }
-    }
-    copy_stage(st + 2);
-    const uint8_t* xs = smem + (st % S::kCount) * S::kBytes;
-    const uint8_t* ws = xs + S::kXBytes;
-    uint32_t cw[TN][8], s[TN];
+  };
+  auto read_x = [&](uint32_t st, auto num) {
+    constexpr int J = decltype(num)::value;
+    const uint8_t* xs = smem + st % R::kCount * R::kXBytes;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+      xf[J % 2][i] =
+          __builtin_bit_cast(bf16x8, *reinterpret_cast<const word4*>(xs + R::x(wm + 32 * i + l, 4 * h + J)));
+  };
+  auto decode = [&](auto num) {
+    constexpr int J = decltype(num)::value;
+#pragma unroll
+    for (int j = 0; j < TN; ++j) wf[J % 2][j] = decode_eighth<FMT, J>(cw[j], sc[j]);
+  };
+  auto products = [&](auto num) {
+    constexpr int J = decltype(num)::value;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wf[J % 2][j], xf[J % 2][i], acc[i][j], 0, 0, 0);
+  };
+  auto step_scales = [&](auto num) {
+    constexpr int P = decltype(num)::value;
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      const uint32_t r = wn + 32 * j + l;
-      if constexpr (kFourBit<FMT>) {
-        const word4 c = *reinterpret_cast<const word4*>(ws + w_slot<FMT>(r, h) * 16);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) cw[j][q] = c[q];
-      } else {
-        const word4 c = *reinterpret_cast<const word4*>(ws + w_slot<FMT>(r, 2 * h) * 16);
-        const word4 d = *reinterpret_cast<const word4*>(ws + w_slot<FMT>(r, 2 * h + 1) * 16);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          cw[j][q] = c[q];
-          cw[j][4 + q] = d[q];
-        }
-      }
-      if constexpr (FMT == FMT_NVFP4) s[j] = h ? sc[j] >> 16 : sc[j];
-      else s[j] = (sc[j] >> ((st % 2) * 16 + h * 8)) & 0xFFu;
+      if constexpr (FMT == FMT_NVFP4) sc[j] = (uint32_t)(scales[j] >> (32 * P)) >> (16 * h);
+      else sc[j] = (scales[j] >> (16 * P + 8 * h)) & 0xFFu;
     }
-    auto eighth = [&](auto num) {
-      constexpr int J = decltype(num)::value;
-      bf16x8 xf[TM], wf[TN];
+  };
+  auto load_scales = [&](uint32_t pair) {
 #pragma unroll
-      for (int i = 0; i < TM; ++i)
-        xf[i] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const word4*>(xs + x_slot(wm + 32 * i + l, 4 * h + J) * 16));
-#pragma unroll
-      for (int j = 0; j < TN; ++j) wf[j] = decode_eighth<FMT, J>(cw[j], s[j]);
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wf[j], xf[i], acc[i][j], 0, 0, 0);
-    };
-    eighth(std::integral_constant<int, 0>());
-    eighth(std::integral_constant<int, 1>());
-    eighth(std::integral_constant<int, 2>());
-    eighth(std::integral_constant<int, 3>());
+    for (int j = 0; j < TN; ++j) scales[j] = srow[j][pair < pairs ? pair : pairs - 1];
+  };
+
+  load_scales(0);
+  auto copy_step = [&](uint32_t st) {
+    copy_w(st, s0);
+    copy_w(st, s1);
+    copy_x(st, s0);
+    copy_x(st, s1);
+    copy_x(st, s2);
+    copy_x(st, s3);
+  };
+  copy_step(0);
+  copy_step(1);
+  wait_loads<4 + kWCopies>();
+  stage_barrier();
+  copy_x(2, s0);
+  step_scales(s0);
+  read_codes(0);
+  read_x(0, s0);
+  decode(s0);
+  // vector instructions of a slice's decoding, about
+  constexpr int kDecode = TN * (FMT == FMT_NVFP4 ? 17 : FMT == FMT_MXINT8 ? 20 : 4) + 2;
+  constexpr int kReads = TN * (kTwoSteps ? 1 : 2);
+  auto step = [&](uint32_t st, auto parity) {
+    constexpr int P = decltype(parity)::value;
+    constexpr bool kCodes = !kTwoSteps || P == 0;  // a unit of codes is copied
+    const uint32_t unit = (kTwoSteps ? st / 2 : st) + 2;
+    region();
+    read_x(st, s1);
+    copy_x(st + 2, s1);
+    if constexpr (kCodes) copy_w(unit, s0);
+    products(s0);
+    decode(s1);
+    spread<TM * TN, TM, 1 + kCodes, kDecode>();
+    region();
+    read_x(st, s2);
+    copy_x(st + 2, s2);
+    if constexpr (kCodes) copy_w(unit, s1);
+    products(s1);
+    decode(s2);
+    spread<TM * TN, TM, 1 + kCodes, kDecode>();
+    region();
+    read_x(st, s3);
+    copy_x(st + 2, s3);
+    products(s2);
+    decode(s3);
+    spread<TM * TN, TM, 1, kDecode>();
+    region();
+    // this step has been read (its last slice is in registers); the next one has
+    // landed: what was issued behind its last copy is not waited for
+    wait_loads<4 + (kCodes ? kWCopies : 0)>();
+    stage_barrier();
+    region();
+    step_scales(std::integral_constant<int, 1 - P>());
+    region();
+    if constexpr (P == 0) load_scales(st / 2 + 1);  // (wanted a step from now)
+    region();
+    copy_x(st + 3, s0);
+    read_codes(st + 1);
+    read_x(st + 1, s0);
+    products(s3);
+    decode(s0);
+    spread<TM * TN, TM + kReads, 1, kDecode + 10>();
+    region();
+  };
+  for (uint32_t pair = 0; pair < pairs; ++pair) {
+    step(2 * pair, s0);
+    step(2 * pair + 1, s1);
   }
   wait_loads<0>();  // the repeated copies too: LDS is used again
   stage_barrier();
@@ -365,7 +450,7 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_linear_tile(Linea
   // 32 tokens at a time through the wave's own part of LDS, so that a lane gets 8
   // neighbouring columns of a row
   constexpr int kCols = 32 * TN, kPitch = kCols + 4, kPer = kCols / 8, kRows = 64 / kPer;
-  static_assert(NW * 32 * kPitch * 4 <= S::kCount * S::kBytes, "epilogue in the stages' LDS");
+  static_assert(NW * 32 * kPitch * 4 <= R::kBytes, "epilogue in the ring's LDS");
   float* mine = reinterpret_cast<float*>(smem) + wid * (32 * kPitch);
   const float ts = FMT == FMT_NVFP4 ? *a.tensor_scale : 1.0f;
 #pragma unroll
@@ -400,8 +485,7 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_linear_tile(Linea
 
 template <int FMT, int BM, int BN, int WAVES_M, int WAVES_N>
 hipError_t launch_tile(const LinearArgs& a, hipStream_t s) {
-  using S = Stage<FMT, BM, BN>;
-  constexpr int kLds = S::kCount * S::kBytes;
+  constexpr int kLds = Ring<BM, BN>::kBytes;
   static_assert(kLds <= 160 * 1024, "LDS of a workgroup");
   auto kernel = k_linear_tile<FMT, BM, BN, WAVES_M, WAVES_N>;
   static std::atomic<uint64_t> done{0};
@@ -416,7 +500,7 @@ template <int FMT>
 hipError_t launch_fmt(const LinearArgs& a, hipStream_t s) {
   if (a.M <= 16) return launch_direct<FMT, 1, 1, 8>(a, s);
   if (a.M <= 32) return launch_direct<FMT, 2, 2, 8>(a, s);
-  // (stages are whole at multiples of 64, scale words at multiples of 128)
+  // (pairs of steps, and their words of scales, are whole at multiples of 128)
   if (a.M > 64 && a.K % 128 == 0 && a.K > 0) {
     const int64_t large = ((a.M + 255) / 256) * ((a.N + 255) / 256);
     return large >= 256 ? launch_tile<FMT, 256, 256, 2, 4>(a, s) : launch_tile<FMT, 128, 128, 2, 2>(a, s);
