@@ -5,6 +5,7 @@
 #include "../launch_dense.h"
 #include "codec.h"
 #include "rows.h"
+#include "wave.h"
 
 namespace mxk {
 
@@ -14,6 +15,34 @@ inline bool rows_aligned16(const void* p, int64_t ld, int dt) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * (dt == DT_F32 ? 4 : 2)) % 16 == 0;
 }
 
+// a chunk as it lies in memory (BF16: a alone)
+typedef uint32_t raw16 __attribute__((ext_vector_type(4)));
+struct RawChunk {
+  raw16 a, b;
+};
+template <int DT>
+__device__ inline RawChunk load_raw8(const void* p, int64_t off, int n, bool vec) {
+  RawChunk r = {};
+  if (n >= 8 && vec) {
+    const raw16* q = reinterpret_cast<const raw16*>(static_cast<const char*>(p) + off * (DT == DT_BF16 ? 2 : 4));
+    r.a = q[0];
+    if constexpr (DT == DT_F32) r.b = q[1];
+    return r;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) {
+      if constexpr (DT == DT_BF16) r.a[i / 2] |= (uint32_t)static_cast<const uint16_t*>(p)[off + i] << (16 * (i & 1));
+      else (i < 4 ? r.a : r.b)[i & 3] = static_cast<const uint32_t*>(p)[off + i];
+    }
+  return r;
+}
+template <int DT>
+__device__ inline float raw_value(const RawChunk& r, int i) {
+  if constexpr (DT == DT_BF16) return u2f(i & 1 ? r.a[i / 2] & 0xFFFF0000u : r.a[i / 2] << 16);
+  else return u2f(i < 4 ? r.a[i & 3] : r.b[i & 3]);
+}
+
 // (the columns past n read as 0)
 template <int DT>
 __device__ inline void load_chunk(const void* p, int64_t off, int n, bool vec, float (&v)[8]) {
@@ -21,9 +50,20 @@ __device__ inline void load_chunk(const void* p, int64_t off, int n, bool vec, f
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = i < n ? load1<DT>(p, off + i) : 0.0f;
 }
-template <int DT>
+// Streaming: a matrix that nothing here reads back at once, larger than the L2s.
+template <int DT, bool STREAM = false>
 __device__ inline void store_chunk(void* p, int64_t off, int n, bool vec, const float (&v)[8]) {
-  if (n >= 8 && vec) return store8<DT>(p, off, v);
+  if (n >= 8 && vec) {
+    if constexpr (!STREAM) return store8<DT>(p, off, v);
+    if constexpr (DT == DT_BF16) {
+      store_nt(static_cast<uint16_t*>(p) + off, pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+               pack_bf16(v[6], v[7]));
+    } else {
+      store_nt(static_cast<float*>(p) + off, f2u(v[0]), f2u(v[1]), f2u(v[2]), f2u(v[3]));
+      store_nt(static_cast<float*>(p) + off + 4, f2u(v[4]), f2u(v[5]), f2u(v[6]), f2u(v[7]));
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (i < n) store1<DT>(p, off + i, v[i]);

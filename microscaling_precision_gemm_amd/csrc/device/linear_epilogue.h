@@ -19,20 +19,24 @@ inline EpilogueVec epilogue_vec(const Epilogue& e) {
           rows_aligned16(e.residual, e.ld_r, e.dt), rows_aligned16(e.out, e.ld_o, e.dt)};
 }
 
-// v: the sums of columns col .. col + 7 (a multiple of 8), of which n exist
-template <int DT>
-__device__ inline void epilogue_chunk(const Epilogue& e, const EpilogueVec& vec, int64_t row, int64_t col, int64_t N,
-                                      int n, float (&v)[8]) {
-  float w[8];
-  if (e.residual) load_chunk<DT>(e.residual, row * e.ld_r + col, n, vec.residual, w);
-  if (e.bias) {
-    float b[8];
-    if (e.bias_dt == DT_BF16) load_chunk<DT_BF16>(e.bias, col, n, vec.bias, b);
-    else load_chunk<DT_F32>(e.bias, col, n, vec.bias, b);
+// bias of columns col .. col + 7 (a multiple of 8), of which n exist
+__device__ inline void load_bias(const Epilogue& e, const EpilogueVec& vec, int64_t col, int n, float (&b)[8]) {
+  if (!e.bias) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += b[i];
-  }
-  if (e.z) store_chunk<DT>(e.z, row * e.ld_z + col, n, vec.z, v);
+    for (int i = 0; i < 8; ++i) b[i] = 0.0f;
+  } else if (e.bias_dt == DT_BF16) load_chunk<DT_BF16>(e.bias, col, n, vec.bias, b);
+  else load_chunk<DT_F32>(e.bias, col, n, vec.bias, b);
+}
+
+// v: the sums of columns col .. col + 7, of which n exist; res: the residual
+// there, if there is one.  Results larger than the L2s go by streaming stores
+// (16384 x 14336 BF16 and z: 1628 -> 1588 us).
+template <int DT, bool STREAM>
+__device__ inline void epilogue_chunk(const Epilogue& e, const EpilogueVec& vec, int64_t row, int64_t col, int64_t N,
+                                      int n, const float (&b)[8], const RawChunk& res, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] += b[i];
+  if (e.z) store_chunk<DT, STREAM>(e.z, row * e.ld_z + col, n, vec.z, v);
   with_act(e.act, [&](auto kind) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = act<decltype(kind)::value>(v[i]);
@@ -40,9 +44,9 @@ __device__ inline void epilogue_chunk(const Epilogue& e, const EpilogueVec& vec,
   if (e.drop.threshold) drop_chunk(e.drop, (uint64_t)(row * ((N + 7) / 8) + col / 8), v);
   if (e.residual) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = w[i] + v[i];
+    for (int i = 0; i < 8; ++i) v[i] = raw_value<DT>(res, i) + v[i];
   }
-  store_chunk<DT>(e.out, row * e.ld_o + col, n, vec.out, v);
+  store_chunk<DT, STREAM>(e.out, row * e.ld_o + col, n, vec.out, v);
 }
 
 }  // namespace mxk

@@ -25,32 +25,45 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 // A workgroup of NW waves takes a tile of 16 TM tokens x 16 TN columns; its waves
 // share out the steps of K and add their sums through LDS, in order.  A step is
 // 128 bytes of a weight row (256 4-bit or 128 8-bit elements): lane group g of
-// four takes 32 bytes of them.
-template <int FMT, int TM, int TN, int NW>
+// four takes 32 bytes of them.  Each wave has neighbouring steps, and tiles start
+// at different ones: rows of a power of two of bytes would otherwise all be read
+// at the same offset at a time, from a part of the memory channels.  The next
+// step's operands are loaded while this one's are multiplied.
+template <int FMT, int TM, int TN>
+struct DirectStep {
+  static constexpr int B = kFourBit<FMT> ? 2 : 1;  // blocks of 32 a lane
+  word4 codes[TN][2];
+  uint32_t scales[TN][B];
+  word4 x[TM][B][4];
+};
+
+template <int FMT, int DT, int TM, int TN, int NW>
 __global__ __launch_bounds__(NW * 64) void k_linear_direct(LinearArgs a, EpilogueVec vec, uint32_t tiles_m) {
-  constexpr int B = kFourBit<FMT> ? 2 : 1;  // blocks of 32 a lane and step
-  constexpr int kPitch = TN * 16 + 4;       // floats of a token's row in LDS
+  using Step = DirectStep<FMT, TM, TN>;
+  constexpr int B = Step::B;
+  constexpr int kPitch = TN * 16 + 4;  // floats of a token's row in LDS
   extern __shared__ __attribute__((aligned(16))) float red[];
-  const uint32_t lane = threadIdx.x & 63u, wid = threadIdx.x >> 6, l = lane & 15u, g = lane >> 4;
-  const int64_t m0 = (int64_t)(blockIdx.x % tiles_m) * (16 * TM), n0 = (int64_t)(blockIdx.x / tiles_m) * (16 * TN);
+  const uint32_t lane = threadIdx.x & 63u, l = lane & 15u, g = lane >> 4;
+  const uint32_t wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t tile = blockIdx.x / tiles_m;
+  const int64_t m0 = (int64_t)(blockIdx.x % tiles_m) * (16 * TM), n0 = (int64_t)tile * (16 * TN);
   const int64_t row_bytes = a.K / 32 * kBlockBytes<FMT>, blocks = a.K / 32;
 
+  // rows past the last are the last one (their results are not stored)
   const uint8_t* w[TN];
   int64_t first[TN];  // block number of the row's first block
 #pragma unroll
   for (int j = 0; j < TN; ++j) {
     int64_t n = n0 + 16 * j + l;
-    n = n < a.N ? n : a.N - 1;  // (columns past N are not stored)
+    n = n < a.N ? n : a.N - 1;
     w[j] = a.codes + n * row_bytes;
     first[j] = n * blocks;
   }
   const uint16_t* x[TM];
-  bool there[TM];
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     const int64_t m = m0 + 16 * i + l;
-    there[i] = m < a.M;
-    x[i] = a.x + (there[i] ? m : 0) * a.ld_x;
+    x[i] = a.x + (m < a.M ? m : a.M - 1) * a.ld_x;
   }
 
   v4f acc[TM][TN];
@@ -59,58 +72,94 @@ __global__ __launch_bounds__(NW * 64) void k_linear_direct(LinearArgs a, Epilogu
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0, 0, 0, 0};
 
-  const int64_t steps = (blocks + 4 * B - 1) / (4 * B);
-  for (int64_t st = wid; st < steps; st += NW) {
+  // the lane's blocks start at `blk`
+  auto load = [&](Step& s, int64_t blk) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const word4* p = reinterpret_cast<const word4*>(w[j] + blk * kBlockBytes<FMT>);
+      s.codes[j][0] = p[0];
+      s.codes[j][1] = p[1];
+#pragma unroll
+      for (int b = 0; b < B; ++b) s.scales[j][b] = load_scale<FMT>(a.scales, first[j] + blk + b);
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s.x[i][b][e] = *reinterpret_cast<const word4*>(x[i] + (blk + b) * 32 + e * 8);
+  };
+  auto eighth = [&](const Step& s, auto block, auto num) {
+    constexpr int b = decltype(block)::value, J = decltype(num)::value;
+    bf16x8 wb[TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      uint32_t u[8];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        u[q] = s.codes[j][kFourBit<FMT> ? b : 0][q];
+        u[4 + q] = s.codes[j][1][q];
+      }
+      wb[j] = decode_eighth<FMT, J>(u, s.scales[j][b]);
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j], __builtin_bit_cast(bf16x8, s.x[i][b][J]), acc[i][j],
+                                                            0, 0, 0);
+  };
+  auto multiply = [&](const Step& s) {
+    auto block = [&](auto b) {
+      eighth(s, b, std::integral_constant<int, 0>());
+      eighth(s, b, std::integral_constant<int, 1>());
+      eighth(s, b, std::integral_constant<int, 2>());
+      eighth(s, b, std::integral_constant<int, 3>());
+    };
+    block(std::integral_constant<int, 0>());
+    if constexpr (B == 2) block(std::integral_constant<int, 1>());
+  };
+
+  const uint32_t steps = (uint32_t)(blocks / (4 * B));  // whole ones
+  const uint32_t per = (steps + NW - 1) / NW, lo = wid * per < steps ? wid * per : steps;
+  const uint32_t count = steps - lo < per ? steps - lo : per;
+  if (count > 0) {
+    const uint32_t turn = tile % count;
+    auto at = [&](uint32_t i) {  // the lane's blocks of the i-th step taken
+      const uint32_t st = turn + i < count ? turn + i : turn + i - count;
+      return (int64_t)(lo + st) * (4 * B) + g * B;
+    };
+    Step p, q;
+    load(p, at(0));
+    for (uint32_t i = 0; i < count; i += 2) {
+      load(q, at(i + 1 < count ? i + 1 : i));
+      multiply(p);
+      if (i + 1 == count) break;
+      load(p, at(i + 2 < count ? i + 2 : i));
+      multiply(q);
+    }
+  }
+  // what is left of K, fewer blocks than a step has: lanes past it take zeros
+  if (wid == NW - 1 && steps * (4 * B) < blocks) {
+    Step s = {};
 #pragma unroll
     for (int b = 0; b < B; ++b) {
-      const int64_t blk = st * 4 * B + g * B + b;
-      const bool in = blk < blocks;
-      word4 cw[TN][2];
-      uint32_t sc[TN];
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        sc[j] = 0;
-        cw[j][0] = cw[j][1] = word4{0, 0, 0, 0};
-        if (in) {
-          const word4* p = reinterpret_cast<const word4*>(w[j] + blk * kBlockBytes<FMT>);
-          cw[j][0] = p[0];
-          if constexpr (!kFourBit<FMT>) cw[j][1] = p[1];
-          sc[j] = load_scale<FMT>(a.scales, first[j] + blk);
-        }
-      }
-      word4 xv[TM][4];
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          xv[i][e] = word4{0, 0, 0, 0};
-          if (in && there[i]) xv[i][e] = *reinterpret_cast<const word4*>(x[i] + blk * 32 + e * 8);
-        }
-      auto eighth = [&](auto num) {
-        constexpr int J = decltype(num)::value;
-        bf16x8 wb[TN];
+      const int64_t blk = (int64_t)steps * (4 * B) + g * B + b;
+      if (blk < blocks) {
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
-          uint32_t u[8];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            u[q] = cw[j][0][q];
-            u[4 + q] = cw[j][1][q];
-          }
-          wb[j] = decode_eighth<FMT, J>(u, sc[j]);
+          const word4* p = reinterpret_cast<const word4*>(w[j] + blk * kBlockBytes<FMT>);
+          s.codes[j][b] = p[0];
+          if constexpr (!kFourBit<FMT>) s.codes[j][1] = p[1];
+          s.scales[j][b] = load_scale<FMT>(a.scales, first[j] + blk);
         }
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
-          for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j], __builtin_bit_cast(bf16x8, xv[i][J]),
-                                                                acc[i][j], 0, 0, 0);
-      };
-      eighth(std::integral_constant<int, 0>());
-      eighth(std::integral_constant<int, 1>());
-      eighth(std::integral_constant<int, 2>());
-      eighth(std::integral_constant<int, 3>());
+          for (int e = 0; e < 4; ++e) s.x[i][b][e] = *reinterpret_cast<const word4*>(x[i] + blk * 32 + e * 8);
+      }
     }
+    multiply(s);
   }
 
   float* mine = red + (size_t)wid * (16 * TM * kPitch);
@@ -142,8 +191,11 @@ __global__ __launch_bounds__(NW * 64) void k_linear_direct(LinearArgs a, Epilogu
       for (int i = 0; i < 8; ++i) v[i] *= ts;
     }
     const int n = (int)(a.N - col < 8 ? a.N - col : 8);
-    if (a.ep.dt == DT_BF16) epilogue_chunk<DT_BF16>(a.ep, vec, row, col, a.N, n, v);
-    else epilogue_chunk<DT_F32>(a.ep, vec, row, col, a.N, n, v);
+    float b[8];
+    load_bias(a.ep, vec, col, n, b);
+    RawChunk res = {};
+    if (a.ep.residual) res = load_raw8<DT>(a.ep.residual, row * a.ep.ld_r + col, n, vec.residual);
+    epilogue_chunk<DT, false>(a.ep, vec, row, col, a.N, n, b, res, v);
   }
 }
 
@@ -162,11 +214,11 @@ hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done)
   return hipSuccess;
 }
 
-template <int FMT, int TM, int TN, int NW>
+template <int FMT, int DT, int TM, int TN, int NW>
 hipError_t launch_direct(const LinearArgs& a, hipStream_t s) {
   constexpr int kLds = NW * 16 * TM * (TN * 16 + 4) * 4;
   static_assert(kLds <= 160 * 1024, "LDS of a workgroup");
-  auto kernel = k_linear_direct<FMT, TM, TN, NW>;
+  auto kernel = k_linear_direct<FMT, DT, TM, TN, NW>;
   static std::atomic<uint64_t> done{0};
   const hipError_t e = allow_lds((const void*)kernel, kLds, done);
   if (e != hipSuccess) return e;
@@ -252,7 +304,7 @@ __device__ inline void spread() {
   }
 }
 
-template <int FMT, int BM, int BN, int WAVES_M, int WAVES_N>
+template <int FMT, int DT, int BM, int BN, int WAVES_M, int WAVES_N>
 __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_linear_tile(LinearArgs a, EpilogueVec vec,
                                                                           uint32_t tiles_m, uint32_t tiles_n) {
   using R = Ring<BM, BN>;
@@ -448,13 +500,27 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_linear_tile(Linea
   stage_barrier();
 
   // 32 tokens at a time through the wave's own part of LDS, so that a lane gets 8
-  // neighbouring columns of a row
-  constexpr int kCols = 32 * TN, kPitch = kCols + 4, kPer = kCols / 8, kRows = 64 / kPer;
+  // neighbouring columns of a row; a pass takes kRows of them.  The residual
+  // comes a pass ahead.  The passes are kept rolled: unrolled, they do not fit the
+  // instruction cache beside the loop above (3 times slower as a whole).
+  constexpr int kCols = 32 * TN, kPitch = kCols + 4, kPer = kCols / 8, kRows = 64 / kPer, kPasses = 32 / kRows;
   static_assert(NW * 32 * kPitch * 4 <= R::kBytes, "epilogue in the ring's LDS");
   float* mine = reinterpret_cast<float*>(smem) + wid * (32 * kPitch);
   const float ts = FMT == FMT_NVFP4 ? *a.tensor_scale : 1.0f;
+  const uint32_t t0 = lane / kPer, c = lane % kPer * 8;
+  const int64_t row0 = m0 + wm + t0, col = n0 + wn + c;
+  const int n = (int)(col >= a.N ? 0 : a.N - col < 8 ? a.N - col : 8);
+  float b[8];
+  load_bias(a.ep, vec, col, n, b);
+  auto residual_of = [&](int pass) {
+    const int64_t row = row0 + pass * kRows;
+    return a.ep.residual && row < a.M ? load_raw8<DT>(a.ep.residual, row * a.ep.ld_r + col, n, vec.residual)
+                                      : RawChunk{};
+  };
+  RawChunk ahead = residual_of(0);
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int j = 0; j < TN; ++j)
 #pragma unroll
@@ -463,31 +529,29 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_linear_tile(Linea
             v4f{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
     __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
-    for (int p = 0; p < 32 / kRows; ++p) {
-      const uint32_t t = p * kRows + lane / kPer, c = lane % kPer * 8;
-      const int64_t row = m0 + wm + 32 * i + t, col = n0 + wn + c;
-      if (row >= a.M || col >= a.N) continue;
-      const v4f lo = *reinterpret_cast<const v4f*>(mine + t * kPitch + c);
-      const v4f hi = *reinterpret_cast<const v4f*>(mine + t * kPitch + c + 4);
+    for (int pass = i * kPasses; pass < (i + 1) * kPasses; ++pass) {
+      const RawChunk res = ahead;
+      if (pass + 1 < TM * kPasses) ahead = residual_of(pass + 1);
+      const int64_t row = row0 + pass * kRows;
+      if (row >= a.M || n == 0) continue;
+      const float* p = mine + (pass % kPasses * kRows + t0) * kPitch + c;
+      const v4f lo = *reinterpret_cast<const v4f*>(p), hi = *reinterpret_cast<const v4f*>(p + 4);
       float v[8];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        v[e] = lo[e] * ts;
-        v[4 + e] = hi[e] * ts;
+        v[e] = FMT == FMT_NVFP4 ? lo[e] * ts : lo[e];
+        v[4 + e] = FMT == FMT_NVFP4 ? hi[e] * ts : hi[e];
       }
-      const int n = (int)(a.N - col < 8 ? a.N - col : 8);
-      if (a.ep.dt == DT_BF16) epilogue_chunk<DT_BF16>(a.ep, vec, row, col, a.N, n, v);
-      else epilogue_chunk<DT_F32>(a.ep, vec, row, col, a.N, n, v);
+      epilogue_chunk<DT, true>(a.ep, vec, row, col, a.N, n, b, res, v);
     }
-    __builtin_amdgcn_wave_barrier();
   }
 }
 
-template <int FMT, int BM, int BN, int WAVES_M, int WAVES_N>
+template <int FMT, int DT, int BM, int BN, int WAVES_M, int WAVES_N>
 hipError_t launch_tile(const LinearArgs& a, hipStream_t s) {
   constexpr int kLds = Ring<BM, BN>::kBytes;
   static_assert(kLds <= 160 * 1024, "LDS of a workgroup");
-  auto kernel = k_linear_tile<FMT, BM, BN, WAVES_M, WAVES_N>;
+  auto kernel = k_linear_tile<FMT, DT, BM, BN, WAVES_M, WAVES_N>;
   static std::atomic<uint64_t> done{0};
   const hipError_t e = allow_lds((const void*)kernel, kLds, done);
   if (e != hipSuccess) return e;
@@ -496,16 +560,21 @@ hipError_t launch_tile(const LinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int FMT>
-hipError_t launch_fmt(const LinearArgs& a, hipStream_t s) {
-  if (a.M <= 16) return launch_direct<FMT, 1, 1, 8>(a, s);
-  if (a.M <= 32) return launch_direct<FMT, 2, 2, 8>(a, s);
+template <int FMT, int DT>
+hipError_t launch_as(const LinearArgs& a, hipStream_t s) {
+  if (a.M <= 16) return launch_direct<FMT, DT, 1, 1, 8>(a, s);
+  if (a.M <= 32) return launch_direct<FMT, DT, 2, 2, 8>(a, s);
   // (pairs of steps, and their words of scales, are whole at multiples of 128)
   if (a.M > 64 && a.K % 128 == 0 && a.K > 0) {
     const int64_t large = ((a.M + 255) / 256) * ((a.N + 255) / 256);
-    return large >= 256 ? launch_tile<FMT, 256, 256, 2, 4>(a, s) : launch_tile<FMT, 128, 128, 2, 2>(a, s);
+    return large >= 256 ? launch_tile<FMT, DT, 256, 256, 2, 4>(a, s) : launch_tile<FMT, DT, 128, 128, 2, 2>(a, s);
   }
-  return launch_direct<FMT, 4, 4, 4>(a, s);
+  return launch_direct<FMT, DT, 4, 4, 4>(a, s);
+}
+
+template <int FMT>
+hipError_t launch_fmt(const LinearArgs& a, hipStream_t s) {
+  return a.ep.dt == DT_BF16 ? launch_as<FMT, DT_BF16>(a, s) : launch_as<FMT, DT_F32>(a, s);
 }
 
 }  // namespace
