@@ -21,6 +21,41 @@ namespace {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
 
+// The sums of NW waves over one tile of BM tokens x BN columns, rows of BN + 4
+// floats in LDS, added in order; then the epilogue.
+template <int FMT, int DT, int BM, int BN, int NW>
+__device__ inline void join_waves(const LinearArgs& a, const EpilogueVec& vec, const float* red, int64_t m0,
+                                  int64_t n0) {
+  constexpr int kPitch = BN + 4;
+  const float ts = FMT == FMT_NVFP4 ? *a.tensor_scale : 1.0f;
+  for (uint32_t q = threadIdx.x; q < BM * BN / 8; q += NW * 64) {
+    const uint32_t t = q / (BN / 8), c = q % (BN / 8) * 8;
+    const int64_t row = m0 + t, col = n0 + c;
+    if (row >= a.M || col >= a.N) continue;
+    const int n = (int)(a.N - col < 8 ? a.N - col : 8);
+    RawChunk res = {};
+    if (a.ep.residual) res = load_raw8<DT>(a.ep.residual, row * a.ep.ld_r + col, n, vec.residual);
+    float b[8];
+    load_bias(a.ep, vec, col, n, b);
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+      const float* p = red + k * (BM * kPitch) + t * kPitch + c;
+      const v4f lo = *reinterpret_cast<const v4f*>(p), hi = *reinterpret_cast<const v4f*>(p + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] += lo[i];
+        v[4 + i] += hi[i];
+      }
+    }
+    if constexpr (FMT == FMT_NVFP4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= ts;
+    }
+    epilogue_chunk<DT, false>(a.ep, vec, row, col, a.N, n, b, res, v);
+  }
+}
+
 // ---- operands straight from memory -----------------------------------------
 // A workgroup of NW waves takes a tile of 16 TM tokens x 16 TN columns; its waves
 // share out the steps of K and add their sums through LDS, in order.  A step is
@@ -170,33 +205,7 @@ __global__ __launch_bounds__(NW * 64) void k_linear_direct(LinearArgs a, Epilogu
       *reinterpret_cast<v4f*>(mine + (16 * i + l) * kPitch + 16 * j + 4 * g) = acc[i][j];
   __syncthreads();
 
-  const float ts = FMT == FMT_NVFP4 ? *a.tensor_scale : 1.0f;
-  for (uint32_t q = threadIdx.x; q < 32u * TM * TN; q += NW * 64) {
-    const uint32_t t = q / (2 * TN), c = (q % (2 * TN)) * 8;
-    const int64_t row = m0 + t, col = n0 + c;
-    if (row >= a.M || col >= a.N) continue;
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-    for (int k = 0; k < NW; ++k) {
-      const float* p = red + (size_t)k * (16 * TM * kPitch) + t * kPitch + c;
-      const v4f lo = *reinterpret_cast<const v4f*>(p), hi = *reinterpret_cast<const v4f*>(p + 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] += lo[i];
-        v[4 + i] += hi[i];
-      }
-    }
-    if constexpr (FMT == FMT_NVFP4) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= ts;
-    }
-    const int n = (int)(a.N - col < 8 ? a.N - col : 8);
-    float b[8];
-    load_bias(a.ep, vec, col, n, b);
-    RawChunk res = {};
-    if (a.ep.residual) res = load_raw8<DT>(a.ep.residual, row * a.ep.ld_r + col, n, vec.residual);
-    epilogue_chunk<DT, false>(a.ep, vec, row, col, a.N, n, b, res, v);
-  }
+  join_waves<FMT, DT, 16 * TM, 16 * TN, NW>(a, vec, red, m0, n0);
 }
 
 // Raise a kernel's dynamic LDS limit once per device, so that later launches
@@ -304,6 +313,31 @@ __device__ inline void spread() {
   }
 }
 
+// What a copy takes past the end of a row.
+__device__ const word4 kZeros = {0, 0, 0, 0};
+
+// The scale bytes of a pair of steps: four blocks of 32, or NVFP4's eight of 16.
+// (A row of scales starts at any byte where K % 128 != 0.)
+template <int FMT>
+using ScaleWord = std::conditional_t<FMT == FMT_NVFP4, uint64_t, uint32_t>;
+template <int FMT>
+__device__ inline ScaleWord<FMT> load_pair_scales(const uint8_t* p) {
+  ScaleWord<FMT> w;
+  __builtin_memcpy(&w, p, sizeof(w));
+  return w;
+}
+// those of the last 1 .. 3 blocks of a row, and 1 behind them
+template <int FMT>
+__device__ inline ScaleWord<FMT> load_rest_scales(const uint8_t* p, uint32_t blocks) {
+  constexpr int kBytes = FMT == FMT_NVFP4 ? 2 : 1;
+  constexpr ScaleWord<FMT> kOne = FMT == FMT_NVFP4 ? 0x38 : 127;
+  ScaleWord<FMT> w = 0;
+#pragma unroll
+  for (uint32_t i = 0; i < sizeof(w); ++i)
+    w |= (i < blocks * kBytes ? (ScaleWord<FMT>)p[i] : kOne) << (8 * i);
+  return w;
+}
+
 template <int FMT, int DT, int BM, int BN, int WAVES_M, int WAVES_N>
 __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_linear_tile(LinearArgs a, EpilogueVec vec,
                                                                           uint32_t tiles_m, uint32_t tiles_n) {
@@ -324,6 +358,7 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_linear_tile(Linea
   const int64_t row_bytes = a.K / 32 * kBlockBytes<FMT>;
   const uint32_t pairs = (uint32_t)(a.K / 128);  // of steps
   const uint32_t units = kTwoSteps ? pairs : 2 * pairs;
+  const uint32_t rest = (uint32_t)(a.K / 32 % 4);  // blocks behind them
 
   // this lane's source of each of the wave's copies; rows past the last are the
   // last one (their results are not stored)
@@ -359,14 +394,11 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_linear_tile(Linea
   constexpr std::integral_constant<int, 2> s2;
   constexpr std::integral_constant<int, 3> s3;
 
-  // scale bytes of this lane's weight rows for a pair of steps: four blocks of
-  // 32, or NVFP4's eight of 16
-  using ScaleWord = std::conditional_t<FMT == FMT_NVFP4, uint64_t, uint32_t>;
-  const ScaleWord* srow[TN];
+  const uint8_t* srow[TN];  // scales of this lane's weight rows
 #pragma unroll
   for (int j = 0; j < TN; ++j) {
     const int64_t n = n0 + wn + 32 * j + l;
-    srow[j] = reinterpret_cast<const ScaleWord*>(a.scales) + (n < a.N ? n : a.N - 1) * (int64_t)pairs;
+    srow[j] = a.scales + (n < a.N ? n : a.N - 1) * (a.K / (FMT == FMT_NVFP4 ? 16 : 32));
   }
 
   v16f acc[TM][TN];
@@ -381,7 +413,7 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_linear_tile(Linea
   // products: its X fragments and decoded weights are in registers when its
   // instructions start, also across the barrier.
   uint32_t cw[TN][8], sc[TN];
-  ScaleWord scales[TN];  // of a pair of steps
+  ScaleWord<FMT> scales[TN];  // of a pair of steps
   bf16x8 xf[2][TM], wf[2][TN];
   auto read_codes = [&](uint32_t st) {
     const uint8_t* ws = wring + (kTwoSteps ? st / 2 : st) % R::kCount * R::kWBytes;
@@ -426,27 +458,10 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_linear_tile(Linea
   };
   auto load_scales = [&](uint32_t pair) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j) scales[j] = srow[j][pair < pairs ? pair : pairs - 1];
+    for (int j = 0; j < TN; ++j)
+      scales[j] = load_pair_scales<FMT>(srow[j] + (pair < pairs ? pair : pairs - 1) * sizeof(ScaleWord<FMT>));
   };
 
-  load_scales(0);
-  auto copy_step = [&](uint32_t st) {
-    copy_w(st, s0);
-    copy_w(st, s1);
-    copy_x(st, s0);
-    copy_x(st, s1);
-    copy_x(st, s2);
-    copy_x(st, s3);
-  };
-  copy_step(0);
-  copy_step(1);
-  wait_loads<4 + kWCopies>();
-  stage_barrier();
-  copy_x(2, s0);
-  step_scales(s0);
-  read_codes(0);
-  read_x(0, s0);
-  decode(s0);
   // vector instructions of a slice's decoding, about
   constexpr int kDecode = TN * (FMT == FMT_NVFP4 ? 17 : FMT == FMT_MXINT8 ? 20 : 4) + 2;
   constexpr int kReads = TN * (kTwoSteps ? 1 : 2);
@@ -492,12 +507,80 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_linear_tile(Linea
     spread<TM * TN, TM + kReads, 1, kDecode + 10>();
     region();
   };
-  for (uint32_t pair = 0; pair < pairs; ++pair) {
-    step(2 * pair, s0);
-    step(2 * pair + 1, s1);
+  if (pairs > 0) {
+    load_scales(0);
+    auto copy_step = [&](uint32_t st) {
+      copy_w(st, s0);
+      copy_w(st, s1);
+      copy_x(st, s0);
+      copy_x(st, s1);
+      copy_x(st, s2);
+      copy_x(st, s3);
+    };
+    copy_step(0);
+    copy_step(1);
+    wait_loads<4 + kWCopies>();
+    stage_barrier();
+    copy_x(2, s0);
+    step_scales(s0);
+    read_codes(0);
+    read_x(0, s0);
+    decode(s0);
+    for (uint32_t pair = 0; pair < pairs; ++pair) {
+      step(2 * pair, s0);
+      step(2 * pair + 1, s1);
+    }
+    wait_loads<0>();  // the repeated copies too: LDS is used again
+    stage_barrier();
   }
-  wait_loads<0>();  // the repeated copies too: LDS is used again
-  stage_barrier();
+  if (rest) {  // what is left of K, as a pair that ends in zeros; nothing runs ahead
+    auto copy_rest_x = [&](uint32_t st, auto num) {
+      constexpr int i = decltype(num)::value;
+      const bool in = st * 64 + lane % 8 * 8 < rest * 32;
+      const uint8_t* from = in ? xsrc[i] + (2 * pairs + st) * 128u : reinterpret_cast<const uint8_t*>(&kZeros);
+      __builtin_amdgcn_global_load_lds((global_ptr)from,
+                                       (lds_ptr)(smem + st * R::kXBytes + (wid * 4 + i) * kCopyPitch), 16, 0, 0);
+    };
+    auto copy_rest_w = [&](uint32_t unit, auto num) {
+      constexpr int i = decltype(num)::value;
+      const bool in = unit * 64 + lane % 4 * 16 < rest * kBlockBytes<FMT>;
+      const uint8_t* from = in ? wsrc[i] + (units + unit) * 64u : reinterpret_cast<const uint8_t*>(&kZeros);
+      __builtin_amdgcn_global_load_lds((global_ptr)from,
+                                       (lds_ptr)(wring + unit * R::kWBytes + (wid * kWCopies + i) * kCopyPitch), 16, 0, 0);
+    };
+    auto copy_rest = [&](uint32_t st) {
+      copy_rest_x(st, s0);
+      copy_rest_x(st, s1);
+      copy_rest_x(st, s2);
+      copy_rest_x(st, s3);
+      if (kTwoSteps && st == 1) return;
+      copy_rest_w(st, s0);
+      copy_rest_w(st, s1);
+    };
+    copy_rest(0);
+    copy_rest(1);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) scales[j] = load_rest_scales<FMT>(srow[j] + pairs * sizeof(ScaleWord<FMT>), rest);
+    wait_loads<0>();
+    stage_barrier();
+    auto rest_step = [&](auto parity) {
+      constexpr uint32_t P = decltype(parity)::value;
+      step_scales(parity);
+      read_codes(P);
+      auto slice = [&](auto num) {
+        read_x(P, num);
+        decode(num);
+        products(num);
+      };
+      slice(s0);
+      slice(s1);
+      slice(s2);
+      slice(s3);
+    };
+    rest_step(s0);
+    if (rest > 2) rest_step(s1);
+    stage_barrier();
+  }
 
   // 32 tokens at a time through the wave's own part of LDS, so that a lane gets 8
   // neighbouring columns of a row; a pass takes kRows of them.  The residual
@@ -560,16 +643,269 @@ hipError_t launch_tile(const LinearArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// ---- K shared out among the waves of a tile ---------------------------------
+// Between the two: batches whose large tiles would leave most of the card idle.
+// Each wave of a workgroup takes the whole BM x BN tile over its own part of K
+// (neighbouring pairs of steps), from a ring of LDS that is its own: no barriers,
+// three steps of copies in flight for each of NW waves.  The waves' sums are added
+// through LDS in order.  What bounds it is the L1: 12 KB of operands for 64 x 64 x
+// 64 products are 188 cycles at 64 bytes a cycle against 512 cycles of a wave's
+// matrix instructions, of which four share it.
+template <int FMT, int BM, int BN>
+struct SplitRing {
+  static constexpr bool kTwoSteps = kFourBit<FMT>;
+  static constexpr uint32_t kXBytes = BM / 8 * kCopyPitch, kWBytes = BN / 16 * kCopyPitch;
+  static constexpr uint32_t kXSlots = 3, kWSlots = kTwoSteps ? 2 : 3;
+  static constexpr uint32_t kBytes = kXSlots * kXBytes + kWSlots * kWBytes;
+};
+
+template <int FMT, int DT, int BM, int BN, int NW>
+__global__ __launch_bounds__(NW * 64) void k_linear_split(LinearArgs a, EpilogueVec vec, uint32_t tiles_m,
+                                                          uint32_t tiles_n) {
+  using R = Ring<BM, BN>;
+  using S = SplitRing<FMT, BM, BN>;
+  constexpr int TM = BM / 32, TN = BN / 32, kXCopies = BM / 8, kWCopies = BN / 16;
+  constexpr bool kTwoSteps = S::kTwoSteps;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  uint32_t ti, tj;
+  tile_at(blockIdx.x, tiles_m, tiles_n, &ti, &tj);
+  const int64_t m0 = (int64_t)ti * BM, n0 = (int64_t)tj * BN;
+  const uint32_t lane = threadIdx.x & 63u, l = lane & 31u, h = lane >> 5;
+  const uint32_t wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint8_t* const xring = smem + wid * S::kBytes;
+  uint8_t* const wring = xring + S::kXSlots * S::kXBytes;
+  const int64_t row_bytes = a.K / 32 * kBlockBytes<FMT>;
+  const uint32_t all = (uint32_t)(a.K / 128);  // pairs of steps
+  const uint32_t per = (all + NW - 1) / NW, lo = wid * per < all ? wid * per : all;
+  const uint32_t pairs = all - lo < per ? all - lo : per;
+  const uint32_t rest = wid == NW - 1 ? (uint32_t)(a.K / 32 % 4) : 0;  // blocks behind them
+
+  v16f acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+
+  // sources of the copies; rows past the last are the last one
+  const uint8_t* xsrc[kXCopies];
+  const uint8_t* wsrc[kWCopies];
+#pragma unroll
+  for (int i = 0; i < kXCopies; ++i) {
+    const int64_t m = m0 + i + lane / 8 * (BM / 8);
+    xsrc[i] = reinterpret_cast<const uint8_t*>(a.x + (m < a.M ? m : a.M - 1) * a.ld_x) + lane % 8 * 16;
+  }
+#pragma unroll
+  for (int i = 0; i < kWCopies; ++i) {
+    const int64_t n = n0 + i + lane / 4 * (BN / 16);
+    wsrc[i] = a.codes + (n < a.N ? n : a.N - 1) * row_bytes + lane % 4 * 16;
+  }
+  const uint8_t* srow[TN];
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    const int64_t n = n0 + 32 * j + l;
+    srow[j] = a.scales + (n < a.N ? n : a.N - 1) * (a.K / (FMT == FMT_NVFP4 ? 16 : 32));
+  }
+  ScaleWord<FMT> scales[TN];
+  uint32_t sc[2][TN], cw[TN][8];
+  bf16x8 xf[4][TM];
+  // a step's operands out of the ring, and its products
+  auto read = [&](uint32_t st, auto parity) {
+    constexpr int P = decltype(parity)::value;
+    const uint8_t* xs = xring + st % S::kXSlots * S::kXBytes;
+    const uint8_t* ws = wring + (kTwoSteps ? st / 2 : st) % S::kWSlots * S::kWBytes;
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int b = 0; b < (kTwoSteps ? 1 : 2); ++b) {
+        const word4 c = *reinterpret_cast<const word4*>(ws + R::w(32 * j + l, kTwoSteps ? P * 2 + h : 2 * h + b));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) cw[j][4 * b + q] = c[q];
+      }
+#pragma unroll
+    for (int J = 0; J < 4; ++J)
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+        xf[J][i] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const word4*>(xs + R::x(32 * i + l, 4 * h + J)));
+  };
+  auto split_scales = [&] {
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        if constexpr (FMT == FMT_NVFP4) sc[p][j] = (uint32_t)(scales[j] >> (32 * p)) >> (16 * h);
+        else sc[p][j] = (scales[j] >> (16 * p + 8 * h)) & 0xFFu;
+      }
+  };
+  auto products = [&](auto parity) {
+    constexpr int P = decltype(parity)::value;
+    auto slice = [&](auto num) {
+      constexpr int J = decltype(num)::value;
+      bf16x8 wf[TN];
+#pragma unroll
+      for (int j = 0; j < TN; ++j) wf[j] = decode_eighth<FMT, J>(cw[j], sc[P][j]);
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wf[j], xf[J][i], acc[i][j], 0, 0, 0);
+    };
+    slice(std::integral_constant<int, 0>());
+    slice(std::integral_constant<int, 1>());
+    slice(std::integral_constant<int, 2>());
+    slice(std::integral_constant<int, 3>());
+  };
+  constexpr std::integral_constant<int, 0> even;
+  constexpr std::integral_constant<int, 1> odd;
+
+  if (pairs > 0) {
+    // the wave's pairs, from another one on for each tile; past the last one it
+    // again, which is then not used
+    const uint32_t turn = (ti + tj) % pairs;
+    auto pair_at = [&](uint32_t i) {
+      i = i < pairs ? i : pairs - 1;
+      return lo + (turn + i < pairs ? turn + i : turn + i - pairs);
+    };
+    auto copy_x = [&](uint32_t st) {
+      const uint32_t from = (pair_at(st / 2) * 2 + st % 2) * 128u;
+#pragma unroll
+      for (int i = 0; i < kXCopies; ++i)
+        __builtin_amdgcn_global_load_lds((global_ptr)(xsrc[i] + from),
+                                         (lds_ptr)(xring + st % S::kXSlots * S::kXBytes + i * kCopyPitch), 16, 0, 0);
+    };
+    auto copy_w = [&](uint32_t unit) {  // a pair's codes, or a step's
+      const uint32_t from = (kTwoSteps ? pair_at(unit) : pair_at(unit / 2) * 2 + unit % 2) * 64u;
+#pragma unroll
+      for (int i = 0; i < kWCopies; ++i)
+        __builtin_amdgcn_global_load_lds((global_ptr)(wsrc[i] + from),
+                                         (lds_ptr)(wring + unit % S::kWSlots * S::kWBytes + i * kCopyPitch), 16, 0, 0);
+    };
+    auto load_scales = [&](uint32_t i) {
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        scales[j] = load_pair_scales<FMT>(srow[j] + pair_at(i) * sizeof(ScaleWord<FMT>));
+    };
+    // three steps of copies in flight; kBehind of them may be younger than what a
+    // step waits for (its own X and codes)
+    constexpr int kBehind = 2 * kXCopies + (kTwoSteps ? 1 : 2) * kWCopies;
+    load_scales(0);
+    copy_w(0);
+    copy_x(0);
+    if constexpr (!kTwoSteps) copy_w(1);
+    copy_x(1);
+    copy_w(kTwoSteps ? 1 : 2);
+    copy_x(2);
+    auto step = [&](uint32_t st, auto parity) {
+      constexpr int P = decltype(parity)::value;
+      wait_loads<kBehind>();
+      asm volatile("" ::: "memory");
+      read(st, parity);
+      if constexpr (P == 0) split_scales();
+      // everything has left the ring: the step three behind takes its place
+      __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4) | (0 << 8));
+      asm volatile("" ::: "memory");
+      if constexpr (P == 0) load_scales(st / 2 + 1);
+      if constexpr (!kTwoSteps) copy_w(st + 3);
+      else if constexpr (P == 1) copy_w(st / 2 + 2);
+      copy_x(st + 3);
+      products(parity);
+    };
+    for (uint32_t i = 0; i < pairs; ++i) {
+      step(2 * i, even);
+      step(2 * i + 1, odd);
+    }
+    wait_loads<0>();  // the repeated copies too: LDS is used again
+    asm volatile("" ::: "memory");
+  }
+  if (rest) {  // what is left of K, as a pair that ends in zeros
+    for (uint32_t st = 0; st < 2; ++st) {
+      const bool in = st * 64 + lane % 8 * 8 < rest * 32;
+#pragma unroll
+      for (int i = 0; i < kXCopies; ++i)
+        __builtin_amdgcn_global_load_lds(
+            (global_ptr)(in ? xsrc[i] + (2 * all + st) * 128u : reinterpret_cast<const uint8_t*>(&kZeros)),
+            (lds_ptr)(xring + st * S::kXBytes + i * kCopyPitch), 16, 0, 0);
+    }
+    for (uint32_t unit = 0; unit < (kTwoSteps ? 1 : 2); ++unit) {
+      const bool in = unit * 64 + lane % 4 * 16 < rest * kBlockBytes<FMT>;
+#pragma unroll
+      for (int i = 0; i < kWCopies; ++i)
+        __builtin_amdgcn_global_load_lds((global_ptr)(in ? wsrc[i] + ((kTwoSteps ? all : 2 * all) + unit) * 64u
+                                                         : reinterpret_cast<const uint8_t*>(&kZeros)),
+                                         (lds_ptr)(wring + unit * S::kWBytes + i * kCopyPitch), 16, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < TN; ++j) scales[j] = load_rest_scales<FMT>(srow[j] + all * sizeof(ScaleWord<FMT>), rest);
+    split_scales();
+    wait_loads<0>();
+    asm volatile("" ::: "memory");
+    read(0, even);
+    products(even);
+    if (rest > 2) {
+      read(1, odd);
+      products(odd);
+    }
+  }
+  __syncthreads();
+
+  constexpr int kPitch = BN + 4;
+  static_assert(BM * kPitch * 4 <= S::kBytes, "sums in the rings' LDS");
+  float* red = reinterpret_cast<float*>(smem);
+  float* mine = red + wid * (BM * kPitch);
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<v4f*>(mine + (32 * i + l) * kPitch + 32 * j + 8 * q + 4 * h) =
+            v4f{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+  __syncthreads();
+  join_waves<FMT, DT, BM, BN, NW>(a, vec, red, m0, n0);
+}
+
+template <int FMT, int DT, int BM, int BN, int NW>
+hipError_t launch_split(const LinearArgs& a, hipStream_t s) {
+  constexpr int kLds = NW * SplitRing<FMT, BM, BN>::kBytes;
+  static_assert(kLds <= 160 * 1024, "LDS of a workgroup");
+  auto kernel = k_linear_split<FMT, DT, BM, BN, NW>;
+  static std::atomic<uint64_t> done{0};
+  const hipError_t e = allow_lds((const void*)kernel, kLds, done);
+  if (e != hipSuccess) return e;
+  const uint32_t tm = (uint32_t)((a.M + BM - 1) / BM), tn = (uint32_t)((a.N + BN - 1) / BN);
+  hipLaunchKernelGGL(kernel, dim3(tm * tn), dim3(NW * 64), kLds, s, a, epilogue_vec(a.ep), tm, tn);
+  return hipGetLastError();
+}
+
 template <int FMT, int DT>
 hipError_t launch_as(const LinearArgs& a, hipStream_t s) {
-  if (a.M <= 16) return launch_direct<FMT, DT, 1, 1, 8>(a, s);
-  if (a.M <= 32) return launch_direct<FMT, DT, 2, 2, 8>(a, s);
-  // (pairs of steps, and their words of scales, are whole at multiples of 128)
-  if (a.M > 64 && a.K % 128 == 0 && a.K > 0) {
-    const int64_t large = ((a.M + 255) / 256) * ((a.N + 255) / 256);
-    return large >= 256 ? launch_tile<FMT, DT, 256, 256, 2, 4>(a, s) : launch_tile<FMT, DT, 128, 128, 2, 2>(a, s);
+  auto tiles = [&](int64_t bm, int64_t bn) { return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
+  // One token, and few over few columns: operands straight to registers (1 x 8192
+  // x 4096 4-bit 7.8 us, through LDS 9.2; 16 x 4096 x 14336 8-bit 25 and 34).
+  // Lanes of one row read X in pieces of 16 bytes there, which for more columns
+  // costs more than LDS does (16 x 28672 x 4096 4-bit 40 us, through LDS 24).
+  if (a.M <= 4 || (a.M <= 16 && a.N <= 4096)) return launch_direct<FMT, DT, 1, 1, 8>(a, s);
+  // Up to 640 tiles of 64 x 64, and 64 tokens in any case, share K out among the
+  // waves: larger tiles leave CUs idle (256 x 4096 x 4096 4-bit 15 us, 128 x 128
+  // tiles 41), and beyond that they read less (1024 x 4096 x 4096 52 and 41).
+  // Among those: large enough a grid for the card, then the larger tile (32 x
+  // 14336 x 4096 4-bit 13.5 us, with 32 x 32 16.7; 32 x 7168 x 2048 8.3 and 7.2;
+  // 64 x 14336 x 4096 17.7 us, with 64 x 32 24.6; 128 x 4096 x 4096 13.8 and 11.4; 48 x
+  // 4096 x 14336 8-bit with 64 x 32 44.6, with 32 x 32 and twice the waves 31.9).
+  if (a.M <= 32)
+    return tiles(32, 64) >= 192 ? launch_split<FMT, DT, 32, 64, 4>(a, s) : launch_split<FMT, DT, 32, 32, 8>(a, s);
+  if (a.M <= 64 || tiles(64, 64) <= 640) {
+    if (tiles(64, 64) >= 192) return launch_split<FMT, DT, 64, 64, 4>(a, s);
+    return tiles(32, 32) <= 256 ? launch_split<FMT, DT, 32, 32, 8>(a, s) : launch_split<FMT, DT, 64, 32, 4>(a, s);
   }
-  return launch_direct<FMT, DT, 4, 4, 4>(a, s);
+  // A round of 256 tiles of 256 x 256 takes the card 1 / 0.61 times as long as one
+  // of 512 tiles of 128 x 128, which is half the work (2048 x 4096 x 4096 77 us in
+  // half a round of the large, 66 in one of the small; 4096 x 7168 x 2048 115 in
+  // two, 147 in four).
+  const int64_t large = (tiles(256, 256) + 255) / 256, small = (tiles(128, 128) + 511) / 512;
+  return 100 * large <= 61 * small ? launch_tile<FMT, DT, 256, 256, 2, 4>(a, s)
+                                   : launch_tile<FMT, DT, 128, 128, 2, 2>(a, s);
 }
 
 template <int FMT>

@@ -99,6 +99,21 @@ def test_batches(fmt, M, N, K):
     run(M * 3 + N, M, N, K, fmt, bias="bf16", act="silu", residual=True, drop=0.1)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(70, 130, 32), (100, 264, 64), (20, 96, 96), (90, 200, 224), (300, 264, 1056),
+                                   (1030, 1300, 96), (1500, 1000, 288), (1900, 1040, 192)])
+def test_ragged_sums(fmt, M, N, K):
+    run(M + K, M, N, K, fmt, bias="f32", act="gelu_tanh", keep_z=True)
+
+
+@pytest.mark.parametrize("fmt,K", [("mxfp4", 128), ("nvfp4", 160), ("mxfp8", 192), ("mxfp8_e5m2", 224),
+                                   ("mxint8", 256), ("mxfp4", 32), ("nvfp4", 384), ("mxfp8", 640)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_large_tiles(fmt, K, dtype):
+    """A whole round of the largest tiles, the last ones not full."""
+    run(K, 2040, 8190, K, fmt, dtype, bias="bf16", act="silu", residual=True)
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("M,N,K", [(5, 50, 96), (200, 264, 256), (520, 640, 128)])
