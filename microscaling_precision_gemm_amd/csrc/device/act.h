@@ -31,15 +31,12 @@ __device__ inline float normal_tail(float t) {
   return fmaf(p, w, -2.77565487e-05f);
 }
 
-// P of gelu, and e^(-z^2 / 2).  The square's rounding, worth up to 87 * 2^-24 of
-// the exponential, goes back in as a factor 1 - rest / 2.
-__device__ inline float normal_below(float z, float* density) {
-  const float t = __builtin_elementwise_minimum(__builtin_fabsf(z), 14.0f);  // e^(-98) is 0 here
-  const float q = t * t;
-  const float e = exp_nonpos(-0.5f * q);
-  *density = fmaf(e, -0.5f * fmaf(t, t, -q), e);
-  const float tail = *density * normal_tail(t);
-  return z < 0.0f ? tail : 1.0f - tail;
+// e^(-t^2 / 2) for 0 <= t <= 14 (0 from 13.3 on): as exp_nonpos, and the rounding
+// of the square, worth up to 87 * 2^-24 of the result, goes back in with the rest.
+__device__ inline float normal_density(float t) {
+  const float q = t * t, lo = fmaf(t, t, -q);
+  const float x = -0.5f * q, p = x * kLog2e, y = __builtin_amdgcn_exp2f(p);
+  return fmaf(y, fmaf(-0.5f, lo, exp_rest(x, p)), y);
 }
 
 // The sigmoid and 1 - sigmoid, both to 7 * 2^-24 relative: with y = e^-x and r =
@@ -63,8 +60,9 @@ __device__ inline float act(float z) {
   if constexpr (ACT == ACT_RELU) return __builtin_elementwise_maximum(z, 0.0f);
   else if constexpr (ACT == ACT_SILU) return z * sigmoid(z);
   else if constexpr (ACT == ACT_GELU) {
-    float e;
-    return z * normal_below(z, &e);
+    const float t = __builtin_elementwise_minimum(__builtin_fabsf(z), 14.0f);
+    const float tail = normal_density(t) * normal_tail(t);
+    return z * (z < 0.0f ? tail : 1.0f - tail);
   } else if constexpr (ACT == ACT_GELU_TANH) return z * sigmoid(z * fmaf(kGeluB, z * z, kGeluA));
   else return z;
 }
@@ -77,9 +75,10 @@ __device__ inline float act_slope(float z) {
     const float s = sigmoid_pair(z, &o);
     return s * fmaf(z, o, 1.0f);
   } else if constexpr (ACT == ACT_GELU) {
-    float e;
-    const float p = normal_below(z, &e);
-    return fmaf(z * kInvSqrt2Pi, e, p);
+    // P(-t) - t e / sqrt(2 pi) below 0, 1 minus that above
+    const float t = __builtin_elementwise_minimum(__builtin_fabsf(z), 14.0f);
+    const float s = normal_density(t) * fmaf(-kInvSqrt2Pi, t, normal_tail(t));
+    return z < 0.0f ? s : 1.0f - s;
   } else if constexpr (ACT == ACT_GELU_TANH) {
     // beyond 12 the sigmoid is 0 or 1 and the second term nothing
     const float c = __builtin_elementwise_minimum(__builtin_elementwise_maximum(z, -12.0f), 12.0f);
