@@ -198,8 +198,10 @@ class MXTensor:
         self.layout = int(layout)
 
     def desc(self) -> _Tensor:
-        return _Tensor(self.fmt, self.layout, self.rows, self.cols, _ptr(self.codes),
-                       _ptr(self.scales), _ptr(self.tensor_scale))
+        ts = self.tensor_scale
+        return _Tensor(self.fmt, self.layout, self.rows, self.cols,
+                       None if self.codes is None else self.codes.data_ptr(),
+                       None if self.scales is None else self.scales.data_ptr(), None if ts is None else ts.data_ptr())
 
     def view_rows(self, r0: int, r1: int, tensor_scale=None) -> "MXTensor":
         """Rows [r0, r1) as a tensor sharing storage (row layout only)."""
@@ -633,27 +635,39 @@ def _stream_at(t, stream) -> int:
     return s
 
 
+def _vector(t, dtype, n: int, what: str) -> int:
+    """Address of a dense vector of n elements (0 for None); _dense without a
+    shape to build."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+        raise MXError(f"{what}: expected a dense {dtype} [{n}], got {t.dtype} {list(t.shape)}")
+    return t.data_ptr()
+
+
 def mx_linear(x, W: MXTensor, out, bias=None, act: int = MX_ACT_NONE, z=None, residual=None, drop: float = 0.0,
               seed: int = 0, counter: int = 0, stream=None):
     """out [M, N] (bf16 or fp32) = residual + drop(act(x W^T + bias)) for x bf16
     [M, K] and block-scaled weights W [N, K] (row layout); `z` receives x W^T +
     bias.  bias: bf16 or fp32 [N]; z, residual: dtype of out."""
-    _need(x.dim() == 2 and x.dtype == _torch().bfloat16, "x: a bf16 matrix expected")
-    M, N = x.shape[0], W.rows
-    ldx, ldo = _rows_of(x, M, W.cols, "x"), _rows_of(out, M, N, "out")
-    e = _Epilogue(act=act, drop=drop, rng=_Rng(seed, counter))
+    N, shape = W.rows, x.shape
+    if len(shape) != 2 or shape[1] != W.cols or _dtype_of(x) != MX_BF16:
+        raise MXError(f"x: a bf16 matrix of {W.cols} columns expected, got {x.dtype} {list(shape)}")
+    M = shape[0]
+    dt = _dtype_of(out)
+    b = r = kept = None
+    bias_dt = ld_r = ld_z = 0
     if bias is not None:
-        _need(bias.shape == (N,) and bias.is_contiguous(), "bias: a dense vector of N expected")
-        e.bias, e.bias_dt = bias.data_ptr(), _dtype_of(bias)
+        b, bias_dt = _vector(bias, bias.dtype, N, "bias"), _dtype_of(bias)
     if residual is not None:
-        _need(residual.dtype == out.dtype, "residual: dtype of out expected")
-        e.residual, e.ld_residual = residual.data_ptr(), _rows_of(residual, M, N, "residual")
+        _need(_dtype_of(residual) == dt, "residual: dtype of out expected")
+        r, ld_r = residual.data_ptr(), _rows_of(residual, M, N, "residual")
     if z is not None:
-        _need(z.dtype == out.dtype, "z: dtype of out expected")
-        e.z, e.ld_z = z.data_ptr(), _rows_of(z, M, N, "z")
-    d = W.desc()
-    _check(load().mx_linear(x.data_ptr(), ldx, M, ctypes.byref(d), ctypes.byref(e), out.data_ptr(), _dtype_of(out), ldo,
-                            _stream_at(x, stream)))
+        _need(_dtype_of(z) == dt, "z: dtype of out expected")
+        kept, ld_z = z.data_ptr(), _rows_of(z, M, N, "z")
+    e = _Epilogue(act, bias_dt, b, r, ld_r, kept, ld_z, drop, _Rng(seed, counter))
+    _check(load().mx_linear(x.data_ptr(), _rows_of(x, M, W.cols, "x"), M, ctypes.byref(W.desc()), ctypes.byref(e),
+                            out.data_ptr(), dt, _rows_of(out, M, N, "out"), _stream_at(x, stream)))
     return out
 
 
@@ -669,42 +683,42 @@ def mx_epilogue_backward(d_out, z, d_z, d_bias=None, act: int = MX_ACT_NONE, dro
     mx_epilogue_workspace_bytes(rows, cols); None takes it from torch's
     allocator, for the stream of the call."""
     torch = _torch()
-    _need(d_out.dim() == 2, "d_out: a matrix expected")
-    rows, cols = d_out.shape
-    ld_do = _rows_of(d_out, rows, cols, "d_out")
+    shape, dt = d_out.shape, _dtype_of(d_out)
+    _need(len(shape) == 2, "d_out: a matrix expected")
     _need(z is not None or act == MX_ACT_NONE, "z: wanted with an activation")
-    for t in (z, d_z):
-        _need(t is None or t.dtype == d_out.dtype, "z, d_z: dtype of d_out expected")
-    ld_z = _rows_of(z, rows, cols, "z") if z is not None else 0
-    ld_dz = _rows_of(d_z, rows, cols, "d_z") if d_z is not None else 0
-    db = _dense(d_bias, torch.float32, (cols,), "d_bias")
-    L = load()
-    ws, size = None, 0
+    rows, cols = shape
+    zp = dzp = ld_z = ld_dz = size = 0
+    if z is not None:
+        _need(_dtype_of(z) == dt, "z: dtype of d_out expected")
+        zp, ld_z = z.data_ptr(), _rows_of(z, rows, cols, "z")
+    if d_z is not None:
+        _need(_dtype_of(d_z) == dt, "d_z: dtype of d_out expected")
+        dzp, ld_dz = d_z.data_ptr(), _rows_of(d_z, rows, cols, "d_z")
+    db = _vector(d_bias, torch.float32, cols, "d_bias")
+    L, ws = load(), None
     if workspace is not None:
         size = workspace.numel()
-        ws = _dense(workspace, torch.uint8, (size,), "workspace")
+        ws = _vector(workspace, torch.uint8, size, "workspace")
     elif d_bias is not None:
         size = L.mx_epilogue_workspace_bytes(rows, cols)
         if size:
             with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
                 workspace = torch.empty(size, dtype=torch.uint8, device=d_out.device)
             ws = workspace.data_ptr()
-    _check(L.mx_epilogue_backward(d_out.data_ptr(), _dtype_of(d_out), rows, cols, ld_do,
-                                  0 if z is None else z.data_ptr(), ld_z, act, drop, _Rng(seed, counter),
-                                  0 if d_z is None else d_z.data_ptr(), ld_dz, db, ws, size,
-                                  _stream_at(d_out, stream)))
+    _check(L.mx_epilogue_backward(d_out.data_ptr(), dt, rows, cols, _rows_of(d_out, rows, cols, "d_out"), zp, ld_z, act,
+                                  drop, _Rng(seed, counter), dzp, ld_dz, db, ws, size, _stream_at(d_out, stream)))
     return d_z, d_bias
 
 
 def mx_dropout(x, out, drop: float, seed: int = 0, counter: int = 0, residual=None, stream=None):
     """out = residual + drop(x) (bf16 or fp32); the gradient of x is the same call
     on d_out without a residual."""
-    _need(x.dim() == 2, "x: a matrix expected")
-    rows, cols = x.shape
+    shape = x.shape
+    _need(len(shape) == 2, "x: a matrix expected")
+    rows, cols = shape
     ld_x, ld_out = _rows_of(x, rows, cols, "x"), _rows_of(out, rows, cols, "out")
     ld_r = _rows_of(residual, rows, cols, "residual") if residual is not None else 0
-    for t in (out, residual):
-        _need(t is None or t.dtype == x.dtype, "out, residual: dtype of x expected")
+    _need(out.dtype is x.dtype and (residual is None or residual.dtype is x.dtype), "out, residual: dtype of x expected")
     _check(load().mx_dropout(x.data_ptr(), _dtype_of(x), rows, cols, ld_x,
                              0 if residual is None else residual.data_ptr(), ld_r, drop, _Rng(seed, counter),
                              out.data_ptr(), ld_out, _stream_at(x, stream)))
@@ -744,7 +758,7 @@ def mx_logprob(logits, target, out: Logprobs, scale: float = 1.0, stream=None) -
     * logits): the log probability of target (int64 [tokens]; outside [0, vocab):
     padding; None: no token is given), the entropy, and the topk largest."""
     ld = _rows_of(logits, out.tokens, out.vocab, "logits")
-    at = _dense(target, _torch().int64, (out.tokens,), "target")
+    at = _vector(target, _torch().int64, out.tokens, "target")
     _check(load().mx_logprob(logits.data_ptr(), _dtype_of(logits), ld, at, scale, out._ref, _stream_at(logits, stream)))
     return out
 
@@ -758,9 +772,9 @@ def mx_logprob_backward(logits, target, saved: Logprobs, d_logp, d_entropy, d_lo
     ld = _rows_of(logits, saved.tokens, saved.vocab, "logits")
     ld_d = _rows_of(d_logits, saved.tokens, saved.vocab, "d_logits")
     _need(d_logits.dtype == logits.dtype, "d_logits: dtype of logits expected")
-    at = _dense(target, torch.int64, (saved.tokens,), "target")
-    dl = _dense(d_logp, torch.float32, (saved.tokens,), "d_logp")
-    dh = _dense(d_entropy, torch.float32, (saved.tokens,), "d_entropy")
+    at = _vector(target, torch.int64, saved.tokens, "target")
+    dl = _vector(d_logp, torch.float32, saved.tokens, "d_logp")
+    dh = _vector(d_entropy, torch.float32, saved.tokens, "d_entropy")
     _check(load().mx_logprob_backward(logits.data_ptr(), _dtype_of(logits), ld, at, scale, saved._ref, dl, dh,
                                       d_logits.data_ptr(), ld_d, _stream_at(logits, stream)))
     return d_logits
