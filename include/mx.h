@@ -700,11 +700,15 @@ typedef struct {
  * An entry of -inf has probability 0, logp -inf, and is never an alternative (nor
  * is NaN).  A row without any other entry gets row_max = logp = -inf and 0
  * elsewhere, no alternatives, and a gradient of 0.  A row that holds NaN or +inf
- * gets NaN log probabilities, entropy and gradient.
+ * gets NaN log probabilities, entropy and gradient (its alternatives stay valid
+ * indices).  workspace: mx_logprob_workspace_bytes(tokens, vocab, topk) bytes of
+ * device memory, 16-byte aligned, written before it is read (NULL when that is 0):
+ * few rows are scored in parts.
  * Requirements: 0 <= tokens <= MX_LOGPROB_MAX_TOKENS, 1 <= vocab < 2^31, 0 <= topk
  * <= min(vocab, MX_LOGPROB_MAX_TOPK). */
+size_t mx_logprob_workspace_bytes(int64_t tokens, int64_t vocab, int32_t topk);
 mx_status mx_logprob(const void* logits, int32_t ldt, int64_t ld, const int64_t* target, float scale,
-                     const mx_logprobs* out, mx_stream stream);
+                     const mx_logprobs* out, void* workspace, size_t workspace_bytes, mx_stream stream);
 
 /* Gradient of the logits for d_logp and d_entropy ([tokens] FP32 each, NULL: zero;
  * d_logp of a call without target is not looked at), with p the probabilities:

@@ -46,7 +46,7 @@ EXPORTED = [
     "mx_quantize_batch_noalloc", "mx_route_workspace_bytes", "mx_route", "mx_route_backward", "mx_swiglu",
     "mx_swiglu_backward", "mx_wgrad_workspace_bytes", "mx_wgrad_grouped", "mx_combine",
     "mx_combine_backward", "mx_linear", "mx_epilogue_workspace_bytes", "mx_epilogue_backward", "mx_dropout",
-    "mx_logprob", "mx_logprob_backward", "mx_status_string",
+    "mx_logprob_workspace_bytes", "mx_logprob", "mx_logprob_backward", "mx_status_string",
 ]
 
 
@@ -144,7 +144,8 @@ def load():
         "mx_epilogue_backward": (i32, [vp, i32, i64, i64, i64, vp, i64, i32, f64, _Rng, vp, i64, vp, vp,
                                        ctypes.c_size_t, vp]),
         "mx_dropout": (i32, [vp, i32, i64, i64, i64, vp, i64, f64, _Rng, vp, i64, vp]),
-        "mx_logprob": (i32, [vp, i32, i64, vp, f32, LP, vp]),
+        "mx_logprob_workspace_bytes": (ctypes.c_size_t, [i64, i64, i32]),
+        "mx_logprob": (i32, [vp, i32, i64, vp, f32, LP, vp, ctypes.c_size_t, vp]),
         "mx_logprob_backward": (i32, [vp, i32, i64, vp, f32, LP, vp, vp, vp, i64, vp]),
         "mx_status_string": (ctypes.c_char_p, [i32]),
     }
@@ -630,8 +631,8 @@ def _stream_at(t, stream) -> int:
     goes to that one)."""
     s = _stream_of(stream)
     here = _raw_stream[1]() if _raw_stream else _torch().cuda.current_device()
-    _need(t.get_device() == here and (stream is None or stream.device_index == here),
-          "tensors and streams of the current device expected")
+    if t.get_device() != here or (stream is not None and stream.device_index != here):
+        raise MXError("tensors and streams of the current device expected")
     return s
 
 
@@ -718,7 +719,8 @@ def mx_dropout(x, out, drop: float, seed: int = 0, counter: int = 0, residual=No
     rows, cols = shape
     ld_x, ld_out = _rows_of(x, rows, cols, "x"), _rows_of(out, rows, cols, "out")
     ld_r = _rows_of(residual, rows, cols, "residual") if residual is not None else 0
-    _need(out.dtype is x.dtype and (residual is None or residual.dtype is x.dtype), "out, residual: dtype of x expected")
+    _need(out.dtype is x.dtype and (residual is None or residual.dtype is x.dtype),
+          "out, residual: dtype of x expected")
     _check(load().mx_dropout(x.data_ptr(), _dtype_of(x), rows, cols, ld_x,
                              0 if residual is None else residual.data_ptr(), ld_r, drop, _Rng(seed, counter),
                              out.data_ptr(), ld_out, _stream_at(x, stream)))
@@ -726,10 +728,10 @@ def mx_dropout(x, out, drop: float, seed: int = 0, counter: int = 0, residual=No
 
 
 class Logprobs:
-    """The device buffers of one scoring (the fields of mx_logprobs in mx.h):
-    logp, entropy, row_max, log_sum [tokens]; top_id, top_logp [tokens, topk].
-    The tensors belong to the scoring and are not exchanged for others; copy
-    into them instead."""
+    """The device buffers of one scoring (the fields of mx_logprobs in mx.h) and
+    the workspace that mx_logprob needs: logp, entropy, row_max, log_sum [tokens];
+    top_id, top_logp [tokens, topk].  The tensors belong to the scoring and are not
+    exchanged for others; copy into them instead."""
 
     def __init__(self, tokens: int, vocab: int, topk: int = 0, device="cuda"):
         torch = _torch()
@@ -739,6 +741,7 @@ class Logprobs:
         for n in ("logp", "entropy", "row_max", "log_sum"):
             fields[n] = new(torch.float32, tokens)
         fields.update(top_id=new(torch.int32, tokens, topk), top_logp=new(torch.float32, tokens, topk))
+        fields["workspace"] = new(torch.uint8, int(load().mx_logprob_workspace_bytes(tokens, vocab, topk)))
         d = _Logprobs(tokens, vocab, topk, *(fields[n].data_ptr() for n in (
             "logp", "entropy", "row_max", "log_sum", "top_id", "top_logp")))
         fields.update(_desc=d, _ref=ctypes.byref(d))
@@ -753,13 +756,19 @@ def logprobs(tokens: int, vocab: int, topk: int = 0, device="cuda") -> Logprobs:
     return Logprobs(tokens, vocab, topk, device)
 
 
+def mx_logprob_workspace_bytes(tokens: int, vocab: int, topk: int) -> int:
+    return int(load().mx_logprob_workspace_bytes(tokens, vocab, topk))
+
+
 def mx_logprob(logits, target, out: Logprobs, scale: float = 1.0, stream=None) -> Logprobs:
     """Score each row of logits [tokens, vocab] (bf16 or fp32) under softmax(scale
     * logits): the log probability of target (int64 [tokens]; outside [0, vocab):
     padding; None: no token is given), the entropy, and the topk largest."""
     ld = _rows_of(logits, out.tokens, out.vocab, "logits")
     at = _vector(target, _torch().int64, out.tokens, "target")
-    _check(load().mx_logprob(logits.data_ptr(), _dtype_of(logits), ld, at, scale, out._ref, _stream_at(logits, stream)))
+    ws = out.workspace
+    _check(load().mx_logprob(logits.data_ptr(), _dtype_of(logits), ld, at, scale, out._ref, ws.data_ptr(), ws.numel(),
+                             _stream_at(logits, stream)))
     return out
 
 

@@ -864,15 +864,28 @@ mx_status mx_dropout(const void* x, int32_t dt, int64_t rows, int64_t cols, int6
   return hip_status(mxk::launch_dropout(a, reinterpret_cast<hipStream_t>(stream)));
 }
 
+size_t mx_logprob_workspace_bytes(int64_t tokens, int64_t vocab, int32_t topk) {
+  if (tokens < 1 || tokens > MX_LOGPROB_MAX_TOKENS || vocab < 1 || vocab > INT32_MAX || topk < 0 ||
+      topk > MX_LOGPROB_MAX_TOPK)
+    return 0;
+  return mxk::logprob_workspace(tokens, vocab, topk);
+}
+
 mx_status mx_logprob(const void* logits, int32_t ldt, int64_t ld, const int64_t* target, float scale,
-                     const mx_logprobs* out, mx_stream stream) {
+                     const mx_logprobs* out, void* workspace, size_t workspace_bytes, mx_stream stream) {
   mxk::LogprobArgs a;
   const mx_status st = make_logprob_args(logits, ldt, ld, target, scale, out, &a);
   if (st != MX_OK) return st;
   if (a.tokens == 0) return MX_OK;
   if ((target && !out->logp) || (a.topk > 0 && (!a.top_id || !a.top_logp))) return MX_ERR_NULL;
   if (!elem_aligned(a.logp, 4) || !elem_aligned(a.top_id, 4) || !elem_aligned(a.top_logp, 4)) return MX_ERR_ALIGN;
-  return hip_status(mxk::launch_logprob(a, reinterpret_cast<hipStream_t>(stream)));
+  const size_t need = mxk::logprob_workspace(a.tokens, a.vocab, a.topk);
+  if (need > 0) {
+    if (!workspace) return MX_ERR_NULL;
+    if (workspace_bytes < need) return MX_ERR_SHAPE;
+    if (!aligned16(workspace)) return MX_ERR_ALIGN;
+  }
+  return hip_status(mxk::launch_logprob(a, workspace, reinterpret_cast<hipStream_t>(stream)));
 }
 
 mx_status mx_logprob_backward(const void* logits, int32_t ldt, int64_t ld, const int64_t* target, float scale,

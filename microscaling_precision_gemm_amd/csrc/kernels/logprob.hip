@@ -160,40 +160,89 @@ __device__ inline float max8(const float (&v)[8]) {
   return fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
 }
 
-// One workgroup a row.  Lane t of its NW * 64 takes chunks t, t + NW * 64, ...
-template <int DT, int NW>
-__global__ __launch_bounds__(NW * 64) void k_logprob(LogprobArgs a) {
+// What padding gets.
+__device__ inline bool skip_padding(const LogprobArgs& a, int64_t t, int64_t target) {
+  if (target >= 0 && target < a.vocab) return false;
+  if (threadIdx.x == 0) {
+    if (a.logp) a.logp[t] = 0.0f;
+    a.entropy[t] = 0.0f;
+    a.row_max[t] = 0.0f;
+    a.log_sum[t] = 0.0f;
+  }
+  if ((int)threadIdx.x < a.topk) {
+    a.top_id[t * a.topk + threadIdx.x] = -1;
+    a.top_logp[t * a.topk + threadIdx.x] = -__builtin_inff();
+  }
+  return true;
+}
+
+// A row's results but the alternatives, from its sums; m and log S.
+struct RowSums {
+  float m, log_sum;
+};
+__device__ inline RowSums finish_row(const LogprobArgs& a, int64_t t, const Stats& all, float given) {
+  // s is 0 only where no entry is above -inf (the largest one adds 1)
+  const bool none = all.s == 0.0f;
+  const float m = none ? -__builtin_inff() : all.m, log_sum = none ? 0.0f : logf(all.s);
+  if (threadIdx.x == 0) {
+    a.row_max[t] = m;
+    a.log_sum[t] = log_sum;
+    a.entropy[t] = none ? 0.0f : log_sum - kLn2 * (all.w / all.s);
+    if (a.logp) a.logp[t] = none ? -__builtin_inff() : a.scale * (given - m) - log_sum;
+  }
+  return {m, log_sum};
+}
+__device__ inline void write_alternative(const LogprobArgs& a, int64_t t, uint32_t place, uint64_t key, RowSums r) {
+  a.top_id[t * a.topk + place] = (int32_t)~(uint32_t)key;
+  a.top_logp[t * a.topk + place] = a.scale * (value_of((uint32_t)(key >> 32)) - r.m) - r.log_sum;
+}
+// the places from n on
+__device__ inline void no_alternatives(const LogprobArgs& a, int64_t t, uint32_t n) {
+  if ((int)threadIdx.x < a.topk && threadIdx.x >= n) {
+    a.top_id[t * a.topk + threadIdx.x] = -1;
+    a.top_logp[t * a.topk + threadIdx.x] = -__builtin_inff();
+  }
+}
+
+// What a workgroup leaves of its part of a row: the sums, then topk keys in falling
+// order (0: none).
+__device__ inline char* part_of(void* workspace, int64_t part, int topk) {
+  return static_cast<char*>(workspace) + part * (16 + 8 * topk);
+}
+
+// One workgroup a row, or one of `parts` for a part of it each (SPLIT: few rows,
+// which k_logprob_join puts together).  Lane t of its NW * 64 takes chunks t, t +
+// NW * 64, ...
+template <int DT, int NW, bool SPLIT>
+__global__ __launch_bounds__(NW * 64) void k_logprob(LogprobArgs a, uint32_t parts, void* workspace) {
   constexpr int kLanes = NW * 64, kKeys = 512;
   static_assert(NW * kMaxAlternatives <= kKeys, "the waves' lists");
   __shared__ float part[3][NW];
   __shared__ uint32_t lane_max[kLanes];  // order_of the lanes' maxima; then lanes that reach the bound
   __shared__ uint32_t bound_of, reach[NW], found;
   __shared__ uint64_t keys[kKeys];
-  const int64_t t = blockIdx.x;
+  const int64_t t = SPLIT ? blockIdx.x / parts : blockIdx.x;
   const uint32_t lane = threadIdx.x & 63u, wid = threadIdx.x >> 6;
   const int k = a.topk;
   const int64_t target = a.target ? a.target[t] : 0;
-  if (target < 0 || target >= a.vocab) {  // padding
-    if (threadIdx.x == 0) {
-      if (a.logp) a.logp[t] = 0.0f;
-      a.entropy[t] = 0.0f;
-      a.row_max[t] = 0.0f;
-      a.log_sum[t] = 0.0f;
-    }
-    if ((int)threadIdx.x < k) {
-      a.top_id[t * k + threadIdx.x] = -1;
-      a.top_logp[t * k + threadIdx.x] = -__builtin_inff();
-    }
-    return;
+  if constexpr (SPLIT) {
+    if (target < 0 || target >= a.vocab) return;
+  } else {
+    if (skip_padding(a, t, target)) return;
   }
   const char* row = static_cast<const char*>(a.logits) + t * a.ld * (DT == DT_BF16 ? 2 : 4);
   const int shift = shift_of<DT>(row);
-  const int64_t chunks = (a.vocab + shift + 7) / 8;
+  const uint32_t all_chunks = (uint32_t)((a.vocab + shift + 7) / 8), number = SPLIT ? blockIdx.x % parts : 0;
+  const uint32_t chunk0 = SPLIT ? (uint32_t)((uint64_t)all_chunks * number / parts) : 0;
+  const uint32_t chunk1 = SPLIT ? (uint32_t)((uint64_t)all_chunks * (number + 1) / parts) : all_chunks;
+  const uint32_t chunks = chunk1 - chunk0;
+  const int64_t start = (int64_t)chunk0 * 8 - shift, stop = (int64_t)chunk1 * 8 - shift;
+  const int64_t end = stop < a.vocab ? stop : a.vocab;
   const float c = a.scale * kLog2e;
-  const float given = threadIdx.x == 0 && a.logp ? load1<DT>(row, target) : 0.0f;
+  const float given = !SPLIT && threadIdx.x == 0 && a.logp ? load1<DT>(row, target) : 0.0f;
   Stats st;
   // two chunks at a time, the next two on their way
-  auto chunk_at = [&](int64_t q) { return load_part<DT>(row, q * 8 - shift, a.vocab); };
+  auto chunk_at = [&](int64_t q) { return load_part<DT>(row, start + q * 8, end); };
   RawChunk n0 = chunk_at(threadIdx.x), n1 = chunk_at(threadIdx.x + kLanes);
   for (int64_t q = threadIdx.x; q < chunks + threadIdx.x; q += 2 * kLanes) {
     const RawChunk c0 = n0, c1 = n1;
@@ -237,15 +286,17 @@ __global__ __launch_bounds__(NW * 64) void k_logprob(LogprobArgs a) {
   all.w = part[2][0];
 #pragma unroll
   for (int i = 1; i < NW; ++i) all.join(part[0][i], part[1][i], part[2][i], c);
-  // s is 0 only where no entry is above -inf (the largest one adds 1)
-  const bool none = all.s == 0.0f;
-  const float m = none ? -__builtin_inff() : all.m;
-  const float log_sum = none ? 0.0f : logf(all.s);
-  if (threadIdx.x == 0) {
-    a.row_max[t] = m;
-    a.log_sum[t] = log_sum;
-    a.entropy[t] = none ? 0.0f : log_sum - kLn2 * (all.w / all.s);
-    if (a.logp) a.logp[t] = none ? -__builtin_inff() : a.scale * (given - m) - log_sum;
+  RowSums sums = {};
+  float* mine_out = nullptr;
+  if constexpr (SPLIT) {
+    mine_out = reinterpret_cast<float*>(part_of(workspace, blockIdx.x, k));
+    if (threadIdx.x == 0) {
+      mine_out[0] = all.m;
+      mine_out[1] = all.s;
+      mine_out[2] = all.w;
+    }
+  } else {
+    sums = finish_row(a, t, all, given);
   }
   if (k == 0) return;
 
@@ -278,16 +329,16 @@ __global__ __launch_bounds__(NW * 64) void k_logprob(LogprobArgs a) {
   if (mine >= bound) lane_max[before + (uint32_t)__popcll(here & below)] = threadIdx.x;
   __syncthreads();
   // their chunks by index, 64 a strip and wave
-  const int64_t each = (chunks + kLanes - 1) / kLanes, total = each * lanes;
-  auto strip = [&](int64_t e0, float (&v)[8]) {
-    const int64_t e = e0 + lane, i = e / lanes;
-    const int64_t first = e < total ? (lane_max[e - i * lanes] + i * kLanes) * 8 - shift : a.vocab;
-    const RawChunk r = load_part<DT>(row, first, a.vocab);
+  const uint32_t each = (chunks + kLanes - 1) / kLanes, total = each * lanes;
+  auto strip = [&](uint32_t e0, float (&v)[8]) {
+    const uint32_t e = e0 + lane, i = e / lanes;
+    const int64_t first = e < total ? start + ((int64_t)lane_max[e - i * lanes] + (int64_t)i * kLanes) * 8 : end;
+    const RawChunk r = load_part<DT>(row, first, end);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = raw_value<DT>(r, j);
     return first;
   };
-  for (int64_t e0 = (int64_t)wid * 64; e0 < total; e0 += kLanes) {
+  for (uint32_t e0 = wid * 64; e0 < total; e0 += kLanes) {
     float v[8];
     const int64_t first = strip(e0, v);
     if (__builtin_amdgcn_ballot_w64(order_of(max8(v)) >= bound) == 0) continue;
@@ -312,7 +363,7 @@ __global__ __launch_bounds__(NW * 64) void k_logprob(LogprobArgs a) {
   uint32_t n = found;
   if (n > kKeys) {  // (the same for all)
     TopList list;
-    for (int64_t e0 = (int64_t)wid * 64; e0 < total; e0 += kLanes) {
+    for (uint32_t e0 = wid * 64; e0 < total; e0 += kLanes) {
       float v[8];
       const int64_t first = strip(e0, v);
       take_strip(list, v, max8(v), first, bound, lane, k);
@@ -322,22 +373,86 @@ __global__ __launch_bounds__(NW * 64) void k_logprob(LogprobArgs a) {
     n = NW * k;
     __syncthreads();
   }
-  // a key's place is the number of larger ones
+  // a key's place is the number of larger ones (the lists hold k keys: more than
+  // that many were found)
+  uint64_t* keys_out = SPLIT ? reinterpret_cast<uint64_t*>(mine_out + 4) : nullptr;
   for (uint32_t i = threadIdx.x; i < n; i += kLanes) {
     const uint64_t key = keys[i];
     uint32_t place = 0;
 #pragma unroll 4
     for (uint32_t j = 0; j < n; ++j) place += keys[j] > key;
     if (key && place < (uint32_t)k) {
-      a.top_id[t * k + place] = (int32_t)~(uint32_t)key;
-      a.top_logp[t * k + place] = a.scale * (value_of((uint32_t)(key >> 32)) - m) - log_sum;
+      if constexpr (SPLIT) keys_out[place] = key;
+      else write_alternative(a, t, place, key, sums);
     }
   }
-  // (the lists hold k keys wherever the row has as many)
-  if ((int)threadIdx.x < k && threadIdx.x >= n) {
-    a.top_id[t * k + threadIdx.x] = -1;
-    a.top_logp[t * k + threadIdx.x] = -__builtin_inff();
+  if constexpr (SPLIT) {
+    if ((int)threadIdx.x < k && threadIdx.x >= n) keys_out[threadIdx.x] = 0;
+  } else {
+    no_alternatives(a, t, n);
   }
+}
+
+// The parts of a row put together, their sums in order; of their keys those that
+// reach the upper 16 bits of the k-th largest are ranked.
+constexpr int kMaxParts = 32;  // (8 threads each)
+template <int DT>
+__global__ __launch_bounds__(256) void k_logprob_join(LogprobArgs a, uint32_t parts, void* workspace) {
+  __shared__ uint64_t every[kMaxParts * kMaxAlternatives], keys[kMaxParts * kMaxAlternatives], bound_of;
+  __shared__ float part[kMaxParts][3];
+  __shared__ uint32_t found;
+  const int64_t t = blockIdx.x;
+  const int k = a.topk;
+  const int64_t target = a.target ? a.target[t] : 0;
+  if (skip_padding(a, t, target)) return;
+  const float c = a.scale * kLog2e;
+  const char* row = static_cast<const char*>(a.logits) + t * a.ld * (DT == DT_BF16 ? 2 : 4);
+  const float given = threadIdx.x == 0 && a.logp ? load1<DT>(row, target) : 0.0f;
+  // 8 threads a part fetch what it left
+  const uint32_t p0 = threadIdx.x / 8, l0 = threadIdx.x % 8;
+  if (p0 < parts) {
+    const char* from = part_of(workspace, t * parts + p0, k);
+    if (l0 < 3) part[p0][l0] = reinterpret_cast<const float*>(from)[l0];
+    for (int i = l0; i < k; i += 8) every[p0 * k + i] = reinterpret_cast<const uint64_t*>(from + 16)[i];
+  }
+  if (threadIdx.x == 0) found = 0;
+  __syncthreads();
+  Stats all;
+  for (uint32_t p = 0; p < parts; ++p) all.join(part[p][0], part[p][1], part[p][2], c);
+  const RowSums sums = finish_row(a, t, all, given);
+  if (k == 0) return;
+  if (threadIdx.x < 64) {  // (one wave)
+    constexpr int kEach = kMaxParts * kMaxAlternatives / 64;
+    uint32_t v[kEach], bound = 0;
+    const int rows = (int)(parts * k + 63) / 64;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      v[i] = i * 64 + threadIdx.x < parts * k ? (uint32_t)(every[i * 64 + threadIdx.x] >> 32) : 0;
+#pragma unroll 1
+    for (int b = 31; b >= 16; --b) {
+      const uint32_t next = bound | (1u << b);
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i)
+        if (i < rows) n += __popcll(__builtin_amdgcn_ballot_w64(v[i] >= next));
+      if (n >= k) bound = next;
+    }
+    if (threadIdx.x == 0) bound_of = bound > 0 ? (uint64_t)bound << 32 : 1;
+  }
+  __syncthreads();
+  const uint64_t bound = bound_of;
+  for (uint32_t i = threadIdx.x; i < parts * k; i += 256)
+    if (every[i] >= bound) keys[atomicAdd(&found, 1u)] = every[i];
+  __syncthreads();
+  const uint32_t n = found;
+  for (uint32_t i = threadIdx.x; i < n; i += 256) {
+    const uint64_t key = keys[i];
+    uint32_t place = 0;
+#pragma unroll 4
+    for (uint32_t j = 0; j < n; ++j) place += keys[j] > key;
+    if (place < (uint32_t)k) write_alternative(a, t, place, key, sums);
+  }
+  no_alternatives(a, t, n);
 }
 
 constexpr int kBwdChunks = 4;                     // chunks of 8 a thread
@@ -394,17 +509,52 @@ __global__ __launch_bounds__(256) void k_logprob_bwd(LogprobArgs a, const float*
 
 }  // namespace
 
-hipError_t launch_logprob(const LogprobArgs& a, hipStream_t s) {
-  const dim3 grid((uint32_t)a.tokens);
-#define MXK_LP(NW)                                                                                 \
-  do {                                                                                             \
-    if (a.dt == DT_BF16) hipLaunchKernelGGL((k_logprob<DT_BF16, NW>), grid, dim3(NW * 64), 0, s, a); \
-    else hipLaunchKernelGGL((k_logprob<DT_F32, NW>), grid, dim3(NW * 64), 0, s, a);                  \
+namespace {
+// Parts that a row is scored in.  Few rows leave most of the device idle, and
+// long ones keep it so: 1 x 262144 BF16 takes 23.4 us in one part and 7.6 in 16
+// (27.9 and 14.8 with 20 alternatives), 128 x 128000 14.6 and 11.9.  A second
+// kernel is what it costs, the more with alternatives to rank: 1 x 65536 takes 7.9
+// us in one part and 7.5 in four, with 20 alternatives 10.4 and 12.8; 1 x 100000
+// 14.2 and 13.8 with them, 64 x 128000 17.6 and 15.6, 128 x 100000 16.0 and 18.6.
+// Parts of 16384 entries for few tokens (1 x 128000 with 20: 14.2 us, of 8192
+// 14.7, of 4096 16.2), of 8192 from 16 tokens on.
+uint32_t parts_of(int64_t tokens, int64_t vocab, int32_t topk) {
+  if (topk > 0 ? tokens > 64 || vocab < 98304 : tokens > 128 || vocab < 65536) return 1;
+  const int64_t fill = (512 + tokens - 1) / tokens, most = vocab / (tokens < 16 ? 16384 : 8192);
+  const int64_t p = fill < most ? fill : most;
+  return (uint32_t)(p < kMaxParts ? p : kMaxParts);
+}
+}  // namespace
+
+size_t logprob_workspace(int64_t tokens, int64_t vocab, int32_t topk) {
+  const uint32_t parts = parts_of(tokens, vocab, topk);
+  return parts > 1 ? (size_t)tokens * parts * (16 + 8 * (size_t)topk) : 0;
+}
+
+hipError_t launch_logprob(const LogprobArgs& a, void* workspace, hipStream_t s) {
+  const uint32_t parts = parts_of(a.tokens, a.vocab, a.topk);
+  const dim3 grid((uint32_t)a.tokens * parts);
+#define MXK_LP(NW, SPLIT)                                                                                \
+  do {                                                                                                   \
+    if (a.dt == DT_BF16)                                                                                 \
+      hipLaunchKernelGGL((k_logprob<DT_BF16, NW, SPLIT>), grid, dim3(NW * 64), 0, s, a, parts, workspace); \
+    else                                                                                                 \
+      hipLaunchKernelGGL((k_logprob<DT_F32, NW, SPLIT>), grid, dim3(NW * 64), 0, s, a, parts, workspace);  \
   } while (0)
-  if (a.vocab <= 4096) MXK_LP(1);
-  else if (a.vocab <= 32768) MXK_LP(4);
-  else MXK_LP(8);
+  if (parts == 1) {
+    if (a.vocab <= 4096) MXK_LP(1, false);
+    else if (a.vocab <= 32768) MXK_LP(4, false);
+    else MXK_LP(8, false);
+    return hipGetLastError();
+  }
+  MXK_LP(4, true);
 #undef MXK_LP
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (a.dt == DT_BF16)
+    hipLaunchKernelGGL((k_logprob_join<DT_BF16>), dim3((uint32_t)a.tokens), dim3(256), 0, s, a, parts, workspace);
+  else
+    hipLaunchKernelGGL((k_logprob_join<DT_F32>), dim3((uint32_t)a.tokens), dim3(256), 0, s, a, parts, workspace);
   return hipGetLastError();
 }
 

@@ -95,7 +95,9 @@ struct LogprobArgs {
   float* top_logp;
 };
 constexpr int kMaxAlternatives = 32;
-hipError_t launch_logprob(const LogprobArgs& a, hipStream_t s);
+// workspace: logprob_workspace(tokens, vocab, topk) bytes
+size_t logprob_workspace(int64_t tokens, int64_t vocab, int32_t topk);
+hipError_t launch_logprob(const LogprobArgs& a, void* workspace, hipStream_t s);
 // d_logp, d_entropy: [tokens] or nullptr
 hipError_t launch_logprob_bwd(const LogprobArgs& a, const float* d_logp, const float* d_entropy, void* d_logits,
                               int64_t ld_d, hipStream_t s);

@@ -101,8 +101,8 @@ def scoring(mx, tokens=4, vocab=50, topk=2, **kw):
 def test_logprob(mx):
     L = mx.load()
 
-    def call(p, x=FAKE, dt=0, ld=50, target=FAKE, scale=1.0):
-        return L.mx_logprob(x, dt, ld, target, scale, p, None)
+    def call(p, x=FAKE, dt=0, ld=50, target=FAKE, scale=1.0, ws=None, size=0):
+        return L.mx_logprob(x, dt, ld, target, scale, p, ws, size, None)
 
     ok = scoring(mx)
     assert call(None) == NUL and call(ok, x=None) == NUL and call(ok, dt=2) == FORMAT
@@ -116,6 +116,15 @@ def test_logprob(mx):
     assert call(ok, x=FAKE + 1) == ALIGN and call(ok, x=FAKE + 2, dt=1) == ALIGN and call(ok, target=FAKE + 4) == ALIGN
     for scale in (0.0, -1.0, float("inf"), float("nan")):
         assert call(ok, scale=scale) == UNSUP
+    # few long rows are scored in parts
+    need = mx.mx_logprob_workspace_bytes(2, 100000, 5)
+    assert need > 0 and need % 8 == 0
+    few = scoring(mx, tokens=2, vocab=100000, topk=5)
+    assert call(few, ld=100000) == NUL and call(few, ld=100000, ws=FAKE, size=need - 1) == SHAPE
+    assert call(few, ld=100000, ws=FAKE + 8, size=need) == ALIGN
+    for args in ((0, 100000, 5), (-1, 100000, 5), (2, 0, 0), (2, 1 << 31, 5), (2, 100000, 33), (2, 100000, -1),
+                 (5000, 100000, 5), (2, 1000, 5), ((1 << 21) + 1, 100000, 5)):
+        assert mx.mx_logprob_workspace_bytes(*args) == 0
     assert call(scoring(mx, tokens=0, **dict.fromkeys(("logp", "entropy", "row_max", "log_sum", "top_id", "top_logp"))),
                 x=None) == 0
 

@@ -73,7 +73,8 @@ def run(values, target, topk, scale=1.0, dtype="bf16", pad=0, shift=0, grads=Tru
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T,V,topk", [(1, 1, 1), (2, 2, 2), (3, 7, 5), (5, 8, 0), (4, 63, 20), (7, 64, 32), (3, 511, 1),
-                                      (2, 513, 20), (6, 4097, 8), (3, 8191, 32), (2, 50257, 20), (1, 70001, 0)])
+                                      (2, 513, 20), (6, 4097, 8), (3, 8191, 32), (2, 50257, 20), (1, 70001, 0),
+                                      (1, 65536, 32), (5, 100003, 20), (100, 70000, 0), (64, 100000, 1), (140, 66000, 5)])
 def test_sizes(dtype, T, V, topk):
     g = np.random.default_rng(T * V)
     run(g.normal(size=(T, V)) * 3, g.integers(0, V, T), topk, dtype=dtype)
@@ -94,9 +95,30 @@ def test_many_rows(tokens):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pad,shift", [(0, 1), (5, 3)])
+def test_rows_in_parts(dtype, pad, shift):
+    """Few long rows: alternatives spread over the parts, all in one, parts without
+    an entry, rows without any, padding."""
+    V = 120001
+    g = np.random.default_rng(shift)
+    x = g.normal(size=(9, V)) * 2
+    x[1, 40000:40040] = np.linspace(30, 40, 40)
+    x[2, :70000] = -INF
+    x[3] = -INF
+    x[4] = -INF
+    x[4, [5, 50000, V - 1]] = [1.0, 1.0, 2.0]
+    x[5] = 0.25
+    x[6, ::9000] = 20.0
+    x[7, 80000] = NAN
+    target = [0, 40039, V - 1, 3, 50000, 7, 9000, 1, -1]
+    run(x, target, 32, 1.0, dtype, pad, shift)
+    run(x, None, 4, 0.5, dtype, pad, shift)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("order", ["rising", "falling", "equal", "two values", "zeros of both signs", "steps"])
-def test_ties_and_orders(dtype, order):
-    V = 20000
+@pytest.mark.parametrize("V", [2500, 20000, 110000])
+def test_ties_and_orders(dtype, order, V):
     v = {"rising": np.linspace(-5, 5, V), "falling": np.linspace(5, -5, V), "equal": np.full(V, 1.5),
          "two values": np.where(np.arange(V) % 777 == 5, 2.0, 1.0),
          "zeros of both signs": np.where(np.arange(V) % 2 == 0, -0.0, 0.0), "steps": np.arange(V) // 640 % 5 * 1.0}[order]
