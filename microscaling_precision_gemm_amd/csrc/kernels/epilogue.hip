@@ -52,6 +52,7 @@ inline BwdPlan plan_bwd(int64_t M, int64_t N) {
   const int64_t parts = (1024 + p.stripes - 1) / p.stripes;  // workgroups that fill the card
   const int64_t most = (M + 4 * ty - 1) / (4 * ty);          // at least 4 rows a thread
   p.parts = (uint32_t)(parts < most ? parts : most);
+  if (p.parts == 0) p.parts = 1;  // no rows: their sums are still written
   return p;
 }
 
@@ -148,25 +149,22 @@ size_t epilogue_workspace(int64_t M, int64_t N) {
 }
 
 hipError_t launch_epilogue_bwd(const EpilogueBwdArgs& a, hipStream_t s) {
-  const BwdPlan p = a.M > 0 ? plan_bwd(a.M, a.N) : BwdPlan{1, 0, 0};
+  const BwdPlan p = plan_bwd(a.M, a.N);
   float* sums = !a.d_bias ? nullptr : p.parts > 1 ? a.parts : a.d_bias;
-  if (p.parts > 0) {
-    const dim3 grid(p.stripes, p.parts);
-    const bool vd = rows_aligned16(a.d_out, a.ld_do, a.dt), vz = rows_aligned16(a.z, a.ld_z, a.dt),
-               vo = rows_aligned16(a.d_z, a.ld_dz, a.dt);
-    if (a.dt == DT_BF16)
-      hipLaunchKernelGGL((k_epilogue_bwd<DT_BF16>), grid, dim3(kThreads), 0, s, a, p, sums, vd, vz, vo);
-    else
-      hipLaunchKernelGGL((k_epilogue_bwd<DT_F32>), grid, dim3(kThreads), 0, s, a, p, sums, vd, vz, vo);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+  const dim3 grid(p.stripes, p.parts);
+  const bool vd = rows_aligned16(a.d_out, a.ld_do, a.dt), vz = rows_aligned16(a.z, a.ld_z, a.dt),
+             vo = rows_aligned16(a.d_z, a.ld_dz, a.dt);
+  if (a.dt == DT_BF16)
+    hipLaunchKernelGGL((k_epilogue_bwd<DT_BF16>), grid, dim3(kThreads), 0, s, a, p, sums, vd, vz, vo);
+  else
+    hipLaunchKernelGGL((k_epilogue_bwd<DT_F32>), grid, dim3(kThreads), 0, s, a, p, sums, vd, vz, vo);
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && a.d_bias && p.parts > 1) {
+    hipLaunchKernelGGL(k_join_sums, dim3((uint32_t)((a.N + 15) / 16)), dim3(kThreads), 0, s, a.parts, p.parts, a.N,
+                       a.d_bias);
+    e = hipGetLastError();
   }
-  if (a.d_bias && p.parts != 1) {
-    hipLaunchKernelGGL(k_join_sums, dim3((uint32_t)((a.N + 15) / 16)), dim3(kThreads), 0, s, a.parts,
-                       p.parts, a.N, a.d_bias);
-    return hipGetLastError();
-  }
-  return hipSuccess;
+  return e;
 }
 
 }  // namespace mxk

@@ -68,3 +68,12 @@ def test_dropout_and_epilogue_backward():
     # a column keeps rows * 0.75 of its ones: eight standard deviations (7 per 32768 columns), and the sums' rounding
     kept = d_bias.double() * 0.75
     assert ((kept - rows * 0.75).abs() <= 8 * (rows * 0.1875) ** 0.5 + rows * rows * 2.0 ** -24 / 64).all()
+
+
+@pytest.mark.parametrize("rows", [0, 1])
+def test_bias_gradient_of_many_columns(rows):
+    cols = 2 ** 28 + 24
+    d_out = torch.full((rows, cols), 0.5, dtype=torch.bfloat16, device=dev())
+    d_bias = torch.full((cols,), 7.0, device=dev())
+    mx.mx_epilogue_backward(d_out, None, None, d_bias)
+    assert (d_bias == 0.5 * rows).all()
