@@ -644,8 +644,8 @@ typedef struct {
  * Gradients: d_z and d_bias by mx_epilogue_backward, that of the residual is that
  * of out; X's is mx_linear of d_z by the transposed weights (mx_requant_transpose
  * or mx_quantize of them), W's is mx_wgrad_grouped of d_z and the 8-bit X.
- * Requirements: K % 32 == 0, M and N below 2^26, M * N at most 2^35.  M == 0 or
- * N == 0 enqueues nothing; K == 0 is an empty sum. */
+ * Requirements: K % 32 == 0 and below 2^31, M and N below 2^26, M * N at
+ * most 2^35.  M == 0 or N == 0 enqueues nothing; K == 0 is an empty sum. */
 mx_status mx_linear(const void* X, int64_t ldx, int64_t M, const mx_tensor* W, const mx_epilogue* ep, void* out,
                     int32_t odt, int64_t ldo, mx_stream stream);
 

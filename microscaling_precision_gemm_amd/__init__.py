@@ -626,13 +626,16 @@ def mx_combine_backward(d_out, Y, slot_row, weights, dY, d_weights, stream=None)
 
 
 # ---- a dense layer, and a head that scores tokens ---------------------------
-def _stream_at(t, stream) -> int:
-    """_stream_of for a call on t, which has to be on the current device (a launch
-    goes to that one)."""
+def _stream_at(stream, *tensors) -> int:
+    """_stream_of for a call on these tensors (None: not given), which have to be
+    on the current device (a launch goes to that one)."""
     s = _stream_of(stream)
     here = _raw_stream[1]() if _raw_stream else _torch().cuda.current_device()
-    if t.get_device() != here or (stream is not None and stream.device_index != here):
-        raise MXError("tensors and streams of the current device expected")
+    if stream is not None and stream.device_index != here:
+        raise MXError("a stream of the current device expected")
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise MXError("tensors of the current device expected")
     return s
 
 
@@ -668,7 +671,8 @@ def mx_linear(x, W: MXTensor, out, bias=None, act: int = MX_ACT_NONE, z=None, re
         kept, ld_z = z.data_ptr(), _rows_of(z, M, N, "z")
     e = _Epilogue(act, bias_dt, b, r, ld_r, kept, ld_z, drop, _Rng(seed, counter))
     _check(load().mx_linear(x.data_ptr(), _rows_of(x, M, W.cols, "x"), M, ctypes.byref(W.desc()), ctypes.byref(e),
-                            out.data_ptr(), dt, _rows_of(out, M, N, "out"), _stream_at(x, stream)))
+                            out.data_ptr(), dt, _rows_of(out, M, N, "out"),
+                            _stream_at(stream, x, W.codes, W.scales, W.tensor_scale, bias, z, residual, out)))
     return out
 
 
@@ -707,7 +711,8 @@ def mx_epilogue_backward(d_out, z, d_z, d_bias=None, act: int = MX_ACT_NONE, dro
                 workspace = torch.empty(size, dtype=torch.uint8, device=d_out.device)
             ws = workspace.data_ptr()
     _check(L.mx_epilogue_backward(d_out.data_ptr(), dt, rows, cols, _rows_of(d_out, rows, cols, "d_out"), zp, ld_z, act,
-                                  drop, _Rng(seed, counter), dzp, ld_dz, db, ws, size, _stream_at(d_out, stream)))
+                                  drop, _Rng(seed, counter), dzp, ld_dz, db, ws, size,
+                                  _stream_at(stream, d_out, z, d_z, d_bias, workspace)))
     return d_z, d_bias
 
 
@@ -723,7 +728,7 @@ def mx_dropout(x, out, drop: float, seed: int = 0, counter: int = 0, residual=No
           "out, residual: dtype of x expected")
     _check(load().mx_dropout(x.data_ptr(), _dtype_of(x), rows, cols, ld_x,
                              0 if residual is None else residual.data_ptr(), ld_r, drop, _Rng(seed, counter),
-                             out.data_ptr(), ld_out, _stream_at(x, stream)))
+                             out.data_ptr(), ld_out, _stream_at(stream, x, out, residual)))
     return out
 
 
@@ -768,7 +773,7 @@ def mx_logprob(logits, target, out: Logprobs, scale: float = 1.0, stream=None) -
     at = _vector(target, _torch().int64, out.tokens, "target")
     ws = out.workspace
     _check(load().mx_logprob(logits.data_ptr(), _dtype_of(logits), ld, at, scale, out._ref, ws.data_ptr(), ws.numel(),
-                             _stream_at(logits, stream)))
+                             _stream_at(stream, logits, target, ws)))
     return out
 
 
@@ -785,5 +790,7 @@ def mx_logprob_backward(logits, target, saved: Logprobs, d_logp, d_entropy, d_lo
     dl = _vector(d_logp, torch.float32, saved.tokens, "d_logp")
     dh = _vector(d_entropy, torch.float32, saved.tokens, "d_entropy")
     _check(load().mx_logprob_backward(logits.data_ptr(), _dtype_of(logits), ld, at, scale, saved._ref, dl, dh,
-                                      d_logits.data_ptr(), ld_d, _stream_at(logits, stream)))
+                                      d_logits.data_ptr(), ld_d,
+                                      _stream_at(stream, logits, target, saved.workspace, d_logp, d_entropy,
+                                                 d_logits)))
     return d_logits

@@ -64,6 +64,9 @@ __device__ inline void join_waves(const LinearArgs& a, const EpilogueVec& vec, c
 // at different ones: rows of a power of two of bytes would otherwise all be read
 // at the same offset at a time, from a part of the memory channels.  The next
 // step's operands are loaded while this one's are multiplied.
+// A call is bound by latency: 1 x 7168 x 2048 NVFP4 with residual takes 5.7 us for
+// 8.3 MB, an empty kernel 1.5 to 2; a wave has one step, so load, decoding and the
+// sum over the waves follow one another.
 template <int FMT, int TM, int TN>
 struct DirectStep {
   static constexpr int B = kFourBit<FMT> ? 2 : 1;  // blocks of 32 a lane
@@ -252,6 +255,17 @@ hipError_t launch_direct(const LinearArgs& a, hipStream_t s) {
 // a permutation of chunks and 32-byte pieces of codes did that).  The rows of one
 // copy are BM / 8 (BN / 16) apart and the copies 1040 bytes, so that 16
 // neighbouring rows, which are read together, lie in all banks.
+//
+// The matrix unit at the card's power limit is what bounds a large product: 16384
+// x 14336 x 4096 MXFP4 is 1488 us (1293 TFLOP/s), the instructions busy 71% of the
+// time at 1.7 GHz, where a library's product of BF16 weights is busy 85% at 1.6
+// GHz (1332 us).  Decoding W costs about 10% of that (both waves of a column
+// decode it; from LDS as BF16 its reads would fill the LDS), and bias, gelu and a
+// kept z 8% (1607 us), since nothing runs beside a tile's end.  4096 x 7168 x 2048
+// NVFP4 with dropout and residual is 134 us (897 TFLOP/s): 448 tiles are 1.75
+// rounds of 256, and NVFP4 takes 16 vector instructions for 8 weights, MXFP4 4.
+// No faster: four steps in the ring, 256 x 128 tiles two a CU, wave tiles of 128 x
+// 128, workgroups that start at different steps.
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 constexpr uint32_t kCopyPitch = 1040;
@@ -379,8 +393,9 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_linear_tile(Linea
   auto copy_x = [&](uint32_t step, auto num) {
     constexpr int i = decltype(num)::value;
     const uint32_t from = step < 2 * pairs ? step : 2 * pairs - 1;
-    __builtin_amdgcn_global_load_lds((global_ptr)(xsrc[i] + from * 128u),
-                                     (lds_ptr)(smem + step % R::kCount * R::kXBytes + (wid * 4 + i) * kCopyPitch), 16, 0, 0);
+    __builtin_amdgcn_global_load_lds(
+        (global_ptr)(xsrc[i] + from * 128u),
+        (lds_ptr)(smem + step % R::kCount * R::kXBytes + (wid * 4 + i) * kCopyPitch), 16, 0, 0);
   };
   auto copy_w = [&](uint32_t unit, auto num) {
     constexpr int i = decltype(num)::value;
@@ -545,8 +560,8 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_linear_tile(Linea
       constexpr int i = decltype(num)::value;
       const bool in = unit * 64 + lane % 4 * 16 < rest * kBlockBytes<FMT>;
       const uint8_t* from = in ? wsrc[i] + (units + unit) * 64u : reinterpret_cast<const uint8_t*>(&kZeros);
-      __builtin_amdgcn_global_load_lds((global_ptr)from,
-                                       (lds_ptr)(wring + unit * R::kWBytes + (wid * kWCopies + i) * kCopyPitch), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds(
+          (global_ptr)from, (lds_ptr)(wring + unit * R::kWBytes + (wid * kWCopies + i) * kCopyPitch), 16, 0, 0);
     };
     auto copy_rest = [&](uint32_t st) {
       copy_rest_x(st, s0);
@@ -648,9 +663,11 @@ hipError_t launch_tile(const LinearArgs& a, hipStream_t s) {
 // Each wave of a workgroup takes the whole BM x BN tile over its own part of K
 // (neighbouring pairs of steps), from a ring of LDS that is its own: no barriers,
 // three steps of copies in flight for each of NW waves.  The waves' sums are added
-// through LDS in order.  What bounds it is the L1: 12 KB of operands for 64 x 64 x
-// 64 products are 188 cycles at 64 bytes a cycle against 512 cycles of a wave's
-// matrix instructions, of which four share it.
+// through LDS in order.  On a full card the L1 bounds it: 12 KB of operands for 64 x
+// 64 x 64 products are 188 cycles at 64 bytes a cycle against 512 cycles of a
+// wave's matrix instructions, of which four share it (256 x 4096 x 4096 MXFP4 15
+// us, 573 TFLOP/s).  With few tokens it is HBM, and a start and an end that nothing
+// overlaps: 37 x 14336 x 4096 MXFP8 with silu 18.8 us for 63 MB, 3.4 TB/s.
 template <int FMT, int BM, int BN>
 struct SplitRing {
   static constexpr bool kTwoSteps = kFourBit<FMT>;

@@ -15,8 +15,13 @@
 // value in an order of integers above its index's complement, so equal entries go
 // by lower index.  Where ties make more of them than LDS holds, each wave keeps a
 // sorted list instead, one key a lane, and the lists are ranked.  (Lists kept during
-// the pass: 436 us for 4096 x 128000 BF16 and k = 5, now 195; 27.5 for one token's
-// 50257 and k = 20.)
+// the pass: 436 us for 4096 x 128000 BF16 and k = 5, now 190; 27.5 for one token's
+// 50257 and k = 20, now 9.9.)
+//
+// HBM bounds a batch (4096 x 128000 BF16 190 us, 5.5 TB/s; 11 vector instructions an
+// entry), one CU's vector unit and the steps after the pass a single row: of the 9.4
+// us for 50257 entries with 20 alternatives, 2.7 find these.  Sixteen waves for a
+// row instead of eight take longer (11.5 us).
 #include "../device/chunk8.h"
 #include "../device/exp.h"
 #include "../device/wave.h"
@@ -455,6 +460,9 @@ __global__ __launch_bounds__(256) void k_logprob_join(LogprobArgs a, uint32_t pa
   no_alternatives(a, t, n);
 }
 
+// The gradient: what a thread takes follows from the saved sums and nothing is
+// exchanged, so HBM bounds it (4096 x 128000 BF16, 10% padding whose logits are not
+// read: 350 us, 5.6 TB/s; 509 x 50257 FP32 33 us, 6.1 TB/s).
 constexpr int kBwdChunks = 4;                     // chunks of 8 a thread
 constexpr int64_t kBwdPart = 256 * kBwdChunks;    // chunks of a workgroup
 

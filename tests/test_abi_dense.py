@@ -182,3 +182,39 @@ def test_binding_refuses_mismatched_tensors(mx):
             f()
     with pytest.raises(AttributeError):
         s.logp = z(4)
+
+
+def test_tensors_of_another_device(mx, monkeypatch):
+    """One tensor elsewhere (host memory, say) is refused, whichever it is."""
+    import torch
+
+    class Here(torch.Tensor):
+        def get_device(self):
+            return 0
+
+    monkeypatch.setattr(mx, "_raw_stream", (lambda device: 0, lambda: 0))
+    f32, b, i64, u8 = torch.float32, torch.bfloat16, torch.int64, torch.uint8
+    T = lambda *shape, dt=f32: torch.zeros(shape, dtype=dt).as_subclass(Here)
+    W = lambda t: mx.MXTensor(mx.FORMATS["nvfp4"], 8, 64, t["codes"], t["scales"], t["ts"])
+    s = mx.Logprobs(4, 50, 3, device="cpu")
+    s.__dict__["workspace"] = s.workspace.as_subclass(Here)
+    calls = [
+        (dict(x=T(4, 64, dt=b), codes=T(8, 32, dt=u8), scales=T(8, 4, dt=u8), ts=T(1), bias=T(8), z=T(4, 8),
+              residual=T(4, 8), out=T(4, 8)),
+         lambda t: mx.mx_linear(t["x"], W(t), t["out"], bias=t["bias"], z=t["z"], residual=t["residual"])),
+        (dict(d_out=T(4, 8), z=T(4, 8), d_z=T(4, 8), d_bias=T(8), workspace=T(64, dt=u8)),
+         lambda t: mx.mx_epilogue_backward(t["d_out"], t["z"], t["d_z"], t["d_bias"], act=1,
+                                           workspace=t["workspace"])),
+        (dict(x=T(4, 8), out=T(4, 8), residual=T(4, 8)),
+         lambda t: mx.mx_dropout(t["x"], t["out"], 0.1, residual=t["residual"])),
+        (dict(x=T(4, 50), target=T(4, dt=i64)), lambda t: mx.mx_logprob(t["x"], t["target"], s)),
+        (dict(x=T(4, 50), target=T(4, dt=i64), dl=T(4), dh=T(4), out=T(4, 50)),
+         lambda t: mx.mx_logprob_backward(t["x"], t["target"], s, t["dl"], t["dh"], t["out"])),
+    ]
+    for tensors, call in calls:
+        for name in tensors:
+            with pytest.raises(mx.MXError, match="current device"):
+                call({**tensors, name: tensors[name].as_subclass(torch.Tensor)})
+    s.__dict__["workspace"] = s.workspace.as_subclass(torch.Tensor)
+    with pytest.raises(mx.MXError, match="current device"):
+        calls[3][1](calls[3][0])
