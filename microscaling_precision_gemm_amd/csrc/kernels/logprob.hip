@@ -139,10 +139,10 @@ struct Stats {
 };
 
 // Entries first .. first + 7 of a row as they lie in memory, those outside it as
-// -inf; a chunk inside it is 16-byte aligned.
+// -inf; a chunk inside it is 16-byte aligned if `vec`.
 template <int DT>
-__device__ inline RawChunk load_part(const void* row, int64_t first, int64_t vocab) {
-  if (first >= 0 && first + 8 <= vocab) return load_raw8<DT>(row, first, 8, true);
+__device__ inline RawChunk load_part(const void* row, int64_t first, int64_t vocab, bool vec = true) {
+  if (first >= 0 && first + 8 <= vocab) return load_raw8<DT>(row, first, 8, vec);
   constexpr uint32_t kNone = DT == DT_BF16 ? 0xFF80FF80u : 0xFF800000u;
   RawChunk r = {{kNone, kNone, kNone, kNone}, {kNone, kNone, kNone, kNone}};
   if (first >= vocab) return r;
@@ -460,20 +460,32 @@ __global__ __launch_bounds__(256) void k_logprob_join(LogprobArgs a, uint32_t pa
   no_alternatives(a, t, n);
 }
 
+// a whole chunk, by a streaming store
+template <int DT>
+__device__ inline void store16(char* p, const float* v) {
+  if constexpr (DT == DT_BF16)
+    store_nt(p, pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+  else store_nt(p, f2u(v[0]), f2u(v[1]), f2u(v[2]), f2u(v[3]));
+}
 // The gradient: what a thread takes follows from the saved sums and nothing is
-// exchanged, so HBM bounds it (4096 x 128000 BF16, 10% padding whose logits are not
-// read: 350 us, 5.6 TB/s; 509 x 50257 FP32 33 us, 6.1 TB/s).
-constexpr int kBwdChunks = 4;                     // chunks of 8 a thread
-constexpr int64_t kBwdPart = 256 * kBwdChunks;    // chunks of a workgroup
+// exchanged, so HBM bounds it (4096 x 128000 BF16 372 us, 5.6 TB/s; 2048 x 128000
+// FP32 343, 6.1; 509 x 50257 FP32 40, 5.1).  Lanes take 16 bytes next to each other
+// in both types: FP32 in pieces of 32 bytes, as two accesses that leave every other
+// one out, took 414 and 50 us.  Streaming stores are worth 4% (BF16 386 us without);
+// half the chunks a thread cost as much (383 us; FP32 354 with twice as many).
+template <int DT>
+constexpr int kBwdChunks = DT == DT_BF16 ? 4 : 2;  // 16-byte chunks of a thread
+template <int DT>
+constexpr int kBwdPart = 256 * kBwdChunks<DT>;       // of a workgroup
 
 template <int DT>
 __global__ __launch_bounds__(256) void k_logprob_bwd(LogprobArgs a, const float* __restrict__ d_logp,
                                                      const float* __restrict__ d_entropy, void* d_logits, int64_t ld_d,
                                                      uint32_t parts) {
-  constexpr int EB = DT == DT_BF16 ? 2 : 4;
+  constexpr int EB = DT == DT_BF16 ? 2 : 4, U = 16 / EB;  // bytes of an entry, entries of a chunk
   const int64_t total = a.tokens * parts;
   for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
-    const int64_t t = id / parts, q0 = (id - t * parts) * kBwdPart + threadIdx.x;
+    const int64_t t = id / parts, q0 = (id - t * parts) * kBwdPart<DT> + threadIdx.x;
     const char* row = static_cast<const char*>(a.logits) + t * a.ld * EB;
     char* out = static_cast<char*>(d_logits) + t * ld_d * EB;
     const int shift = shift_of<DT>(out);
@@ -484,32 +496,36 @@ __global__ __launch_bounds__(256) void k_logprob_bwd(LogprobArgs a, const float*
     const float dl = a.target && d_logp ? a.scale * d_logp[t] : 0.0f;
     const float dh = d_entropy ? a.scale * d_entropy[t] : 0.0f;
 #pragma unroll
-    for (int u = 0; u < kBwdChunks; ++u) {
-      const int64_t first = (q0 + u * 256) * 8 - shift;
+    for (int u = 0; u < kBwdChunks<DT>; ++u) {
+      const int64_t first = (q0 + u * 256) * U - shift;
       if (first >= a.vocab) break;
-      float v[8];
-      const bool whole = first >= 0 && first + 8 <= a.vocab;
+      float v[U];
+      const bool whole = first >= 0 && first + U <= a.vocab;
       if (nothing) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+        for (int i = 0; i < U; ++i) v[i] = 0.0f;
       } else {
-        if (whole && vec_in) load8<DT>(row, first, v);
-        else
+        if (whole && vec_in) {
+          const RawChunk r = {*reinterpret_cast<const raw16*>(row + first * EB), {}};
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
+          for (int i = 0; i < U; ++i) v[i] = raw_value<DT>(r, i);
+        } else {
+#pragma unroll
+          for (int i = 0; i < U; ++i)
             v[i] = first + i >= 0 && first + i < a.vocab ? load1<DT>(row, first + i) : -__builtin_inff();
+        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < U; ++i) {
           const float lp = __builtin_elementwise_maximum(fmaf(a.scale, v[i] - m, -log_sum), -150.0f);
           const float p = exp_nonpos(lp);
           const float d = -p * fmaf(dh, lp + H, dl);
           v[i] = first + i == target ? d + dl : d;
         }
       }
-      if (whole) store8<DT>(out, first, v);
+      if (whole) store16<DT>(out + first * EB, v);
       else
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < U; ++i)
           if (first + i >= 0 && first + i < a.vocab) store1<DT>(out, first + i, v[i]);
     }
   }
@@ -568,7 +584,8 @@ hipError_t launch_logprob(const LogprobArgs& a, void* workspace, hipStream_t s) 
 
 hipError_t launch_logprob_bwd(const LogprobArgs& a, const float* d_logp, const float* d_entropy, void* d_logits,
                               int64_t ld_d, hipStream_t s) {
-  const int64_t parts = ((a.vocab + 14) / 8 + kBwdPart - 1) / kBwdPart;  // (a row may start inside a chunk)
+  const int64_t unit = a.dt == DT_BF16 ? 8 : 4, part = a.dt == DT_BF16 ? kBwdPart<DT_BF16> : kBwdPart<DT_F32>;
+  const int64_t parts = ((a.vocab + 2 * unit - 2) / unit + part - 1) / part;  // (a row may start inside a chunk)
   const int64_t total = a.tokens * parts;
   const dim3 grid((uint32_t)(total < (1 << 22) ? total : (1 << 22)));
   if (a.dt == DT_BF16)
