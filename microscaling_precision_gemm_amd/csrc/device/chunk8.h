@@ -69,6 +69,38 @@ __device__ inline void store_chunk(void* p, int64_t off, int n, bool vec, const 
     if (i < n) store1<DT>(p, off + i, v[i]);
 }
 
+// A unit is 16 bytes of a row: 8 BF16 or 4 FP32 values.  Passes that HBM bounds go by
+// units, so that lanes' accesses lie next to each other in both types.
+template <int DT>
+constexpr int kUnit = DT == DT_BF16 ? 8 : 4;
+template <int DT>
+__device__ inline raw16 load_unit(const void* p, int64_t off, int n, bool vec) {
+  if (n >= kUnit<DT> && vec)
+    return *reinterpret_cast<const raw16*>(static_cast<const char*>(p) + off * (DT == DT_BF16 ? 2 : 4));
+  return load_raw8<DT>(p, off, n < kUnit<DT> ? n : kUnit<DT>, false).a;
+}
+template <int DT>
+__device__ inline float unit_value(const raw16& r, int i) {
+  return raw_value<DT>(RawChunk{r, r}, i);
+}
+// v: kUnit values, the first n of which are stored
+template <int DT, bool STREAM>
+__device__ inline void store_unit(void* p, int64_t off, int n, bool vec, const float* v) {
+  if (n >= kUnit<DT> && vec) {
+    char* q = static_cast<char*>(p) + off * (DT == DT_BF16 ? 2 : 4);
+    raw16 r;
+    if constexpr (DT == DT_BF16)
+      r = raw16{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
+    else r = raw16{f2u(v[0]), f2u(v[1]), f2u(v[2]), f2u(v[3])};
+    if constexpr (STREAM) store_nt(q, r[0], r[1], r[2], r[3]);
+    else *reinterpret_cast<raw16*>(q) = r;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kUnit<DT>; ++i)
+    if (i < n) store1<DT>(p, off + i, v[i]);
+}
+
 // Chunk q of the stream (row * ceil(cols / 8) + column / 8): element i takes the
 // 16 bits that the quantizers' stochastic rounding would.
 __device__ inline void drop_chunk(const Drop& d, uint64_t q, float (&v)[8]) {
@@ -76,6 +108,19 @@ __device__ inline void drop_chunk(const Drop& d, uint64_t q, float (&v)[8]) {
   rand16x8(d.seed, d.counter, q, r);
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = r[i] < d.threshold ? 0.0f : v[i] * d.factor;
+}
+
+// The same for FP32 units: lanes 2 j and 2 j + 1 hold the halves of chunk qa in v[0 ..
+// 3] and those of chunk qb in v[4 .. 7].  Each lane draws one of them and gives the
+// other the half that is its.
+__device__ inline void drop_halves(const Drop& d, uint64_t qa, uint64_t qb, float (&v)[8]) {
+  const bool odd = threadIdx.x & 1;
+  const u32x4 w = rand_words(d.seed, d.counter, odd ? qb : qa);
+  const uint32_t g0 = dpp_xor1(odd ? w.x : w.z), g1 = dpp_xor1(odd ? w.y : w.w);
+  const uint32_t r[4] = {odd ? g0 : w.x, odd ? g1 : w.y, odd ? w.z : g0, odd ? w.w : g1};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    v[i] = (i & 1 ? r[i / 2] >> 16 : r[i / 2] & 0xFFFFu) < d.threshold ? 0.0f : v[i] * d.factor;
 }
 
 }  // namespace mxk

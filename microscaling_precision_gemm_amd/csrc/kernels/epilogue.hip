@@ -18,19 +18,35 @@ constexpr int kThreads = 256;
 template <int DT>
 __global__ __launch_bounds__(kThreads) void k_dropout(DropoutArgs a, uint32_t per_row, bool vec_x, bool vec_r,
                                                       bool vec_o) {
+  constexpr int U = kUnit<DT>, R = 8 / U;  // a thread's units: threadIdx.x and kThreads behind it
   const int64_t total = a.M * per_row;
-  for (int64_t q = (int64_t)blockIdx.x * kThreads + threadIdx.x; q < total; q += (int64_t)gridDim.x * kThreads) {
-    const int64_t r = q / per_row, c = (q - r * per_row) * 8;
-    const int n = (int)(a.N - c < 8 ? a.N - c : 8);
-    float v[8], w[8];
-    load_chunk<DT>(a.x, r * a.ld_x + c, n, vec_x, v);
-    if (a.residual) load_chunk<DT>(a.residual, r * a.ld_r + c, n, vec_r, w);
-    if (a.drop.threshold) drop_chunk(a.drop, (uint64_t)q, v);
+  for (int64_t base = (int64_t)blockIdx.x * kThreads; base < total; base += (int64_t)gridDim.x * kThreads) {
+    int64_t q[R], r[R], c[R];
+    int n[R];
+    raw16 x[R], res[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const uint32_t unit = threadIdx.x + k * kThreads;
+      q[k] = base + unit / R;
+      r[k] = q[k] / per_row;
+      c[k] = (q[k] - r[k] * per_row) * 8 + unit % R * U;
+      n[k] = q[k] < total ? (int)(a.N - c[k] < U ? a.N - c[k] : U) : 0;
+      x[k] = load_unit<DT>(a.x, r[k] * a.ld_x + c[k], n[k], vec_x);
+      if (a.residual) res[k] = load_unit<DT>(a.residual, r[k] * a.ld_r + c[k], n[k], vec_r);
+    }
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = unit_value<DT>(x[i / U], i % U);
+    if (a.drop.threshold) {
+      if constexpr (R == 1) drop_chunk(a.drop, (uint64_t)q[0], v);
+      else drop_halves(a.drop, (uint64_t)q[0], (uint64_t)q[1], v);
+    }
     if (a.residual) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = w[i] + v[i];
+      for (int i = 0; i < 8; ++i) v[i] = unit_value<DT>(res[i / U], i % U) + v[i];
     }
-    store_chunk<DT>(a.out, r * a.ld_o + c, n, vec_o, v);
+#pragma unroll
+    for (int k = 0; k < R; ++k) store_unit<DT, false>(a.out, r[k] * a.ld_o + c[k], n[k], vec_o, v + k * U);
   }
 }
 
@@ -65,50 +81,68 @@ inline BwdPlan plan_bwd(int64_t M, int64_t N) {
 template <int DT>
 __global__ __launch_bounds__(kThreads) void k_epilogue_bwd(EpilogueBwdArgs a, BwdPlan p, float* sums, bool vec_do,
                                                            bool vec_z, bool vec_dz) {
-  __shared__ float part[kThreads][9];
-  const uint32_t tx = threadIdx.x & (p.tx - 1), ty = threadIdx.x / p.tx, ny = kThreads / p.tx;
-  const int64_t chunk = (int64_t)blockIdx.x * p.tx + tx, c = chunk * 8;
+  constexpr int U = kUnit<DT>, R = 8 / U;  // columns and rows of a thread at a time
+  __shared__ float part[kThreads][U + 1];
+  const uint32_t wide = p.tx * R, tx = threadIdx.x & (wide - 1), ty = threadIdx.x / wide, ny = kThreads / wide;
+  const int64_t chunk = (int64_t)blockIdx.x * p.tx + tx / R, c = chunk * 8 + tx % R * U;
   const int64_t per_row = (a.N + 7) / 8;
-  const int n = (int)(a.N - c < 8 ? a.N - c : 8);
-  const int64_t step = (int64_t)ny * p.parts;
-  float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (n > 0)
+  const int n = (int)(a.N - c < U ? a.N - c : U);  // (a chunk's second half may not be there)
+  const int64_t step = (int64_t)ny * R * p.parts;
+  float sum[U] = {};
+  if (chunk < per_row)
     with_act(a.act, [&](auto kind) {
       constexpr int ACT = decltype(kind)::value;
-      // (the next row's operands are loaded before this one's are used)
-      RawChunk d_next = {}, z_next = {};
-      auto load = [&](int64_t r) {
-        if (r >= a.M) return;
-        d_next = load_raw8<DT>(a.d_out, r * a.ld_do + c, n, vec_do);
-        if constexpr (ACT != ACT_NONE) z_next = load_raw8<DT>(a.z, r * a.ld_z + c, n, vec_z);
+      // (the next rows' operands are loaded before these are used)
+      raw16 d_next[R] = {}, z_next[R] = {};
+      auto load = [&](int64_t first) {
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+          const int64_t r = first + k * ny;
+          if (r >= a.M) return;
+          d_next[k] = load_unit<DT>(a.d_out, r * a.ld_do + c, n, vec_do);
+          if constexpr (ACT != ACT_NONE) z_next[k] = load_unit<DT>(a.z, r * a.ld_z + c, n, vec_z);
+        }
       };
-      const int64_t r0 = (int64_t)blockIdx.y * ny + ty;
+      const int64_t r0 = (int64_t)blockIdx.y * ny * R + ty;
       load(r0);
       for (int64_t r = r0; r < a.M; r += step) {
-        const RawChunk dr = d_next, zr = z_next;
+        raw16 dr[R], zr[R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+          dr[k] = d_next[k];
+          zr[k] = z_next[k];
+        }
         load(r + step);
         float d[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          d[i] = raw_value<DT>(dr, i);
-          if constexpr (ACT != ACT_NONE) d[i] *= act_slope<ACT>(raw_value<DT>(zr, i));
+          d[i] = unit_value<DT>(dr[i / U], i % U);
+          if constexpr (ACT != ACT_NONE) d[i] *= act_slope<ACT>(unit_value<DT>(zr[i / U], i % U));
         }
-        if (a.drop.threshold) drop_chunk(a.drop, (uint64_t)(r * per_row + chunk), d);
+        if (a.drop.threshold) {
+          const uint64_t q = (uint64_t)(r * per_row + chunk);
+          if constexpr (R == 1) drop_chunk(a.drop, q, d);
+          else drop_halves(a.drop, q, q + (uint64_t)(ny * per_row), d);
+        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] += d[i];
-        if (a.d_z) store_chunk<DT, true>(a.d_z, r * a.ld_dz + c, n, vec_dz, d);
+        for (int k = 0; k < R; ++k) {
+          if (r + k * ny >= a.M) break;
+#pragma unroll
+          for (int i = 0; i < U; ++i) sum[i] += d[k * U + i];
+          if (a.d_z) store_unit<DT, true>(a.d_z, (r + k * ny) * a.ld_dz + c, n, vec_dz, d + k * U);
+        }
       }
     });
   if (!sums) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) part[threadIdx.x][i] = sum[i];
+  for (int i = 0; i < U; ++i) part[threadIdx.x][i] = sum[i];
   __syncthreads();
-  if (ty == 0 && n > 0) {
+  if (ty == 0) {
     for (uint32_t y = 1; y < ny; ++y)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] += part[y * p.tx + tx][i];
+      for (int i = 0; i < U; ++i) sum[i] += part[y * wide + tx][i];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < U; ++i)
       if (i < n) sums[(int64_t)blockIdx.y * a.N + c + i] = sum[i];
   }
 }

@@ -460,29 +460,22 @@ __global__ __launch_bounds__(256) void k_logprob_join(LogprobArgs a, uint32_t pa
   no_alternatives(a, t, n);
 }
 
-// a whole chunk, by a streaming store
-template <int DT>
-__device__ inline void store16(char* p, const float* v) {
-  if constexpr (DT == DT_BF16)
-    store_nt(p, pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-  else store_nt(p, f2u(v[0]), f2u(v[1]), f2u(v[2]), f2u(v[3]));
-}
 // The gradient: what a thread takes follows from the saved sums and nothing is
 // exchanged, so HBM bounds it (4096 x 128000 BF16 372 us, 5.6 TB/s; 2048 x 128000
 // FP32 343, 6.1; 509 x 50257 FP32 40, 5.1).  Lanes take 16 bytes next to each other
 // in both types: FP32 in pieces of 32 bytes, as two accesses that leave every other
 // one out, took 414 and 50 us.  Streaming stores are worth 4% (BF16 386 us without);
-// half the chunks a thread cost as much (383 us; FP32 354 with twice as many).
+// half the units a thread cost as much (383 us; FP32 354 with twice as many).
 template <int DT>
-constexpr int kBwdChunks = DT == DT_BF16 ? 4 : 2;  // 16-byte chunks of a thread
+constexpr int kBwdUnits = DT == DT_BF16 ? 4 : 2;  // units of a thread
 template <int DT>
-constexpr int kBwdPart = 256 * kBwdChunks<DT>;       // of a workgroup
+constexpr int kBwdPart = 256 * kBwdUnits<DT>;     // of a workgroup
 
 template <int DT>
 __global__ __launch_bounds__(256) void k_logprob_bwd(LogprobArgs a, const float* __restrict__ d_logp,
                                                      const float* __restrict__ d_entropy, void* d_logits, int64_t ld_d,
                                                      uint32_t parts) {
-  constexpr int EB = DT == DT_BF16 ? 2 : 4, U = 16 / EB;  // bytes of an entry, entries of a chunk
+  constexpr int EB = DT == DT_BF16 ? 2 : 4, U = kUnit<DT>;  // bytes of an entry, entries of a unit
   const int64_t total = a.tokens * parts;
   for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
     const int64_t t = id / parts, q0 = (id - t * parts) * kBwdPart<DT> + threadIdx.x;
@@ -496,7 +489,7 @@ __global__ __launch_bounds__(256) void k_logprob_bwd(LogprobArgs a, const float*
     const float dl = a.target && d_logp ? a.scale * d_logp[t] : 0.0f;
     const float dh = d_entropy ? a.scale * d_entropy[t] : 0.0f;
 #pragma unroll
-    for (int u = 0; u < kBwdChunks<DT>; ++u) {
+    for (int u = 0; u < kBwdUnits<DT>; ++u) {
       const int64_t first = (q0 + u * 256) * U - shift;
       if (first >= a.vocab) break;
       float v[U];
@@ -506,9 +499,9 @@ __global__ __launch_bounds__(256) void k_logprob_bwd(LogprobArgs a, const float*
         for (int i = 0; i < U; ++i) v[i] = 0.0f;
       } else {
         if (whole && vec_in) {
-          const RawChunk r = {*reinterpret_cast<const raw16*>(row + first * EB), {}};
+          const raw16 r = load_unit<DT>(row, first, U, true);
 #pragma unroll
-          for (int i = 0; i < U; ++i) v[i] = raw_value<DT>(r, i);
+          for (int i = 0; i < U; ++i) v[i] = unit_value<DT>(r, i);
         } else {
 #pragma unroll
           for (int i = 0; i < U; ++i)
@@ -522,7 +515,7 @@ __global__ __launch_bounds__(256) void k_logprob_bwd(LogprobArgs a, const float*
           v[i] = first + i == target ? d + dl : d;
         }
       }
-      if (whole) store16<DT>(out + first * EB, v);
+      if (whole) store_unit<DT, true>(out, first, U, true, v);
       else
 #pragma unroll
         for (int i = 0; i < U; ++i)
