@@ -83,8 +83,8 @@ template <int DT>
 __device__ inline float unit_value(const raw16& r, int i) {
   return raw_value<DT>(RawChunk{r, r}, i);
 }
-// v: kUnit values, the first n of which are stored
-template <int DT, bool STREAM>
+// v: kUnit values, the first n of which are stored, streaming
+template <int DT>
 __device__ inline void store_unit(void* p, int64_t off, int n, bool vec, const float* v) {
   if (n >= kUnit<DT> && vec) {
     char* q = static_cast<char*>(p) + off * (DT == DT_BF16 ? 2 : 4);
@@ -92,8 +92,7 @@ __device__ inline void store_unit(void* p, int64_t off, int n, bool vec, const f
     if constexpr (DT == DT_BF16)
       r = raw16{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
     else r = raw16{f2u(v[0]), f2u(v[1]), f2u(v[2]), f2u(v[3])};
-    if constexpr (STREAM) store_nt(q, r[0], r[1], r[2], r[3]);
-    else *reinterpret_cast<raw16*>(q) = r;
+    store_nt(q, r[0], r[1], r[2], r[3]);
     return;
   }
 #pragma unroll

@@ -12,9 +12,10 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// A chunk of 8 columns a thread, whose 8 draws are one Philox block.  HBM bounds it
-// (16384 x 7168 BF16 with residual 119.5 us, 5.9 TB/s; 171 vector instructions a
-// chunk run beside that), a small call its launch (8 x 4096: 2.3 us).
+// 8 columns a thread, whose draws are one Philox block.  HBM bounds it (16384 x 7168
+// BF16 with residual 119 us, 5.9 TB/s; FP32 8192 x 7168 without 77 us, 6.1; some 170
+// vector instructions a thread run beside that), a small call its launch (8 x 4096:
+// 2.3 us).  Streaming stores: 1% of the first, 5% of the second.
 template <int DT>
 __global__ __launch_bounds__(kThreads) void k_dropout(DropoutArgs a, uint32_t per_row, bool vec_x, bool vec_r,
                                                       bool vec_o) {
@@ -46,7 +47,7 @@ __global__ __launch_bounds__(kThreads) void k_dropout(DropoutArgs a, uint32_t pe
       for (int i = 0; i < 8; ++i) v[i] = unit_value<DT>(res[i / U], i % U) + v[i];
     }
 #pragma unroll
-    for (int k = 0; k < R; ++k) store_unit<DT, false>(a.out, r[k] * a.ld_o + c[k], n[k], vec_o, v + k * U);
+    for (int k = 0; k < R; ++k) store_unit<DT>(a.out, r[k] * a.ld_o + c[k], n[k], vec_o, v + k * U);
   }
 }
 
@@ -56,8 +57,10 @@ __global__ __launch_bounds__(kThreads) void k_dropout(DropoutArgs a, uint32_t pe
 // their own 286; 1792 workgroups 2048 columns wide 311).  Each thread sums its
 // columns, then the threads of one chunk are added in order through LDS.  HBM bounds
 // it, with the slopes' arithmetic close behind (gelu takes 32 vector instructions an
-// element, silu with dropout 31: 4099 x 2047 FP32 20.8 us, 4.8 TB/s, and 3.8 of the
-// joining kernel).
+// element, silu with dropout 31).  FP32 goes by units of 16 bytes too, two rows a
+// thread: in pieces of 32 bytes, whose two accesses each leave out every other
+// unit, 4099 x 2047 with dropout took 29.9 us from HBM, now 24.4, of it 3.8 for the
+// joining kernel; 8192 x 14336 took 314, now 295 (4.8 TB/s).
 struct BwdPlan {
   uint32_t tx;       // chunks side by side, a power of two
   uint32_t stripes;  // workgroups along the columns
@@ -129,7 +132,7 @@ __global__ __launch_bounds__(kThreads) void k_epilogue_bwd(EpilogueBwdArgs a, Bw
           if (r + k * ny >= a.M) break;
 #pragma unroll
           for (int i = 0; i < U; ++i) sum[i] += d[k * U + i];
-          if (a.d_z) store_unit<DT, true>(a.d_z, (r + k * ny) * a.ld_dz + c, n, vec_dz, d + k * U);
+          if (a.d_z) store_unit<DT>(a.d_z, (r + k * ny) * a.ld_dz + c, n, vec_dz, d + k * U);
         }
       }
     });

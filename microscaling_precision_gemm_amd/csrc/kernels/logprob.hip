@@ -515,7 +515,7 @@ __global__ __launch_bounds__(256) void k_logprob_bwd(LogprobArgs a, const float*
           v[i] = first + i == target ? d + dl : d;
         }
       }
-      if (whole) store_unit<DT, true>(out, first, U, true, v);
+      if (whole) store_unit<DT>(out, first, U, true, v);
       else
 #pragma unroll
         for (int i = 0; i < U; ++i)
