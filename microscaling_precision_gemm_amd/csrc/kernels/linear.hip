@@ -666,8 +666,11 @@ hipError_t launch_tile(const LinearArgs& a, hipStream_t s) {
 // through LDS in order.  On a full card the L1 bounds it: 12 KB of operands for 64 x
 // 64 x 64 products are 188 cycles at 64 bytes a cycle against 512 cycles of a
 // wave's matrix instructions, of which four share it (256 x 4096 x 4096 MXFP4 15
-// us, 573 TFLOP/s).  With few tokens it is HBM, and a start and an end that nothing
-// overlaps: 37 x 14336 x 4096 MXFP8 with silu 18.8 us for 63 MB, 3.4 TB/s.
+// us, 573 TFLOP/s).  With few tokens it is still X, of which each tile reads all rows
+// (37 x 14336 x 4096 with silu: 117 MB of X, MXFP4 18.1 us, of 24 tokens 58 MB,
+// 13.1; rows that are not 128-byte aligned 20), then W (MXFP8 24.8 us from HBM, 18.8
+// from the last-level cache).  Copies that leave the rows past the last out are
+// slower by their branches (20.2 us).
 template <int FMT, int BM, int BN>
 struct SplitRing {
   static constexpr bool kTwoSteps = kFourBit<FMT>;
