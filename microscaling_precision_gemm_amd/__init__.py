@@ -12,6 +12,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmx.so")
@@ -112,7 +113,7 @@ def load():
     vp, i32, i64, u32, u64, u16 = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
                                    ctypes.c_uint32, ctypes.c_uint64, ctypes.c_uint16)
     TP, RP = ctypes.POINTER(_Tensor), ctypes.POINTER(_Routing)
-    EP, LP, f32, f64 = ctypes.POINTER(_Epilogue), ctypes.POINTER(_Logprobs), ctypes.c_float, ctypes.c_double
+    LP, f32, f64 = ctypes.POINTER(_Logprobs), ctypes.c_float, ctypes.c_double
     sig = {
         "mx_codes_bytes": (ctypes.c_size_t, [i32, i64, i64]),
         "mx_scales_bytes": (ctypes.c_size_t, [i32, i64, i64]),
@@ -139,7 +140,7 @@ def load():
         "mx_wgrad_grouped": (i32, [vp, i64, i64, i64, TP, vp, i32, vp, vp, i32, i64, u32, vp, ctypes.c_size_t, vp]),
         "mx_combine": (i32, [vp, i32, i64, i64, i64, vp, vp, i64, i32, vp, i32, i64, vp]),
         "mx_combine_backward": (i32, [vp, i32, i64, vp, i64, i64, i64, vp, vp, i64, i32, vp, i64, vp, vp]),
-        "mx_linear": (i32, [vp, i64, i64, TP, EP, vp, i32, i64, vp]),
+        "mx_linear": (i32, [vp, i64, i64, vp, vp, vp, i32, i64, vp]),  # (the structures as bytes)
         "mx_epilogue_workspace_bytes": (ctypes.c_size_t, [i64, i64]),
         "mx_epilogue_backward": (i32, [vp, i32, i64, i64, i64, vp, i64, i32, f64, _Rng, vp, i64, vp, vp,
                                        ctypes.c_size_t, vp]),
@@ -626,27 +627,61 @@ def mx_combine_backward(d_out, Y, slot_row, weights, dY, d_weights, stream=None)
 
 
 # ---- a dense layer, and a head that scores tokens ---------------------------
-def _stream_at(stream, *tensors) -> int:
-    """_stream_of for a call on these tensors (None: not given), which have to be
-    on the current device (a launch goes to that one)."""
+def _stream_at(stream, device: int) -> int:
+    """_stream_of for a call on tensors of `device`, which has to be the current
+    one (a launch goes to that)."""
     s = _stream_of(stream)
     here = _raw_stream[1]() if _raw_stream else _torch().cuda.current_device()
-    if stream is not None and stream.device_index != here:
-        raise MXError("a stream of the current device expected")
-    for t in tensors:
-        if t is not None and t.get_device() != here:
-            raise MXError("tensors of the current device expected")
+    if device != here or (stream is not None and stream.device_index != here):
+        raise MXError("tensors and a stream of the current device expected")
     return s
 
 
-def _vector(t, dtype, n: int, what: str) -> int:
-    """Address of a dense vector of n elements (0 for None); _dense without a
-    shape to build."""
+def _vector(t, dtype, n: int, device: int, what: str) -> int:
+    """Address of a dense vector of n elements on `device` (0 for None); _dense
+    without a shape to build."""
     if t is None:
         return 0
     if t.dtype is not dtype or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
         raise MXError(f"{what}: expected a dense {dtype} [{n}], got {t.dtype} {list(t.shape)}")
+    if t.get_device() != device:
+        raise MXError(f"{what}: tensors of the current device expected")
     return t.data_ptr()
+
+
+def _matrix(t, dtype, rows: int, cols: int, device: int, what: str):
+    """Address and row pitch (see _rows_of) of a [rows, cols] matrix on `device`
+    whose columns are adjacent; (0, 0) for None."""
+    if t is None:
+        return 0, 0
+    if t.dtype is not dtype or t.shape != (rows, cols):
+        raise MXError(f"{what}: expected {dtype} [{rows}, {cols}], got {t.dtype} {list(t.shape)}")
+    if t.get_device() != device:
+        raise MXError(f"{what}: tensors of the current device expected")
+    pitch, step = t.stride()
+    if step != 1 and cols > 1:
+        raise MXError(f"{what}: columns must be adjacent")
+    return t.data_ptr(), pitch if rows > 1 else (cols + 7) // 8 * 8
+
+
+def _is_matrix(t, what: str):
+    if t.dim() != 2:
+        raise MXError(f"{what}: a matrix expected, got {list(t.shape)}")
+    return t.shape
+
+
+# _Tensor and _Epilogue as bytes (packing them is faster than building the structures)
+_PACK_TENSOR, _PACK_EPILOGUE = struct.Struct("=iiqqQQQ").pack, struct.Struct("=iiQQqQqdQQ").pack
+_MASK64 = (1 << 64) - 1
+
+
+def _weights(W: MXTensor, device: int) -> bytes:
+    codes, scales, ts = W.codes, W.scales, W.tensor_scale
+    for t in (codes, scales, ts):
+        if t is not None and t.get_device() != device:
+            raise MXError("W: tensors of the current device expected")
+    return _PACK_TENSOR(W.fmt, W.layout, W.rows, W.cols, 0 if codes is None else codes.data_ptr(),
+                        0 if scales is None else scales.data_ptr(), 0 if ts is None else ts.data_ptr())
 
 
 def mx_linear(x, W: MXTensor, out, bias=None, act: int = MX_ACT_NONE, z=None, residual=None, drop: float = 0.0,
@@ -654,25 +689,17 @@ def mx_linear(x, W: MXTensor, out, bias=None, act: int = MX_ACT_NONE, z=None, re
     """out [M, N] (bf16 or fp32) = residual + drop(act(x W^T + bias)) for x bf16
     [M, K] and block-scaled weights W [N, K] (row layout); `z` receives x W^T +
     bias.  bias: bf16 or fp32 [N]; z, residual: dtype of out."""
-    N, shape = W.rows, x.shape
-    if len(shape) != 2 or shape[1] != W.cols or _dtype_of(x) != MX_BF16:
-        raise MXError(f"x: a bf16 matrix of {W.cols} columns expected, got {x.dtype} {list(shape)}")
-    M = shape[0]
-    dt = _dtype_of(out)
-    b = r = kept = None
-    bias_dt = ld_r = ld_z = 0
+    M, N, dtype, dev = _is_matrix(x, "x")[0], W.rows, out.dtype, x.get_device()
+    _need(_dtype_of(x) == MX_BF16, "x: a bf16 matrix expected")
+    xp, ld_x = _matrix(x, x.dtype, M, W.cols, dev, "x")
+    op, ld_o = _matrix(out, dtype, M, N, dev, "out")
+    rp, ld_r = _matrix(residual, dtype, M, N, dev, "residual")
+    zp, ld_z = _matrix(z, dtype, M, N, dev, "z")
+    bp = bias_dt = 0
     if bias is not None:
-        b, bias_dt = _vector(bias, bias.dtype, N, "bias"), _dtype_of(bias)
-    if residual is not None:
-        _need(_dtype_of(residual) == dt, "residual: dtype of out expected")
-        r, ld_r = residual.data_ptr(), _rows_of(residual, M, N, "residual")
-    if z is not None:
-        _need(_dtype_of(z) == dt, "z: dtype of out expected")
-        kept, ld_z = z.data_ptr(), _rows_of(z, M, N, "z")
-    e = _Epilogue(act, bias_dt, b, r, ld_r, kept, ld_z, drop, _Rng(seed, counter))
-    _check(load().mx_linear(x.data_ptr(), _rows_of(x, M, W.cols, "x"), M, ctypes.byref(W.desc()), ctypes.byref(e),
-                            out.data_ptr(), dt, _rows_of(out, M, N, "out"),
-                            _stream_at(stream, x, W.codes, W.scales, W.tensor_scale, bias, z, residual, out)))
+        bp, bias_dt = _vector(bias, bias.dtype, N, dev, "bias"), _dtype_of(bias)
+    e = _PACK_EPILOGUE(act, bias_dt, bp, rp, ld_r, zp, ld_z, drop, seed & _MASK64, counter & _MASK64)
+    _check(load().mx_linear(xp, ld_x, M, _weights(W, dev), e, op, _dtype_of(out), ld_o, _stream_at(stream, dev)))
     return out
 
 
@@ -688,47 +715,38 @@ def mx_epilogue_backward(d_out, z, d_z, d_bias=None, act: int = MX_ACT_NONE, dro
     mx_epilogue_workspace_bytes(rows, cols); None takes it from torch's
     allocator, for the stream of the call."""
     torch = _torch()
-    shape, dt = d_out.shape, _dtype_of(d_out)
-    _need(len(shape) == 2, "d_out: a matrix expected")
+    rows, cols = _is_matrix(d_out, "d_out")
+    dtype, dev = d_out.dtype, d_out.get_device()
     _need(z is not None or act == MX_ACT_NONE, "z: wanted with an activation")
-    rows, cols = shape
-    zp = dzp = ld_z = ld_dz = size = 0
-    if z is not None:
-        _need(_dtype_of(z) == dt, "z: dtype of d_out expected")
-        zp, ld_z = z.data_ptr(), _rows_of(z, rows, cols, "z")
-    if d_z is not None:
-        _need(_dtype_of(d_z) == dt, "d_z: dtype of d_out expected")
-        dzp, ld_dz = d_z.data_ptr(), _rows_of(d_z, rows, cols, "d_z")
-    db = _vector(d_bias, torch.float32, cols, "d_bias")
-    L, ws = load(), None
+    dop, ld_do = _matrix(d_out, dtype, rows, cols, dev, "d_out")
+    zp, ld_z = _matrix(z, dtype, rows, cols, dev, "z")
+    dzp, ld_dz = _matrix(d_z, dtype, rows, cols, dev, "d_z")
+    db = _vector(d_bias, torch.float32, cols, dev, "d_bias")
+    L, dt, ws, size = load(), _dtype_of(d_out), None, 0
     if workspace is not None:
         size = workspace.numel()
-        ws = _vector(workspace, torch.uint8, size, "workspace")
+        ws = _vector(workspace, torch.uint8, size, dev, "workspace")
     elif d_bias is not None:
         size = L.mx_epilogue_workspace_bytes(rows, cols)
         if size:
             with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
                 workspace = torch.empty(size, dtype=torch.uint8, device=d_out.device)
             ws = workspace.data_ptr()
-    _check(L.mx_epilogue_backward(d_out.data_ptr(), dt, rows, cols, _rows_of(d_out, rows, cols, "d_out"), zp, ld_z, act,
-                                  drop, _Rng(seed, counter), dzp, ld_dz, db, ws, size,
-                                  _stream_at(stream, d_out, z, d_z, d_bias, workspace)))
+    _check(L.mx_epilogue_backward(dop, dt, rows, cols, ld_do, zp, ld_z, act, drop, _Rng(seed, counter), dzp, ld_dz, db,
+                                  ws, size, _stream_at(stream, dev)))
     return d_z, d_bias
 
 
 def mx_dropout(x, out, drop: float, seed: int = 0, counter: int = 0, residual=None, stream=None):
     """out = residual + drop(x) (bf16 or fp32); the gradient of x is the same call
     on d_out without a residual."""
-    shape = x.shape
-    _need(len(shape) == 2, "x: a matrix expected")
-    rows, cols = shape
-    ld_x, ld_out = _rows_of(x, rows, cols, "x"), _rows_of(out, rows, cols, "out")
-    ld_r = _rows_of(residual, rows, cols, "residual") if residual is not None else 0
-    _need(out.dtype is x.dtype and (residual is None or residual.dtype is x.dtype),
-          "out, residual: dtype of x expected")
-    _check(load().mx_dropout(x.data_ptr(), _dtype_of(x), rows, cols, ld_x,
-                             0 if residual is None else residual.data_ptr(), ld_r, drop, _Rng(seed, counter),
-                             out.data_ptr(), ld_out, _stream_at(stream, x, out, residual)))
+    rows, cols = _is_matrix(x, "x")
+    dtype, dev = x.dtype, x.get_device()
+    xp, ld_x = _matrix(x, dtype, rows, cols, dev, "x")
+    op, ld_o = _matrix(out, dtype, rows, cols, dev, "out")
+    rp, ld_r = _matrix(residual, dtype, rows, cols, dev, "residual")
+    _check(load().mx_dropout(xp, _dtype_of(x), rows, cols, ld_x, rp, ld_r, drop, _Rng(seed, counter), op, ld_o,
+                             _stream_at(stream, dev)))
     return out
 
 
@@ -769,11 +787,12 @@ def mx_logprob(logits, target, out: Logprobs, scale: float = 1.0, stream=None) -
     """Score each row of logits [tokens, vocab] (bf16 or fp32) under softmax(scale
     * logits): the log probability of target (int64 [tokens]; outside [0, vocab):
     padding; None: no token is given), the entropy, and the topk largest."""
-    ld = _rows_of(logits, out.tokens, out.vocab, "logits")
-    at = _vector(target, _torch().int64, out.tokens, "target")
-    ws = out.workspace
-    _check(load().mx_logprob(logits.data_ptr(), _dtype_of(logits), ld, at, scale, out._ref, ws.data_ptr(), ws.numel(),
-                             _stream_at(stream, logits, target, ws)))
+    dev, ws = logits.get_device(), out.workspace
+    _need(ws.get_device() == dev, "out: tensors of the current device expected")
+    lp, ld = _matrix(logits, logits.dtype, out.tokens, out.vocab, dev, "logits")
+    at = _vector(target, _torch().int64, out.tokens, dev, "target")
+    _check(load().mx_logprob(lp, _dtype_of(logits), ld, at, scale, out._ref, ws.data_ptr(), ws.numel(),
+                             _stream_at(stream, dev)))
     return out
 
 
@@ -782,15 +801,13 @@ def mx_logprob_backward(logits, target, saved: Logprobs, d_logp, d_entropy, d_lo
     """Gradient of the logits from d_logp and d_entropy (fp32 [tokens] or None),
     for the scoring `saved` of the same logits, target and scale; d_logits may
     be logits itself."""
-    torch = _torch()
-    ld = _rows_of(logits, saved.tokens, saved.vocab, "logits")
-    ld_d = _rows_of(d_logits, saved.tokens, saved.vocab, "d_logits")
-    _need(d_logits.dtype == logits.dtype, "d_logits: dtype of logits expected")
-    at = _vector(target, torch.int64, saved.tokens, "target")
-    dl = _vector(d_logp, torch.float32, saved.tokens, "d_logp")
-    dh = _vector(d_entropy, torch.float32, saved.tokens, "d_entropy")
-    _check(load().mx_logprob_backward(logits.data_ptr(), _dtype_of(logits), ld, at, scale, saved._ref, dl, dh,
-                                      d_logits.data_ptr(), ld_d,
-                                      _stream_at(stream, logits, target, saved.workspace, d_logp, d_entropy,
-                                                 d_logits)))
+    torch, T, V, dev = _torch(), saved.tokens, saved.vocab, logits.get_device()
+    _need(saved.workspace.get_device() == dev, "saved: tensors of the current device expected")
+    lp, ld = _matrix(logits, logits.dtype, T, V, dev, "logits")
+    dlp, ld_d = _matrix(d_logits, logits.dtype, T, V, dev, "d_logits")
+    at = _vector(target, torch.int64, T, dev, "target")
+    dl = _vector(d_logp, torch.float32, T, dev, "d_logp")
+    dh = _vector(d_entropy, torch.float32, T, dev, "d_entropy")
+    _check(load().mx_logprob_backward(lp, _dtype_of(logits), ld, at, scale, saved._ref, dl, dh, dlp, ld_d,
+                                      _stream_at(stream, dev)))
     return d_logits

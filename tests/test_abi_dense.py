@@ -218,3 +218,14 @@ def test_tensors_of_another_device(mx, monkeypatch):
     s.__dict__["workspace"] = s.workspace.as_subclass(torch.Tensor)
     with pytest.raises(mx.MXError, match="current device"):
         calls[3][1](calls[3][0])
+
+
+def test_packed_structures(mx):
+    """The bytes that mx_linear is given are those of the structures."""
+    import torch
+    e = (3, 1, FAKE, FAKE + 64, 2 ** 40, FAKE + 128, 7, 0.25, 2 ** 64 - 1, 2 ** 63)
+    assert mx._PACK_EPILOGUE(*e) == bytes(mx._Epilogue(*e[:8], mx._Rng(*e[8:])))
+    W = mx.MXTensor(3, 8, 64, torch.zeros(8, 32, dtype=torch.uint8), torch.zeros(8, 4, dtype=torch.uint8), None)
+    assert mx._weights(W, -1) == bytes(W.desc())
+    W.tensor_scale = torch.ones(1)
+    assert mx._weights(W, -1) == bytes(W.desc())
