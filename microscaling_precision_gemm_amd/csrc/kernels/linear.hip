@@ -598,9 +598,11 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_linear_tile(Linea
   }
 
   // 32 tokens at a time through the wave's own part of LDS, so that a lane gets 8
-  // neighbouring columns of a row; a pass takes kRows of them.  The residual
-  // comes a pass ahead.  The passes are kept rolled: unrolled, they do not fit the
-  // instruction cache beside the loop above (3 times slower as a whole).
+  // neighbouring columns of a row; a pass takes kRows of them.  The residual of the
+  // next 32 tokens is on its way meanwhile (16384 x 14336 x 4096 with residual 1475
+  // us; that of the next pass alone 1548).  Two passes are unrolled (one: 1490);
+  // all of them do not fit the instruction cache beside the loop above (3 times
+  // slower as a whole).
   constexpr int kCols = 32 * TN, kPitch = kCols + 4, kPer = kCols / 8, kRows = 64 / kPer, kPasses = 32 / kRows;
   static_assert(NW * 32 * kPitch * 4 <= R::kBytes, "epilogue in the ring's LDS");
   float* mine = reinterpret_cast<float*>(smem) + wid * (32 * kPitch);
@@ -615,7 +617,12 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_linear_tile(Linea
     return a.ep.residual && row < a.M ? load_raw8<DT>(a.ep.residual, row * a.ep.ld_r + col, n, vec.residual)
                                       : RawChunk{};
   };
-  RawChunk ahead = residual_of(0);
+  RawChunk ahead[kPasses];
+  auto load_ahead = [&](int first) {
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) ahead[p] = residual_of(first + p);
+  };
+  load_ahead(0);
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     __builtin_amdgcn_wave_barrier();
@@ -626,10 +633,16 @@ __global__ __launch_bounds__(WAVES_M * WAVES_N * 64, 2) void k_linear_tile(Linea
         *reinterpret_cast<v4f*>(mine + l * kPitch + 32 * j + 8 * q + 4 * h) =
             v4f{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
     __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
+    RawChunk now[kPasses];
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) now[p] = ahead[p];
+    if (i + 1 < TM) load_ahead((i + 1) * kPasses);
+#pragma unroll 2
     for (int pass = i * kPasses; pass < (i + 1) * kPasses; ++pass) {
-      const RawChunk res = ahead;
-      if (pass + 1 < TM * kPasses) ahead = residual_of(pass + 1);
+      RawChunk res = now[0];
+#pragma unroll
+      for (int p = 1; p < kPasses; ++p)
+        if (pass == i * kPasses + p) res = now[p];
       const int64_t row = row0 + pass * kRows;
       if (row >= a.M || n == 0) continue;
       const float* p = mine + (pass % kPasses * kRows + t0) * kPitch + c;
