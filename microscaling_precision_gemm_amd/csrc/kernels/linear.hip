@@ -257,13 +257,14 @@ hipError_t launch_direct(const LinearArgs& a, hipStream_t s) {
 // neighbouring rows, which are read together, lie in all banks.
 //
 // The matrix unit at the card's power limit is what bounds a large product: 16384
-// x 14336 x 4096 MXFP4 is 1488 us (1293 TFLOP/s), the instructions busy 71% of the
+// x 14336 x 4096 MXFP4 is 1405 us (1370 TFLOP/s), the instructions busy 71% of the
 // time at 1.7 GHz, where a library's product of BF16 weights is busy 85% at 1.6
-// GHz (1332 us).  Decoding W costs about 10% of that (both waves of a column
-// decode it; from LDS as BF16 its reads would fill the LDS), and bias, gelu and a
-// kept z 8% (1607 us), since nothing runs beside a tile's end.  4096 x 7168 x 2048
-// NVFP4 with dropout and residual is 134 us (897 TFLOP/s): 448 tiles are 1.75
-// rounds of 256, and NVFP4 takes 16 vector instructions for 8 weights, MXFP4 4.
+// GHz (1307 us).  Decoding W costs about 10% of that (both waves of a column
+// decode it; from LDS as BF16 its reads would fill the LDS).  Nothing runs beside a
+// tile's end: gelu and a kept z make it 1550 us, gelu's 32 vector instructions a
+// result alone 1510.  4096 x 7168 x 2048 NVFP4 with dropout and residual is 123 us
+// (977 TFLOP/s): 448 tiles are 1.75 rounds of 256, and NVFP4 takes 16 vector
+// instructions for 8 weights, MXFP4 4.
 // No faster: four steps in the ring, 256 x 128 tiles two a CU, wave tiles of 128 x
 // 128, workgroups that start at different steps.
 typedef float v16f __attribute__((ext_vector_type(16)));
