@@ -114,6 +114,13 @@ def test_large_tiles(fmt, K, dtype):
     run(K, 2040, 8190, K, fmt, dtype, bias="bf16", act="silu", residual=True)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(25, 8300, 288), (45, 8300, 1056), (500, 1030, 96), (1100, 2300, 224)])
+def test_more_than_a_round_of_small_tiles(fmt, dtype, M, N, K):
+    run(M + K, M, N, K, fmt, dtype, bias="f32", act="relu", residual=True, drop=0.25)
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("M,N,K", [(5, 50, 96), (200, 264, 256), (520, 640, 128)])
