@@ -92,6 +92,19 @@ def test_epilogue_backward(act, dtype, rows, cols, pad, shift, drop):
     assert torch.equal(d, first) and torch.equal(db, bias)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(127, 4), (128, 65), (128, 2051), (129, 2051), (129, 4)])
+def test_few_rows(dtype, rows, cols):
+    g = np.random.default_rng(rows + cols)
+    d, d64 = matrix(g.normal(size=(rows, cols)), dtype)
+    z, z64 = matrix(g.normal(size=(rows, cols)), dtype)
+    (want, tol), (bw, bt) = R.epilogue_backward(d64, z64, "silu", R.drop_factors(0.3, SEED, COUNTER, rows, cols), dtype)
+    dz, db = torch.empty_like(d), torch.full((cols,), 5.0, device=dev())
+    mx.mx_epilogue_backward(d, z, dz, db, act=mx.MX_ACT_SILU, drop=0.3, seed=SEED, counter=COUNTER)
+    check(dz, want, tol, "d_z")
+    check(db, bw, bt, "d_bias")
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
 def test_far_arguments(act):
     """The whole range of finite z: slopes of 0 and 1 at its ends, no NaN."""
