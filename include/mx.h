@@ -692,8 +692,8 @@ typedef struct {
  * [tokens, vocab] (BF16 or FP32, row pitch ld, element alignment) that of entry
  * target[t], the entropy, and the topk largest entries in descending order, equal
  * ones by lower index.  Statistics are FP32; the sums round up to 320 + vocab /
- * 2^21 times, 2^-24 relative each.  scale (an inverse temperature): finite and above
- * 0.
+ * 2^21 times, 2^-24 relative each.  scale (an inverse temperature): above 0 and at
+ * most 2^127.
  * target (device int64 [tokens]): a value outside [0, vocab) marks padding, whose
  * logits are not looked at: 0 in all its results, no alternatives.  NULL: no
  * token is given and no row is padding (out->logp is then not written and may be

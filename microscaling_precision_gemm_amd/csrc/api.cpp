@@ -761,7 +761,7 @@ mx_status make_logprob_args(const void* logits, int32_t ldt, int64_t ld, const i
                             const mx_logprobs* p, mxk::LogprobArgs* a) {
   if (!p) return MX_ERR_NULL;
   if (!valid_dt(ldt)) return MX_ERR_FORMAT;
-  if (!(scale > 0.0f) || std::isinf(scale)) return MX_ERR_UNSUPPORTED;
+  if (!(scale > 0.0f && scale <= 0x1p127f)) return MX_ERR_UNSUPPORTED;  // (scale / ln 2 stays finite)
   if (p->tokens < 0 || p->tokens > MX_LOGPROB_MAX_TOKENS || p->vocab < 1 || p->vocab > INT32_MAX || p->topk < 0 ||
       p->topk > MX_LOGPROB_MAX_TOPK || p->topk > p->vocab || ld < p->vocab)
     return MX_ERR_SHAPE;

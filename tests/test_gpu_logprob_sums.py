@@ -45,3 +45,22 @@ def test_a_large_term_does_not_hide_the_small_ones(dtype, V):
     step = 2.0 ** -8 if dtype == "bf16" else U  # (the exponential 4 U, its argument's rounding 2 U (17.5 + ls))
     assert ((got + p).abs() <= p * (1.01 * step + a + U * (4 + 2 * (17.5 + ls)) + 2 * U * ls)).all()
     assert (d[1, ::65536] == 0).all()
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 127, 2.0 ** 100, 2.0 ** -100, 2.0 ** -149])
+@pytest.mark.parametrize("V", [40, 100000])
+def test_scales_at_the_ends(scale, V):
+    """Far scales leave the largest entries alone or all entries alike: sums of 1s, which
+    are exact, and a logarithm good to two steps."""
+    x = torch.full((2, V), -3.0, device=dev())
+    x[:, [4, V - 2]] = 1.0
+    target = torch.tensor([4, 7], device=dev())
+    s = mx.mx_logprob(x, target, mx.logprobs(2, V, 3, dev()), scale)
+    n = 2 if scale > 1 else V
+    assert (s.row_max == 1).all() and (s.log_sum.double() - math.log(n)).abs().max() <= 4 * U * math.log(n)
+    assert (s.entropy.double() - math.log(n)).abs().max() <= 4 * U * math.log(n)
+    assert float(s.logp[0]) == -float(s.log_sum[0]) and not torch.isnan(s.logp).any()
+    assert s.top_id.tolist() == [[4, V - 2, 0]] * 2
+    d = mx.mx_logprob_backward(x, target, s, torch.full((2,), min(1 / scale, 2.0 ** 100), device=dev()), None,
+                               torch.empty_like(x), scale)
+    assert torch.isfinite(d).all() and (d[0, 4] > 0).all() and (scale < 1 or (d[:, 9] == 0).all())
