@@ -630,11 +630,17 @@ def mx_combine_backward(d_out, Y, slot_row, weights, dY, d_weights, stream=None)
 def _stream_at(stream, device: int) -> int:
     """_stream_of for a call on tensors of `device`, which has to be the current
     one (a launch goes to that)."""
-    s = _stream_of(stream)
-    here = _raw_stream[1]() if _raw_stream else _torch().cuda.current_device()
-    if device != here or (stream is not None and stream.device_index != here):
-        raise MXError("tensors and a stream of the current device expected")
-    return s
+    if stream is None and _raw_stream:
+        get, current = _raw_stream
+        here = current()
+        if device == here:
+            return get(here)
+    else:
+        s = _stream_of(stream)
+        here = _raw_stream[1]() if _raw_stream else _torch().cuda.current_device()
+        if device == here and (stream is None or stream.device_index == here):
+            return s
+    raise MXError("tensors and a stream of the current device expected")
 
 
 def _vector(t, dtype, n: int, device: int, what: str) -> int:
@@ -675,12 +681,30 @@ _PACK_TENSOR, _PACK_EPILOGUE = struct.Struct("=iiqqQQQ").pack, struct.Struct("=i
 _MASK64 = (1 << 64) - 1
 
 
+# (code bytes of 32 elements, elements a scale) of the formats that mx_linear takes
+_WEIGHT_SIZES = {MX_MXFP8_E4M3: (32, 32), MX_MXFP8_E5M2: (32, 32), MX_MXINT8: (32, 32), MX_MXFP4_E2M1: (16, 32),
+                 MX_NVFP4: (16, 16)}
+
+
 def _weights(W: MXTensor, device: int) -> bytes:
-    codes, scales, ts = W.codes, W.scales, W.tensor_scale
-    for t in (codes, scales, ts):
-        if t is not None and t.get_device() != device:
+    """W's descriptor; its tensors are dense bytes of its size on `device` (the
+    library cannot see how long they are)."""
+    fmt, rows, cols, codes, scales, ts = W.fmt, W.rows, W.cols, W.codes, W.scales, W.tensor_scale
+    n, sizes = rows * cols, _WEIGHT_SIZES.get(fmt)
+    if sizes and n > 0 and codes is not None and scales is not None:
+        per32, per_scale = sizes
+        if (codes.nbytes * 32 != n * per32 or scales.nbytes * per_scale != n or codes.element_size() != 1
+                or scales.element_size() != 1 or not codes.is_contiguous() or not scales.is_contiguous()):
+            raise MXError(f"W: expected dense bytes, {n * per32 // 32} codes and {n // per_scale} scales, got {codes.dtype} "
+                          f"{list(codes.shape)} and {scales.dtype} {list(scales.shape)}")
+        if codes.get_device() != device or scales.get_device() != device:
             raise MXError("W: tensors of the current device expected")
-    return _PACK_TENSOR(W.fmt, W.layout, W.rows, W.cols, 0 if codes is None else codes.data_ptr(),
+    if ts is not None:
+        if _dtype_of(ts) != MX_F32:
+            raise MXError(f"W: a float32 tensor scale expected, got {ts.dtype} {list(ts.shape)}")
+        if ts.get_device() != device:
+            raise MXError("W: tensors of the current device expected")
+    return _PACK_TENSOR(fmt, W.layout, rows, cols, 0 if codes is None else codes.data_ptr(),
                         0 if scales is None else scales.data_ptr(), 0 if ts is None else ts.data_ptr())
 
 
@@ -689,17 +713,28 @@ def mx_linear(x, W: MXTensor, out, bias=None, act: int = MX_ACT_NONE, z=None, re
     """out [M, N] (bf16 or fp32) = residual + drop(act(x W^T + bias)) for x bf16
     [M, K] and block-scaled weights W [N, K] (row layout); `z` receives x W^T +
     bias.  bias: bf16 or fp32 [N]; z, residual: dtype of out."""
-    M, N, dtype, dev = _is_matrix(x, "x")[0], W.rows, out.dtype, x.get_device()
-    _need(_dtype_of(x) == MX_BF16, "x: a bf16 matrix expected")
-    xp, ld_x = _matrix(x, x.dtype, M, W.cols, dev, "x")
+    shape, N, K, dtype, dev = x.shape, W.rows, W.cols, out.dtype, x.get_device()
+    if len(shape) != 2 or shape[1] != K or _dtype_of(x) != MX_BF16:
+        raise MXError(f"x: a bf16 [M, {K}] expected, got {x.dtype} {list(shape)}")
+    M = shape[0]
+    ld_x, step = x.stride()
+    if step != 1 and K > 1:
+        raise MXError("x: columns must be adjacent")
+    if M <= 1:  # (see _rows_of)
+        ld_x = (K + 7) // 8 * 8
     op, ld_o = _matrix(out, dtype, M, N, dev, "out")
-    rp, ld_r = _matrix(residual, dtype, M, N, dev, "residual")
-    zp, ld_z = _matrix(z, dtype, M, N, dev, "z")
-    bp = bias_dt = 0
+    rp = ld_r = zp = ld_z = bp = bias_dt = 0
+    if residual is not None:
+        rp, ld_r = _matrix(residual, dtype, M, N, dev, "residual")
+    if z is not None:
+        zp, ld_z = _matrix(z, dtype, M, N, dev, "z")
     if bias is not None:
         bp, bias_dt = _vector(bias, bias.dtype, N, dev, "bias"), _dtype_of(bias)
     e = _PACK_EPILOGUE(act, bias_dt, bp, rp, ld_r, zp, ld_z, drop, seed & _MASK64, counter & _MASK64)
-    _check(load().mx_linear(xp, ld_x, M, _weights(W, dev), e, op, _dtype_of(out), ld_o, _stream_at(stream, dev)))
+    status = (_lib or load()).mx_linear(x.data_ptr(), ld_x, M, _weights(W, dev), e, op, _dtype_of(out), ld_o,
+                                        _stream_at(stream, dev))
+    if status:
+        _check(status)
     return out
 
 
