@@ -57,95 +57,66 @@ __device__ inline void join_waves(const LinearArgs& a, const EpilogueVec& vec, c
 }
 
 // ---- operands straight from memory -----------------------------------------
-// A workgroup of NW waves takes a tile of 16 TM tokens x 16 TN columns; its waves
-// share out the steps of K and add their sums through LDS, in order.  A step is
-// 128 bytes of a weight row (256 4-bit or 128 8-bit elements): lane group g of
-// four takes 32 bytes of them.  Each wave has neighbouring steps, and tiles start
-// at different ones: rows of a power of two of bytes would otherwise all be read
-// at the same offset at a time, from a part of the memory channels.  The next
-// step's operands are loaded while this one's are multiplied.
+// A workgroup of NW waves takes all tokens, at most 16, x 16 columns; its waves share out
+// the steps of K and add their sums through LDS, in order.  A step is 128 bytes of a
+// weight row (256 4-bit or 128 8-bit elements): lane group g of four takes 32 bytes of
+// them.  Each wave has neighbouring steps, and tiles start at different ones: rows of a
+// power of two of bytes would otherwise all be read at the same offset at a time, from
+// a part of the memory channels.  The next step's operands are loaded while this one's
+// are multiplied.
 // A call is bound by latency: 1 x 7168 x 2048 NVFP4 with residual takes 5.7 us for
 // 8.3 MB, an empty kernel 1.5 to 2; a wave has one step, so load, decoding and the
 // sum over the waves follow one another.
-template <int FMT, int TM, int TN>
+template <int FMT>
 struct DirectStep {
   static constexpr int B = kFourBit<FMT> ? 2 : 1;  // blocks of 32 a lane
-  word4 codes[TN][2];
-  uint32_t scales[TN][B];
-  word4 x[TM][B][4];
+  word4 codes[2];
+  uint32_t scales[B];
+  word4 x[B][4];
 };
 
-template <int FMT, int DT, int TM, int TN, int NW>
-__global__ __launch_bounds__(NW * 64) void k_linear_direct(LinearArgs a, EpilogueVec vec, uint32_t tiles_m) {
-  using Step = DirectStep<FMT, TM, TN>;
+template <int FMT, int DT, int NW>
+__global__ __launch_bounds__(NW * 64) void k_linear_direct(LinearArgs a, EpilogueVec vec) {
+  using Step = DirectStep<FMT>;
   constexpr int B = Step::B;
-  constexpr int kPitch = TN * 16 + 4;  // floats of a token's row in LDS
-  extern __shared__ __attribute__((aligned(16))) float red[];
+  constexpr int kPitch = 16 + 4;  // floats of a token's row in LDS
+  __shared__ __attribute__((aligned(16))) float red[NW * 16 * kPitch];
   const uint32_t lane = threadIdx.x & 63u, l = lane & 15u, g = lane >> 4;
   const uint32_t wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t tile = blockIdx.x / tiles_m;
-  const int64_t m0 = (int64_t)(blockIdx.x % tiles_m) * (16 * TM), n0 = (int64_t)tile * (16 * TN);
+  const uint32_t tile = blockIdx.x;
+  const int64_t n0 = (int64_t)tile * 16;
   const int64_t row_bytes = a.K / 32 * kBlockBytes<FMT>, blocks = a.K / 32;
 
   // rows past the last are the last one (their results are not stored)
-  const uint8_t* w[TN];
-  int64_t first[TN];  // block number of the row's first block
-#pragma unroll
-  for (int j = 0; j < TN; ++j) {
-    int64_t n = n0 + 16 * j + l;
-    n = n < a.N ? n : a.N - 1;
-    w[j] = a.codes + n * row_bytes;
-    first[j] = n * blocks;
-  }
-  const uint16_t* x[TM];
-#pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int64_t m = m0 + 16 * i + l;
-    x[i] = a.x + (m < a.M ? m : a.M - 1) * a.ld_x;
-  }
+  const int64_t n = n0 + l < a.N ? n0 + l : a.N - 1, m = l < a.M ? l : a.M - 1;
+  const uint8_t* const w = a.codes + n * row_bytes;
+  const int64_t first = n * blocks;  // block number of the row's first block
+  const uint16_t* const x = a.x + m * a.ld_x;
 
-  v4f acc[TM][TN];
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0, 0, 0, 0};
+  v4f acc = {0, 0, 0, 0};
 
   // the lane's blocks start at `blk`
   auto load = [&](Step& s, int64_t blk) {
+    const word4* p = reinterpret_cast<const word4*>(w + blk * kBlockBytes<FMT>);
+    s.codes[0] = p[0];
+    s.codes[1] = p[1];
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const word4* p = reinterpret_cast<const word4*>(w[j] + blk * kBlockBytes<FMT>);
-      s.codes[j][0] = p[0];
-      s.codes[j][1] = p[1];
+    for (int b = 0; b < B; ++b) s.scales[b] = load_scale<FMT>(a.scales, first + blk + b);
 #pragma unroll
-      for (int b = 0; b < B; ++b) s.scales[j][b] = load_scale<FMT>(a.scales, first[j] + blk + b);
-    }
+    for (int b = 0; b < B; ++b)
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-      for (int b = 0; b < B; ++b)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s.x[i][b][e] = *reinterpret_cast<const word4*>(x[i] + (blk + b) * 32 + e * 8);
+      for (int e = 0; e < 4; ++e) s.x[b][e] = *reinterpret_cast<const word4*>(x + (blk + b) * 32 + e * 8);
   };
   auto eighth = [&](const Step& s, auto block, auto num) {
     constexpr int b = decltype(block)::value, J = decltype(num)::value;
-    bf16x8 wb[TN];
+    uint32_t u[8];
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      uint32_t u[8];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        u[q] = s.codes[j][kFourBit<FMT> ? b : 0][q];
-        u[4 + q] = s.codes[j][1][q];
-      }
-      wb[j] = decode_eighth<FMT, J>(u, s.scales[j][b]);
+    for (int q = 0; q < 4; ++q) {
+      u[q] = s.codes[kFourBit<FMT> ? b : 0][q];
+      u[4 + q] = s.codes[1][q];
     }
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j], __builtin_bit_cast(bf16x8, s.x[i][b][J]), acc[i][j],
-                                                            0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode_eighth<FMT, J>(u, s.scales[b]),
+                                                  __builtin_bit_cast(bf16x8, s.x[b][J]), acc, 0, 0, 0);
   };
   auto multiply = [&](const Step& s) {
     auto block = [&](auto b) {
@@ -184,31 +155,28 @@ __global__ __launch_bounds__(NW * 64) void k_linear_direct(LinearArgs a, Epilogu
     for (int b = 0; b < B; ++b) {
       const int64_t blk = (int64_t)steps * (4 * B) + g * B + b;
       if (blk < blocks) {
+        const word4* p = reinterpret_cast<const word4*>(w + blk * kBlockBytes<FMT>);
+        s.codes[b] = p[0];
+        if constexpr (!kFourBit<FMT>) s.codes[1] = p[1];
+        s.scales[b] = load_scale<FMT>(a.scales, first + blk);
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-          const word4* p = reinterpret_cast<const word4*>(w[j] + blk * kBlockBytes<FMT>);
-          s.codes[j][b] = p[0];
-          if constexpr (!kFourBit<FMT>) s.codes[j][1] = p[1];
-          s.scales[j][b] = load_scale<FMT>(a.scales, first[j] + blk);
-        }
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s.x[i][b][e] = *reinterpret_cast<const word4*>(x[i] + blk * 32 + e * 8);
+        for (int e = 0; e < 4; ++e) s.x[b][e] = *reinterpret_cast<const word4*>(x + blk * 32 + e * 8);
       }
     }
     multiply(s);
   }
 
-  float* mine = red + (size_t)wid * (16 * TM * kPitch);
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-      *reinterpret_cast<v4f*>(mine + (16 * i + l) * kPitch + 16 * j + 4 * g) = acc[i][j];
+  *reinterpret_cast<v4f*>(red + wid * (16 * kPitch) + l * kPitch + 4 * g) = acc;
   __syncthreads();
 
-  join_waves<FMT, DT, 16 * TM, 16 * TN, NW>(a, vec, red, m0, n0);
+  join_waves<FMT, DT, 16, 16, NW>(a, vec, red, 0, n0);
+}
+
+template <int FMT, int DT, int NW>
+hipError_t launch_direct(const LinearArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((k_linear_direct<FMT, DT, NW>), dim3((uint32_t)((a.N + 15) / 16)), dim3(NW * 64), 0, s, a,
+                     epilogue_vec(a.ep));
+  return hipGetLastError();
 }
 
 // Raise a kernel's dynamic LDS limit once per device, so that later launches
@@ -224,19 +192,6 @@ hipError_t allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& done)
     done.fetch_or(bit, std::memory_order_acq_rel);
   }
   return hipSuccess;
-}
-
-template <int FMT, int DT, int TM, int TN, int NW>
-hipError_t launch_direct(const LinearArgs& a, hipStream_t s) {
-  constexpr int kLds = NW * 16 * TM * (TN * 16 + 4) * 4;
-  static_assert(kLds <= 160 * 1024, "LDS of a workgroup");
-  auto kernel = k_linear_direct<FMT, DT, TM, TN, NW>;
-  static std::atomic<uint64_t> done{0};
-  const hipError_t e = allow_lds((const void*)kernel, kLds, done);
-  if (e != hipSuccess) return e;
-  const int64_t tm = (a.M + 16 * TM - 1) / (16 * TM), tn = (a.N + 16 * TN - 1) / (16 * TN);
-  hipLaunchKernelGGL(kernel, dim3((uint32_t)(tm * tn)), dim3(NW * 64), kLds, s, a, epilogue_vec(a.ep), (uint32_t)tm);
-  return hipGetLastError();
 }
 
 // ---- operands through LDS ---------------------------------------------------
@@ -919,7 +874,7 @@ hipError_t launch_as(const LinearArgs& a, hipStream_t s) {
   // x 4096 4-bit 7.8 us, through LDS 9.2; 16 x 4096 x 14336 8-bit 25 and 34).
   // Lanes of one row read X in pieces of 16 bytes there, which for more columns
   // costs more than LDS does (16 x 28672 x 4096 4-bit 40 us, through LDS 24).
-  if (a.M <= 4 || (a.M <= 16 && a.N <= 4096)) return launch_direct<FMT, DT, 1, 1, 8>(a, s);
+  if (a.M <= 4 || (a.M <= 16 && a.N <= 4096)) return launch_direct<FMT, DT, 8>(a, s);
   // Up to two rounds of 256 tiles of 64 x 64, and 64 tokens in any case, share K out
   // among the waves: larger tiles leave CUs idle (256 x 4096 x 4096 4-bit 15 us, 128
   // x 128 tiles 33; 384 x 4096 x 4096 27 and 36), and beyond that they take less time
