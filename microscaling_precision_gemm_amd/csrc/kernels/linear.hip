@@ -14,6 +14,7 @@
 
 #include "../device/linear_epilogue.h"
 #include "../device/weights.h"
+#include "../linear_plan.h"
 
 namespace mxk {
 
@@ -869,35 +870,15 @@ hipError_t launch_split(const LinearArgs& a, hipStream_t s) {
 
 template <int FMT, int DT>
 hipError_t launch_as(const LinearArgs& a, hipStream_t s) {
-  auto tiles = [&](int64_t bm, int64_t bn) { return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
-  // One token, and few over few columns: operands straight to registers (1 x 8192
-  // x 4096 4-bit 7.8 us, through LDS 9.2; 16 x 4096 x 14336 8-bit 25 and 34).
-  // Lanes of one row read X in pieces of 16 bytes there, which for more columns
-  // costs more than LDS does (16 x 28672 x 4096 4-bit 40 us, through LDS 24).
-  if (a.M <= 4 || (a.M <= 16 && a.N <= 4096)) return launch_direct<FMT, DT, 8>(a, s);
-  // Up to two rounds of 256 tiles of 64 x 64, and 64 tokens in any case, share K out
-  // among the waves: larger tiles leave CUs idle (256 x 4096 x 4096 4-bit 15 us, 128
-  // x 128 tiles 33; 384 x 4096 x 4096 27 and 36), and beyond that they take less time
-  // (600 x 4096 x 4096 39 and 36; 4096 x 520 x 2080 34 and 29).  Among those the
-  // smallest tile that fills no more than one round: more CUs share the weights (32
-  // x 7168 x 2048 with 32 x 32 7.2 us, with 32 x 64 8.3; 128 x 4096 x 4096 with 64 x
-  // 32 11.4, with 64 x 64 13.8; 48 x 4096 x 14336 8-bit with 64 x 32 44.6, with 32 x
-  // 32 and twice the waves 31.9), but a second round costs more (32 x 10000 x 4096
-  // with 32 x 32 18.3 us, with 32 x 64 13.1; 48 x 9000 x 4096 8-bit with 64 x 32
-  // 28.5, with 64 x 64 22.1).
-  if (a.M <= 32)
-    return tiles(32, 32) <= 256 ? launch_split<FMT, DT, 32, 32, 8>(a, s) : launch_split<FMT, DT, 32, 64, 4>(a, s);
-  if (a.M <= 64 || tiles(64, 64) <= 512) {
-    if (tiles(32, 32) <= 256) return launch_split<FMT, DT, 32, 32, 8>(a, s);
-    return tiles(64, 32) <= 256 ? launch_split<FMT, DT, 64, 32, 4>(a, s) : launch_split<FMT, DT, 64, 64, 4>(a, s);
+  switch (linear_kernel(a.M, a.N)) {
+    case LinearKernel::kDirect: return launch_direct<FMT, DT, 8>(a, s);
+    case LinearKernel::kSplit32x32: return launch_split<FMT, DT, 32, 32, 8>(a, s);
+    case LinearKernel::kSplit32x64: return launch_split<FMT, DT, 32, 64, 4>(a, s);
+    case LinearKernel::kSplit64x32: return launch_split<FMT, DT, 64, 32, 4>(a, s);
+    case LinearKernel::kSplit64x64: return launch_split<FMT, DT, 64, 64, 4>(a, s);
+    case LinearKernel::kTile128: return launch_tile<FMT, DT, 128, 128, 2, 2>(a, s);
+    default: return launch_tile<FMT, DT, 256, 256, 2, 4>(a, s);
   }
-  // A round of 256 tiles of 256 x 256 takes the card 1 / 0.61 times as long as one
-  // of 512 tiles of 128 x 128, which is half the work (2048 x 4096 x 4096 77 us in
-  // half a round of the large, 66 in one of the small; 4096 x 7168 x 2048 115 in
-  // two, 147 in four).
-  const int64_t large = (tiles(256, 256) + 255) / 256, small = (tiles(128, 128) + 511) / 512;
-  return 100 * large <= 61 * small ? launch_tile<FMT, DT, 256, 256, 2, 4>(a, s)
-                                   : launch_tile<FMT, DT, 128, 128, 2, 2>(a, s);
 }
 
 template <int FMT>
