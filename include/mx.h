@@ -643,7 +643,10 @@ typedef struct {
  * pitch); it and z may not overlap each other or any other argument.
  * Gradients: d_z and d_bias by mx_epilogue_backward, that of the residual is that
  * of out; X's is mx_linear of d_z by the transposed weights (mx_requant_transpose
- * or mx_quantize of them), W's is mx_wgrad_grouped of d_z and the 8-bit X.
+ * or mx_quantize of them), W's is mx_wgrad_grouped of d_z and the 8-bit X.  Both take
+ * d_z in BF16: that of an FP32 layer is cast first.
+ * Activations are good to 20 units of 2^-24 relative, GELU_TANH to 4 |u| (1 - s(u))
+ * more, u the argument of its sigmoid; values below 2^-118 may be 0.
  * Requirements: K % 32 == 0 and below 2^31, M and N below 2^26, M * N at
  * most 2^35.  M == 0 or N == 0 enqueues nothing; K == 0 is an empty sum. */
 mx_status mx_linear(const void* X, int64_t ldx, int64_t M, const mx_tensor* W, const mx_epilogue* ep, void* out,
@@ -691,9 +694,10 @@ typedef struct {
 /* Log probabilities under softmax(scale * logits): for each row of logits
  * [tokens, vocab] (BF16 or FP32, row pitch ld, element alignment) that of entry
  * target[t], the entropy, and the topk largest entries in descending order, equal
- * ones by lower index.  Statistics are FP32; the sums round up to 320 + vocab /
- * 2^21 times, 2^-24 relative each.  scale (an inverse temperature): above 0 and at
- * most 2^127.
+ * ones by lower index.  Statistics are FP32; the roundings of a row's sums stay below
+ * (1300 + vocab / 2^19) 2^-24 of them (a few 2^-24 as a rule), a term's error below
+ * (3 |d| + 2) 2^-24 of it, d = scale (x_v - m).  scale (an inverse temperature): above
+ * 0 and at most 2^127.
  * target (device int64 [tokens]): a value outside [0, vocab) marks padding, whose
  * logits are not looked at: 0 in all its results, no alternatives.  NULL: no
  * token is given and no row is padding (out->logp is then not written and may be

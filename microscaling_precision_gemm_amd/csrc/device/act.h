@@ -7,6 +7,12 @@
 //              u = sqrt(8 / pi) (z + 0.044715 z^3), which is z (1 + tanh(u / 2)) / 2
 // NaN stays NaN (relu's slope of it is 0).  At infinities the formulas are
 // taken as they stand (0 times infinity is NaN).
+// Relative errors, in units of 2^-24: silu 8, gelu 18, gelu_tanh 8 + 4 |u| (1 - s): u
+// has four roundings, which matter where the sigmoid falls (13 units at z = -3, 33 at
+// -5, 160 at -9, where the result is 1e-28; carrying u's rounding along would take
+// four more instructions for digits of results that small).  Below -87.4 the
+// sigmoid is 0 and so are silu and gelu_tanh (at u), whose values are under 2^-119
+// there; gelu is 0 from -13.3 down, where it is subnormal.
 #pragma once
 #include "../launch_dense.h"
 #include "exp.h"
@@ -15,9 +21,9 @@ namespace mxk {
 
 // The lower tail of the normal distribution at -t for t >= 0, times
 // e^(t^2 / 2): R(t) = e^(t^2 / 2) erfc(t / sqrt 2) / 2 falls smoothly from 1/2, so
-// a polynomial in w = 1 / (1 + 0.23 t) holds it to 2^-24 relative on 0 .. 14
-// (coefficients fitted for the smallest largest relative error); in FP32 it
-// comes to 9 * 2^-24 with its own roundings and the reciprocal's.
+// a polynomial in w = 1 / (1 + 0.23 t) holds it to 1.5 * 2^-24 relative on 0 .. 14
+// (coefficients fitted for the smallest largest relative error, then rounded); in
+// FP32 it comes to 9 * 2^-24 with its own roundings and the reciprocal's.
 __device__ inline float normal_tail(float t) {
   const float w = __builtin_amdgcn_rcpf(fmaf(0.23f, t, 1.0f));
   float p = -0.0784666166f;

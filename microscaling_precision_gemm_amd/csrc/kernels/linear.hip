@@ -633,14 +633,17 @@ hipError_t launch_tile(const LinearArgs& a, hipStream_t s) {
 // Each wave of a workgroup takes the whole BM x BN tile over its own part of K
 // (neighbouring pairs of steps), from a ring of LDS that is its own: no barriers,
 // three steps of copies in flight for each of NW waves.  The waves' sums are added
-// through LDS in order.  On a full card the L1 bounds it: 12 KB of operands for 64 x
-// 64 x 64 products are 188 cycles at 64 bytes a cycle against 512 cycles of a
-// wave's matrix instructions, of which four share it (256 x 4096 x 4096 MXFP4 15
-// us, 573 TFLOP/s).  With few tokens it is still X, of which each tile reads all rows
-// (37 x 14336 x 4096 with silu: 117 MB of X, MXFP4 18.1 us, of 24 tokens 58 MB,
-// 13.1; rows that are not 128-byte aligned 20), then W (MXFP8 24.8 us from HBM, 18.8
-// from the last-level cache).  Copies that leave the rows past the last out are
-// slower by their branches (20.2 us).
+// through LDS in order.  On a full card no unit fills its time (256 x 4096 x 4096 MXFP4
+// 15 us, 573 TFLOP/s): of the 35000 cycles that a wave lives, its matrix instructions
+// take 8200 and the vector ones 6700; the L1 serves 17000 accesses in them (four
+// waves' 10 KB a step are 10000 at 64 bytes); a third goes by in waits for copies,
+// since three steps in flight are less than the memory's latency when the card is
+// busy, and a third in waits to issue.  With few tokens every tile reads all rows of X
+// (37 x 14336 x 4096 with silu: 117 MB through the L1s beside the weights, MXFP8 18.2 us
+// from the last-level cache and 23.2 from HBM, MXFP4 14.3 and 17.1; of 24 tokens 58 MB,
+// MXFP8 15.4 and 19.5, MXFP4 10.4 and 13.2; rows of X that are not 128-byte aligned
+// cost 5% more).  Copies that leave the rows past the last out were 10% slower by their
+// branches.
 template <int FMT, int BM, int BN>
 struct SplitRing {
   static constexpr bool kTwoSteps = kFourBit<FMT>;

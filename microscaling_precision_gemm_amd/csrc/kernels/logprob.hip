@@ -18,10 +18,11 @@
 // the pass: 436 us for 4096 x 128000 BF16 and k = 5, now 190; 27.5 for one token's
 // 50257 and k = 20, now 9.9.)
 //
-// HBM bounds a batch (4096 x 128000 BF16 190 us, 5.5 TB/s; 11 vector instructions an
-// entry), one CU's vector unit and the steps after the pass a single row: of the 9.4
-// us for 50257 entries with 20 alternatives, 2.7 find these.  Sixteen waves for a
-// row instead of eight take longer (11.5 us).
+// HBM bounds a batch (4096 x 128000 BF16 190 us, 5.5 TB/s; 2048 x 128000 FP32 175 us,
+// 6.0 TB/s) with the vector unit right behind it (11 instructions a BF16 entry, and an
+// exponential counts four times), one CU's vector unit and the steps after the pass a
+// single row: of the 9.3 us for 50257 entries with 20 alternatives, 2.7 find these.
+// Sixteen waves for a row instead of eight take longer (11.5 us).
 #include "../device/chunk8.h"
 #include "../device/exp.h"
 #include "../device/wave.h"
@@ -104,7 +105,13 @@ __device__ inline void take_strip(TopList& list, const float (&v)[8], float larg
   }
 }
 
-// Running statistics: the largest entry, the sum of e^d and of e^d d / ln 2.
+// Running statistics: the largest entry, the sum of e^d and of e^d d / ln 2.  e^d is the
+// hardware's exponential of (x - m) c as rounded, which is off by 2 units of 2^-24, |d|
+// for the product and 1.2 |d| for c: of log S that leaves 2 units on average, as much
+// as exponentials of d itself do, since most roundings cancel in the sum.  The
+// exponential of exp.h, which the backward pass can afford, is 3 to 4 instructions
+// more an entry: 4096 x 128000 BF16 232 us instead of 185, for a mean error of log S of
+// 1.5e-7 instead of 1.9e-7; so the two passes' p differ by these units.
 struct Stats {
   float m = kLowest, s = 0.0f, w = 0.0f;
   // the same relative to a maximum `to` >= m; c = scale / ln 2
